@@ -396,6 +396,105 @@ int spec_verify_plan(int B, int K, int V, int topk_draft, int dtype,
 /* Static description of a status code (never NULL). */
 const char* spec_verify_status_string(int status);
 
+/* ------------------------------------------------------------------------
+ * Operators around a verification round
+ *
+ * One round of a serving program: attention of the round's tokens (the last
+ * committed token and its drafts: a chain or a tree) over the row's cache
+ * (spec_verify_attention), the model's remaining layers, penalties, biases
+ * and grammar masks on the logits that come of it
+ * (spec_verify_adjust_logits), spec_verify or spec_verify_tree, then the
+ * accepted path's keys and values into the cache (spec_verify_commit: the
+ * cache follows the committed prefix, "Speculative decoding: memverifikasi
+ * token draft sebelum diterima", subsection "KV cache harus mengikuti token
+ * yang di-commit"), and eviction of the blocks that drew the least attention
+ * (spec_verify_evict).
+ *
+ * The rules at the top of this file hold: device pointers owned by the
+ * caller, no allocation, no synchronisation, kernels only on `stream`, whose
+ * device must be the current one; device data is not validated, but every
+ * memory access stays in bounds for any values in the arrays.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * sv_controls - what spec_verify_adjust_logits applies.  NULL members are
+ * left out.  All pointers are device pointers.
+ */
+typedef struct {
+  /* Tokens that count for the penalties: row b's are history[b *
+   * history_stride + 0 .. history_lens[b]), of which the first
+   * prompt_lens[b] are the prompt (prompt_lens NULL: none).  Lengths are
+   * taken as at least 0 and at most history_stride.  A token outside [0, V)
+   * is ignored.  history may be NULL (no tokens but the drafted ones). */
+  const int32_t* history;
+  const int32_t* history_lens;
+  const int32_t* prompt_lens;
+  int64_t history_stride;
+  const float* repetition; /* [B] r > 0, or NULL (1) */
+  const float* presence;   /* [B], or NULL (0)       */
+  const float* frequency;  /* [B], or NULL (0)       */
+  /* Row b's biases are bias_ids / bias_values[b * bias_stride + 0 ..
+   * bias_lens[b]) (bias_lens NULL: bias_stride entries).  Where a token is
+   * listed more than once its last entry counts; ids outside [0, V) are
+   * ignored. */
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const int32_t* bias_lens;
+  int64_t bias_stride;
+  /* Grammar masks [num_masks, ceil(V / 32)]: bit x % 32 of word x / 32 is 1
+   * where token x is allowed.  Position i of row b goes by mask row
+   * mask_rows[b * P + i], none if that is outside [0, num_masks);
+   * mask_rows NULL: by mask row b * P + i. */
+  const uint32_t* mask;
+  const int32_t* mask_rows;
+  int num_masks;
+} sv_controls;
+
+/*
+ * spec_verify_adjust_logits - penalties for repeated tokens, biases and
+ * grammar masks on the logits of every position of a round, before they are
+ * verified.
+ *
+ * Position i of row b follows the row's history and the drafted tokens
+ * before it: of a chain (parents NULL) tokens[b][0 .. i-1], of a tree the
+ * tokens of the nodes on the path from the root to node i, node i included
+ * and the root (whose token ends the history) left out.  So one call serves
+ * target logits [B, K+1, V] or draft logits [B, K, V] with the draft_tokens
+ * of spec_verify, or either logits of spec_verify_tree with its node_tokens
+ * and parents.  With n(x) the occurrences of token x in the history past the
+ * prompt and on that path:
+ *   l1 = l / r where x occurs at all (prompt included) and l > 0, l r where
+ *        it occurs and l <= 0, l elsewhere
+ *   l2 = l1 - frequency n(x) - presence [n(x) > 0]
+ *   l3 = l2 + bias(x)
+ *   out = l3 where x is allowed, -inf elsewhere
+ * in float32, rounded once to dtype.  Logits that nothing applies to keep
+ * their bits.  A mask that allows no token leaves a position all -inf, for
+ * which spec_verify's result is unspecified.
+ *
+ * logits       element (b, i, x) at b * row_stride + i * stride + x, of the
+ *              stated dtype and aligned to it; strides in elements, stride >=
+ *              V.
+ * out          likewise, with out_row_stride and out_stride.  It may be the
+ *              logits themselves with the same strides (then only what
+ *              changes is written, and only what a penalty or bias changes
+ *              is read); otherwise it must not overlap them.
+ * tokens       [B, tokens_stride] int32, tokens_stride >= P - 1 (P for a
+ *              tree); NULL where no penalty is given or P == 1.
+ * parents      [B, P] int32 as in spec_verify_tree, or NULL: a chain.  The
+ *              path of a node whose parent is not an earlier node starts at
+ *              that node.
+ * B >= 1, P in [1, SV_MAX_K + 1] (SV_MAX_NODES with parents), V >= 1.
+ * One kernel, no workspace.  SV_ERR_ARG, SV_ERR_UNSUPPORTED (P too large, or
+ * a grid beyond 2^31 work-groups) or SV_ERR_HIP.
+ */
+int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
+                              int64_t stride, const int32_t* tokens,
+                              int64_t tokens_stride, const int32_t* parents,
+                              const sv_controls* controls, int B, int P, int V,
+                              int dtype, void* out, int64_t out_row_stride,
+                              int64_t out_stride, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

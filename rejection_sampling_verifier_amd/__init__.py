@@ -33,3 +33,6 @@ from .binding import (  # noqa: F401
     verify_tree,
     workspace_bytes,
 )
+from .round_ops import (  # noqa: F401
+    adjust_logits,
+)

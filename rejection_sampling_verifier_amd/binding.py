@@ -49,6 +49,15 @@ class SpecVerifyError(RuntimeError):
         self.status = status
 
 
+class SvControls(ctypes.Structure):
+    """sv_controls of spec_verify.h."""
+    _fields_ = [("history", ctypes.c_void_p), ("history_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p),
+                ("history_stride", ctypes.c_int64), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_lens", ctypes.c_void_p), ("bias_stride", ctypes.c_int64), ("mask", ctypes.c_void_p),
+                ("mask_rows", ctypes.c_void_p), ("num_masks", ctypes.c_int)]
+
+
 _lib = None
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
 _COMMON = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
@@ -86,6 +95,10 @@ def load_library(path: str | None = None):
     lib.spec_verify_tree.restype = _i32
     lib.spec_verify_tree_timed.argtypes = _tree + [ctypes.POINTER(_vp), _i32]
     lib.spec_verify_tree_timed.restype = _i32
+    _i64 = ctypes.c_int64
+    lib.spec_verify_adjust_logits.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, ctypes.POINTER(SvControls), _i32, _i32,
+                                              _i32, _i32, _vp, _i64, _i64, _vp]
+    lib.spec_verify_adjust_logits.restype = _i32
     lib.spec_verify_launches.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.spec_verify_launches.restype = _i32
     lib.spec_verify_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]

@@ -9,6 +9,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,9 @@ LIB = os.path.join(PKG, "libspecverify.so")
 # occupancy) of the last build, written next to the library.
 RESOURCES = os.path.join(PKG, "libspecverify.resources.txt")
 SOURCES = [os.path.join(PKG, "csrc", "spec_verify.hip")]
+# The operators around a verification round, one file each.
+ROUND_DIR = os.path.join(PKG, "csrc_round")
+ROUND_SOURCES = [os.path.join(ROUND_DIR, f) for f in sorted(os.listdir(ROUND_DIR)) if f.endswith(".hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -36,18 +41,28 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-o", tmp, *SOURCES]
+def _run(cmd: list, verbose: bool) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
-    os.replace(tmp, LIB)
+    return res.stderr
+
+
+def build(verbose: bool = False) -> str:
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as tmp:
+        sources = SOURCES + ROUND_SOURCES
+        objects = [os.path.join(tmp, f"{i}.o") for i in range(len(sources))]
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            reports = list(pool.map(lambda so: _run([HIPCC, *compile_flags, "-c", so[0], "-o", so[1]], verbose),
+                                    zip(sources, objects)))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp", *objects], verbose)
+    os.replace(LIB + ".tmp", LIB)
     with open(RESOURCES, "w") as f:
-        f.write(res.stderr)
+        f.write("".join(reports))
     return LIB
 
 
