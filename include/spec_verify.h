@@ -495,6 +495,92 @@ int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
                               int dtype, void* out, int64_t out_row_stride,
                               int64_t out_stride, hipStream_t stream);
 
+/* How a cache's values are held in 8 bits: OCP e4m3 (no infinities) or
+ * two's-complement int8; a value stands for code * its block's scale. */
+typedef enum { SV_E4M3 = 0, SV_INT8 = 1 } sv_kind;
+
+#define SV_MAX_BLOCKS 65536
+
+/*
+ * sv_cache - a paged cache of B rows.  A row's committed tokens are cut into
+ * blocks of `page` tokens.  Full blocks are held in 8 bits, one page each,
+ * with a scale for each block and kv head; the tokens after the last full
+ * block (the tail) are held in bf16, so nothing is ever quantised twice and a
+ * rejected draft leaves no trace.  All pointers are device pointers; the
+ * pages, tails and scales are written by spec_verify_commit only.
+ *
+ * k_pages      [num_pages, Hkv, page, D] codes
+ * v_pages      [num_pages, Hkv, D, page] codes: a channel's tokens side by
+ *              side, as the matrix instructions take them
+ * k_scale, v_scale [num_pages, Hkv] float32, positive (a NaN makes every
+ *              output that sees the block NaN)
+ * k_tail, v_tail [B, tail, Hkv, D] bf16 rings: the row's token number p lies in
+ *              slot p % tail.  tail is a multiple of page.
+ * block_table  [B, max_blocks] int32: the page of each block; entries past a
+ *              row's blocks are its reserve.  A block whose entry is outside
+ *              [0, num_pages) is not seen by attention.
+ * Two counters [B] int32 go with a cache, and are passed to each call:
+ * positions[b], the tokens committed to row b so far, and blocks[b], the full
+ * blocks it keeps.  positions[b] % page tokens lie in the tail; positions[b]
+ * / page - blocks[b] blocks have been evicted.
+ * Pages, tails 16-byte aligned.  page in {16, 32, 64, 128, 256}, D in {64,
+ * 128}, B <= 65536, Hkv <= 4096, max_blocks <= SV_MAX_BLOCKS, tail <= 2^20.
+ */
+typedef struct {
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  float* k_scale;
+  float* v_scale;
+  uint16_t* k_tail;
+  uint16_t* v_tail;
+  int32_t* block_table;
+  int B, num_pages, Hkv, D, page, max_blocks, tail, kind;
+} sv_cache;
+
+/*
+ * spec_verify_attention - attention of a round's T new tokens per row (the
+ * last committed token's successor positions: the root and its drafts) over
+ * the row's cache and over each other.
+ *
+ * Query (b, t, h) goes with kv head h / (H / Hkv).  It sees every full block
+ * of row b, the tail, and of the new tokens those before it and itself (a
+ * chain, parents NULL) or those on its path from the root, itself included (a
+ * tree; the path of a node whose parent is not an earlier node starts at that
+ * node).  With s = scale q.k over what it sees:
+ *   out = sum softmax(s) v
+ *   weights[b][t][j] = the softmax mass of block j, summed over the H heads
+ * Scores and softmax statistics are float32; q, the new tokens and the tail
+ * enter as bf16 and the codes exactly; a probability times its block's
+ * v_scale is rounded to bf16 before its product with v, and so is the output.
+ *
+ * q            element (b, t, h, d) at b * q_row + t * q_tok + h * D + d, bf16
+ * k_new, v_new element (b, t, h, d) at b * kv_row + t * kv_tok + h * D + d,
+ *              bf16.  All three may be views of one projection's output; 16-byte
+ *              aligned, strides multiples of 8.
+ * positions, blocks [B] int32, see sv_cache.
+ * parents      [B, T] int32 or NULL.
+ * query_lens   [B] int32 or NULL: row b has only that many (0 .. T) new
+ *              tokens.  What lies behind them in q, k_new and v_new is not
+ *              read, and in out and weights not written; a row of 0 is idle.
+ * T in [1, SV_MAX_K + 1] ([1, SV_MAX_NODES] with parents), H a multiple of
+ * Hkv, scale positive and finite.
+ * out          [B, T, H, D] bf16 contiguous.
+ * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
+ *              not have.
+ * workspace    at least *workspace_bytes bytes, 256-byte aligned; NULL asks for
+ *              the size.  It need not be cleared.  Calls that overlap in time
+ *              must use different workspaces.
+ * Two kernels, three with weights.
+ */
+int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
+                          const void* k_new, const void* v_new, int64_t kv_row,
+                          int64_t kv_tok, const sv_cache* cache,
+                          const int32_t* positions, const int32_t* blocks,
+                          const int32_t* parents, const int32_t* query_lens,
+                          int T, int H, float scale, void* out, float* weights,
+                          void* workspace, size_t* workspace_bytes,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,7 +8,10 @@ the library is missing.
 
 from .binding import (  # noqa: F401
     SV_BF16,
+    SV_E4M3,
     SV_F32,
+    SV_INT8,
+    SV_MAX_BLOCKS,
     SV_MAX_K,
     SV_MAX_NODES,
     SV_MAX_TOPK,
@@ -34,5 +37,9 @@ from .binding import (  # noqa: F401
     workspace_bytes,
 )
 from .round_ops import (  # noqa: F401
+    KVCache,
     adjust_logits,
+    attention_workspace_bytes,
+    cache_attention,
+    new_cache,
 )

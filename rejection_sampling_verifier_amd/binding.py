@@ -28,6 +28,7 @@ LIB_PATH = os.path.join(PKG, "libspecverify.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "spec_verify.h")
 
 SV_BF16, SV_F32 = 0, 1
+SV_E4M3, SV_INT8 = 0, 1
 SV_OK, SV_ERR_ARG, SV_ERR_WORKSPACE, SV_ERR_UNSUPPORTED, SV_ERR_HIP, SV_ERR_SCRATCH = 0, 1, 2, 3, 4, 5
 
 
@@ -40,6 +41,7 @@ def _header_define(name: str) -> int:
 SV_MAX_TOPK = _header_define("SV_MAX_TOPK")
 SV_MAX_K = _header_define("SV_MAX_K")
 SV_MAX_NODES = _header_define("SV_MAX_NODES")
+SV_MAX_BLOCKS = _header_define("SV_MAX_BLOCKS")
 SV_SCRATCH_BYTES = 32 << 20  # spec_verify.h: (32u << 20)
 
 
@@ -56,6 +58,13 @@ class SvControls(ctypes.Structure):
                 ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
                 ("bias_lens", ctypes.c_void_p), ("bias_stride", ctypes.c_int64), ("mask", ctypes.c_void_p),
                 ("mask_rows", ctypes.c_void_p), ("num_masks", ctypes.c_int)]
+
+
+class SvCache(ctypes.Structure):
+    """sv_cache of spec_verify.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "k_tail", "v_tail",
+                                               "block_table")] + \
+               [(n, ctypes.c_int) for n in ("B", "num_pages", "Hkv", "D", "page", "max_blocks", "tail", "kind")]
 
 
 _lib = None
@@ -99,6 +108,9 @@ def load_library(path: str | None = None):
     lib.spec_verify_adjust_logits.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, ctypes.POINTER(SvControls), _i32, _i32,
                                               _i32, _i32, _vp, _i64, _i64, _vp]
     lib.spec_verify_adjust_logits.restype = _i32
+    lib.spec_verify_attention.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, ctypes.POINTER(SvCache), _vp, _vp,
+                                          _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]
+    lib.spec_verify_attention.restype = _i32
     lib.spec_verify_launches.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.spec_verify_launches.restype = _i32
     lib.spec_verify_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]

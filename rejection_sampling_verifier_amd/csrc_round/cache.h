@@ -1,0 +1,51 @@
+// What the kernels over the paged 8-bit cache share.
+#pragma once
+
+#include <cstdint>
+
+#include "spec_verify.h"
+#include "sv_device.h"
+
+namespace svr {
+
+using sv::u32x4;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// The counters of one row, brought into range: full blocks kept and tokens
+// in the tail (its first token's ring slot is `start`).
+struct RowState {
+  int blocks, tail, start;
+};
+__device__ __forceinline__ RowState row_state(const sv_cache& c, const int32_t* positions, const int32_t* blocks, int b) {
+  RowState s;
+  s.blocks = min(max(blocks[b], 0), c.max_blocks);
+  const int pos = max(positions[b], 0);
+  s.tail = pos % c.page;
+  s.start = (pos - s.tail) % c.tail;
+  return s;
+}
+
+// Checks of the cache's description that every entry point makes.
+inline int check_cache(const sv_cache* c) {
+  if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail || !c->block_table)
+    return SV_ERR_ARG;
+  if (c->B < 1 || c->num_pages < 1 || c->Hkv < 1 || c->max_blocks < 1 || c->page < 1 || c->tail < 1 ||
+      (c->kind != SV_E4M3 && c->kind != SV_INT8))
+    return SV_ERR_ARG;
+  if ((c->D != 64 && c->D != 128) || c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) || c->Hkv > 4096 ||
+      c->max_blocks > SV_MAX_BLOCKS || c->B > 65536)
+    return SV_ERR_UNSUPPORTED;
+  if (c->tail % c->page || c->tail > (1 << 20)) return SV_ERR_ARG;
+  const void* aligned[] = {c->k_pages, c->v_pages, c->k_tail, c->v_tail};
+  for (const void* p : aligned)
+    if (reinterpret_cast<uintptr_t>(p) % 16) return SV_ERR_ARG;
+  const void* words[] = {c->k_scale, c->v_scale, c->block_table};
+  for (const void* p : words)
+    if (reinterpret_cast<uintptr_t>(p) % 4) return SV_ERR_ARG;
+  return SV_OK;
+}
+
+}  // namespace svr

@@ -12,7 +12,10 @@ import ctypes
 
 import torch
 
-from .binding import (SvControls, _check, _dtype_code, _OnStream, _stream_handle, load_library)
+from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, _check, _dtype_code, _OnStream, _stream_handle,
+                      load_library)
+
+_KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
 
 
 class _OnDevice:
@@ -140,3 +143,140 @@ def adjust_logits(logits, tokens=None, *, parents=None, history=None, history_le
             logits.data_ptr(), in_row, in_pos, _p(tokens), tok_stride, _p(parents), ctypes.byref(c), B, P, V, dt,
             out.data_ptr(), out_row, out_pos, handle))
     return out
+
+
+class KVCache:
+    """The tensors of a paged 8-bit cache (sv_cache in the header), checked once.
+
+    k_pages [num_pages, Hkv, page, D] and v_pages [num_pages, Hkv, D, page]
+    uint8 codes, k_scale and v_scale [num_pages, Hkv] fp32, k_tail and v_tail
+    [B, tail, Hkv, D] bf16, block_table [B, max_blocks] int32; kind "e4m3" or
+    "int8".  A row's counters (positions, blocks) are passed to each call.
+    The handle keeps the tensors; their storage must not be replaced.
+    """
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale, k_tail, v_tail, block_table, *, kind="e4m3"):
+        if kind not in _KINDS:
+            raise ValueError(f"kind must be one of {sorted(_KINDS)}, got {kind!r}")
+        dev = _gpu(k_pages, "k_pages")
+        if k_pages.dim() != 4 or not isinstance(k_tail, torch.Tensor) or k_tail.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, Hkv, page, D] and k_tail [B, tail, Hkv, D]")
+        pages, Hkv, page, D = k_pages.shape
+        B, tail = k_tail.shape[:2]
+        _need("k_pages", k_pages, (pages, Hkv, page, D), torch.uint8, dev)
+        _need("v_pages", v_pages, (pages, Hkv, D, page), torch.uint8, dev)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(name, t, (pages, Hkv), torch.float32, dev)
+        for name, t in (("k_tail", k_tail), ("v_tail", v_tail)):
+            _need(name, t, (B, tail, Hkv, D), torch.bfloat16, dev)
+        _need("block_table", block_table, (B, None), torch.int32, dev)
+        if 0 in (pages, Hkv, page, D, B, tail, block_table.shape[1]):
+            raise ValueError("a cache's sizes must be at least 1")
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.k_tail, self.v_tail, self.block_table, self.kind, self.device = k_tail, v_tail, block_table, kind, dev
+        self.B, self.num_pages, self.Hkv, self.D, self.page = B, pages, Hkv, D, page
+        self.max_blocks, self.tail = block_table.shape[1], tail
+        self._c = SvCache(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                          k_tail.data_ptr(), v_tail.data_ptr(), block_table.data_ptr(), B, pages, Hkv, D, page,
+                          self.max_blocks, tail, _KINDS[kind])
+        self._ref = ctypes.byref(self._c)
+        self._sizes = {}  # workspace sizes by (T, H, parents, weights)
+
+
+def new_cache(B, num_pages, Hkv, D, page=64, max_blocks=None, max_new=SV_MAX_K + 1, kind="e4m3", device="cuda"):
+    """An empty cache: no pages are assigned (block_table is -1), and the tails
+    hold what a commit of up to max_new tokens needs."""
+    dev = torch.device(device)
+    tail = -(-(page - 1 + max_new) // page) * page
+    z = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device=dev)  # noqa: E731
+    table = torch.full((B, max_blocks if max_blocks is not None else max(1, num_pages // B)), -1, dtype=torch.int32,
+                       device=dev)
+    return KVCache(z((num_pages, Hkv, page, D), torch.uint8), z((num_pages, Hkv, D, page), torch.uint8),
+                   torch.ones((num_pages, Hkv), device=dev), torch.ones((num_pages, Hkv), device=dev),
+                   z((B, tail, Hkv, D), torch.bfloat16), z((B, tail, Hkv, D), torch.bfloat16), table, kind=kind)
+
+
+def _token_strides(name, t, shape, dev):
+    """(row, token) strides of a bf16 [B, T, heads, D] view whose heads lie side by side."""
+    B, T, n, D = shape
+    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != dev
+            or t.stride(3) != 1 or (n > 1 and t.stride(2) != D)):
+        raise ValueError(f"{name} must be a bfloat16 tensor of shape {shape} on {dev}, its heads side by side")
+    tok = t.stride(1) if T > 1 else n * D
+    row = t.stride(0) if B > 1 else T * tok
+    if tok % 8 or row % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned in every token")
+    return row, tok
+
+
+def _attention_bytes(cache, T, H, tree, weights):
+    key = (T, H, tree, weights)
+    n = cache._sizes.get(key)
+    if n is None:
+        size = ctypes.c_size_t(0)
+        some = ctypes.c_void_p(256)  # tells the query which arguments the call will have
+        _check(load_library().spec_verify_attention(None, 0, 0, None, None, 0, 0, cache._ref, None, None,
+                                                    some if tree else None, None, T, H, 1.0, None,
+                                                    some if weights else None, None, ctypes.byref(size), None))
+        n = cache._sizes[key] = size.value
+    return n
+
+
+def attention_workspace_bytes(cache, T, H, *, tree=False, weights=False):
+    """Bytes of workspace that cache_attention needs for T new tokens and H heads."""
+    return _attention_bytes(cache, T, H, tree, weights)
+
+
+def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, query_lens=None, scale=None,
+                    weights=None, out=None, workspace=None, stream=None):
+    """spec_verify_attention: attention of a round's new tokens over the cache
+    and over each other (see the header).
+
+    q [B, T, H, D], k_new and v_new [B, T, Hkv, D] bf16, views with D-sized
+    heads side by side (slices of a fused projection will do); positions and
+    blocks [B] int32; parents [B, T] int32 for trees; query_lens [B] int32;
+    scale None: D ** -0.5.  weights: True or a [B, T, max_blocks] fp32 tensor to
+    get every block's attention mass.
+
+    Returns out [B, T, H, D], or (out, weights).  Tensors made here hold zeros
+    behind query_lens.
+    """
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    dev, B, D = cache.device, cache.B, cache.D
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or 0 in q.shape:
+        raise ValueError("q must be [B, T, H, D]")
+    T, H = q.shape[1], q.shape[2]
+    q_row, q_tok = _token_strides("q", q, (B, T, H, D), dev)
+    kv = _token_strides("k_new", k_new, (B, T, cache.Hkv, D), dev)
+    if _token_strides("v_new", v_new, (B, T, cache.Hkv, D), dev) != kv:
+        raise ValueError("k_new and v_new must have the same strides")
+    _need("positions", positions, (B,), torch.int32, dev)
+    _need("blocks", blocks, (B,), torch.int32, dev)
+    _maybe("parents", parents, (B, T), torch.int32, dev)
+    _maybe("query_lens", query_lens, (B,), torch.int32, dev)
+    handle = _stream_handle(dev, stream)
+    need = _attention_bytes(cache, T, H, parents is not None, weights is not None and weights is not False)
+    with _OnDevice(dev), _OnStream(dev, handle):
+        make = torch.empty if query_lens is None else torch.zeros
+        if weights is True:
+            weights = make((B, T, cache.max_blocks), dtype=torch.float32, device=dev)
+        elif weights is False:
+            weights = None
+        elif weights is not None:
+            _need("weights", weights, (B, T, cache.max_blocks), torch.float32, dev)
+        if out is None:
+            out = make((B, T, H, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _need("out", out, (B, T, H, D), torch.bfloat16, dev)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+        _check(load_library().spec_verify_attention(
+            q.data_ptr(), q_row, q_tok, k_new.data_ptr(), v_new.data_ptr(), kv[0], kv[1], cache._ref,
+            positions.data_ptr(), blocks.data_ptr(), _p(parents), _p(query_lens), T, H,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), _p(weights), workspace.data_ptr(), ctypes.byref(n),
+            handle))
+    return out if weights is None else (out, weights)

@@ -56,3 +56,68 @@ def test_adjust_logits_takes_gpu_tensors_only():
         rsv.adjust_logits(torch.zeros(1, 1, 8))
     with pytest.raises(ValueError):
         rsv.adjust_logits(None)
+
+
+def cache(**kw):
+    c = B.SvCache(P[0], P[1], P[2], P[3], P[4], P[5], P[6], 2, 100, 2, 64, 16, 10, 32, B.SV_E4M3)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def attention(ws=P[20], ws_n=None, **kw):
+    a = dict(q=P[10], q_row=3 * 512, q_tok=512, kn=P[11], vn=P[12], kv_row=3 * 512, kv_tok=512, c=cache(),
+             positions=P[13], blocks=P[14], parents=None, lens=None, T=3, H=4, scale=0.125, out=P[15], weights=None)
+    a.update(kw)
+    n = ctypes.c_size_t(1 << 40 if ws_n is None else ws_n)
+    rc = B.load_library().spec_verify_attention(
+        a["q"], a["q_row"], a["q_tok"], a["kn"], a["vn"], a["kv_row"], a["kv_tok"],
+        None if a["c"] is None else ctypes.byref(a["c"]), a["positions"], a["blocks"], a["parents"], a["lens"], a["T"],
+        a["H"], a["scale"], a["out"], a["weights"], ws, ctypes.byref(n), None)
+    return rc if ws is not None else (rc, n.value)
+
+
+BAD_CACHES = [dict(k_pages=None), dict(v_pages=None), dict(k_scale=None), dict(v_scale=None), dict(k_tail=None),
+              dict(v_tail=None), dict(block_table=None), dict(B=0), dict(num_pages=0), dict(Hkv=0), dict(max_blocks=0),
+              dict(page=0), dict(tail=0), dict(kind=2), dict(tail=24), dict(k_pages=P[0] + 8), dict(v_tail=P[5] + 2),
+              dict(k_scale=P[2] + 2), dict(block_table=P[6] + 1)]
+UNSUPPORTED_CACHES = [dict(D=32), dict(D=96), dict(D=256), dict(page=8, tail=32), dict(page=48, tail=48),
+                      dict(page=512, tail=512), dict(Hkv=5000), dict(max_blocks=B.SV_MAX_BLOCKS + 1),
+                      dict(B=70000)]
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES)
+def test_attention_refuses_bad_caches(bad):
+    assert attention(c=cache(**bad)) == B.SV_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", UNSUPPORTED_CACHES)
+def test_attention_refuses_unsupported_caches(bad):
+    assert attention(c=cache(**bad)) == B.SV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("bad", [
+    dict(c=None), dict(q=None), dict(kn=None), dict(vn=None), dict(positions=None), dict(blocks=None), dict(out=None),
+    dict(T=0), dict(H=0), dict(H=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
+    dict(scale=float("nan")), dict(q=P[10] + 8), dict(kn=P[11] + 2), dict(out=P[15] + 8), dict(q_tok=516),
+    dict(kv_row=-8), dict(q_row=1 << 50), dict(weights=P[16] + 2), dict(ws=P[20] + 16)])
+def test_attention_refuses(bad):
+    assert attention(**bad) == B.SV_ERR_ARG
+
+
+def test_attention_limits_and_workspace():
+    assert attention(T=B.SV_MAX_K + 2) == B.SV_ERR_UNSUPPORTED
+    assert attention(T=B.SV_MAX_NODES + 1, parents=P[16]) == B.SV_ERR_UNSUPPORTED
+    rc, n = attention(ws=None)
+    assert rc == B.SV_OK and n > 0 and n % 256 == 0
+    rc, more = attention(ws=None, weights=P[16])
+    assert rc == B.SV_OK and more > n
+    assert attention(ws_n=n - 1) == B.SV_ERR_WORKSPACE
+    assert attention(weights=P[16], ws_n=n) == B.SV_ERR_WORKSPACE
+
+
+def test_cache_attention_takes_gpu_tensors_only():
+    with pytest.raises(ValueError):
+        rsv.KVCache(*(torch.zeros(1, 1, 16, 64, dtype=torch.uint8),) * 7)
+    with pytest.raises(ValueError):
+        rsv.new_cache(1, 1, 1, 64, device="cpu")
