@@ -581,6 +581,80 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
                           void* workspace, size_t* workspace_bytes,
                           hipStream_t stream);
 
+/*
+ * spec_verify_commit - the accepted path's keys and values enter the cache.
+ *
+ * Row b commits its root and its accepted drafts: n = num_accepted[b] + 1 of
+ * its new tokens, the first n of a chain (nodes NULL), or token 0 and then
+ * nodes[b][0 .. n-2], spec_verify_tree's out_nodes.  They follow the tail;
+ * each block that this completes is quantised into the page that the row's
+ * block table has in reserve, block_table[b][blocks[b]] first, and the
+ * tokens after the last full block go to their slots of the tail ring.  The
+ * tail's old tokens stay where they are and the counters are put out, so a
+ * round can be undone by keeping the counters from before it.
+ *
+ * A block's scale is, with a the largest magnitude of its head's page * D
+ * values: e4m3, the smallest power of two of at least a / 448; int8, a / 127
+ * rounded to float32; in both at least 2^-126, and 1 where a is 0.  Its codes
+ * are the values over the scale, rounded to nearest even exactly.  A block
+ * that holds an infinity or NaN gets a NaN scale (and codes 0).
+ *
+ * A row is left as it was, its counters repeated, where num_accepted is
+ * outside [0, T - 1] (spec_verify's -1 among it), a node outside [0, T), a
+ * counter out of range, or a completed block has no page (its table entry is
+ * past max_blocks or outside [0, num_pages)): an active row always advances.
+ *
+ * k_new, v_new, kv_row, kv_tok, T as spec_verify_attention.
+ * num_accepted [B] int32; nodes [B, nodes_stride] int32 or NULL, nodes_stride
+ *              >= T - 1.
+ * cache        with tail >= page - 1 + T.  No page may be in reserve for two
+ *              rows.
+ * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
+ *              a second kernel updates them).
+ * weights      [B, T, max_blocks] float32 (spec_verify_attention's) or NULL.
+ * totals, totals_out [B, max_blocks] float32, both or none: totals_out[b][j]
+ *              is totals[b][j] plus the weights of block j from the committed
+ *              tokens for the blocks that row b had, 0 for the rest.  They may
+ *              be the same array.
+ */
+int spec_verify_commit(const void* k_new, const void* v_new, int64_t kv_row,
+                       int64_t kv_tok, int T, const int32_t* num_accepted,
+                       const int32_t* nodes, int64_t nodes_stride,
+                       const sv_cache* cache, const int32_t* positions,
+                       const int32_t* blocks, int32_t* positions_out,
+                       int32_t* blocks_out, const float* weights,
+                       const float* totals, float* totals_out,
+                       hipStream_t stream);
+
+/*
+ * spec_verify_evict - blocks that drew little attention leave the cache.
+ *
+ * Where row b has more than `budget` blocks, the blocks[b] - budget of least
+ * totals leave, of those that are neither among its first keep_first nor its
+ * last keep_last (all of these if they are fewer); of equal totals the
+ * earlier block leaves first, and a NaN counts as above every number.  The
+ * row's table becomes the pages of the blocks kept, then those evicted, then
+ * its old reserve, each in their order: the evicted pages are the next ones
+ * that spec_verify_commit fills.  totals follow the blocks kept; the rest are
+ * 0.  No page is read or moved.  (A key's position is in its values, so a
+ * block's place in the table does not matter to attention.)
+ *
+ * totals       [B, max_blocks] float32
+ * block_table  [B, max_blocks] int32
+ * blocks       [B] int32
+ * totals_out, table_out, blocks_out  as these; each may be its input itself
+ *              (table_out only up to max_blocks = 16384, else
+ *              SV_ERR_UNSUPPORTED), but not overlap it otherwise.
+ * evicted      [B] int32: how many blocks left.
+ * budget, keep_first, keep_last >= 0; 1 <= max_blocks <= SV_MAX_BLOCKS.
+ * One kernel, no workspace.
+ */
+int spec_verify_evict(const float* totals, const int32_t* block_table,
+                      const int32_t* blocks, int B, int max_blocks, int budget,
+                      int keep_first, int keep_last, float* totals_out,
+                      int32_t* table_out, int32_t* blocks_out,
+                      int32_t* evicted, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -41,5 +41,7 @@ from .round_ops import (  # noqa: F401
     adjust_logits,
     attention_workspace_bytes,
     cache_attention,
+    cache_commit,
+    cache_evict,
     new_cache,
 )

@@ -111,6 +111,11 @@ def load_library(path: str | None = None):
     lib.spec_verify_attention.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, ctypes.POINTER(SvCache), _vp, _vp,
                                           _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]
     lib.spec_verify_attention.restype = _i32
+    lib.spec_verify_commit.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, ctypes.POINTER(SvCache), _vp, _vp, _vp,
+                                       _vp, _vp, _vp, _vp, _vp]
+    lib.spec_verify_commit.restype = _i32
+    lib.spec_verify_evict.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+    lib.spec_verify_evict.restype = _i32
     lib.spec_verify_launches.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.spec_verify_launches.restype = _i32
     lib.spec_verify_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]

@@ -28,6 +28,12 @@ __device__ __forceinline__ RowState row_state(const sv_cache& c, const int32_t* 
   return s;
 }
 
+// Whether two arrays of n bytes share any.
+inline bool overlap(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + n && y < x + n;
+}
+
 // Checks of the cache's description that every entry point makes.
 inline int check_cache(const sv_cache* c) {
   if (!c || !c->k_pages || !c->v_pages || !c->k_scale || !c->v_scale || !c->k_tail || !c->v_tail || !c->block_table)

@@ -280,3 +280,89 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
             D ** -0.5 if scale is None else scale, out.data_ptr(), _p(weights), workspace.data_ptr(), ctypes.byref(n),
             handle))
     return out if weights is None else (out, weights)
+
+
+def cache_commit(cache, k_new, v_new, num_accepted, positions, blocks, *, nodes=None, weights=None, totals=None,
+                 positions_out=None, blocks_out=None, totals_out=None, stream=None):
+    """spec_verify_commit: the accepted path's keys and values enter the cache
+    (see the header).
+
+    k_new, v_new as cache_attention's; num_accepted [B] int32 and, for trees,
+    nodes [B, >= T - 1] int32 as verify and verify_tree return them; weights
+    [B, T, max_blocks] fp32 as cache_attention returns them, totals [B,
+    max_blocks] fp32.
+
+    Writes the cache's pages, scales and tails, and returns (positions,
+    blocks), or (positions, blocks, totals) where totals is given: new tensors,
+    or the given outs, which may be the inputs themselves.
+    """
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    dev, B, i32 = cache.device, cache.B, torch.int32
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or 0 in k_new.shape:
+        raise ValueError("k_new must be [B, T, Hkv, D]")
+    T = k_new.shape[1]
+    kv = _token_strides("k_new", k_new, (B, T, cache.Hkv, cache.D), dev)
+    if _token_strides("v_new", v_new, (B, T, cache.Hkv, cache.D), dev) != kv:
+        raise ValueError("k_new and v_new must have the same strides")
+    for name, t in (("num_accepted", num_accepted), ("positions", positions), ("blocks", blocks)):
+        _need(name, t, (B,), i32, dev)
+    stride = 0
+    if nodes is not None:
+        stride = _rows("nodes", nodes, B, i32, dev)
+        if nodes.shape[1] < T - 1:
+            raise ValueError(f"nodes must hold at least {T - 1} nodes per row")
+    _maybe("weights", weights, (B, T, cache.max_blocks), torch.float32, dev)
+    _maybe("totals", totals, (B, cache.max_blocks), torch.float32, dev)
+    if totals is None and (weights is not None or totals_out is not None):
+        raise ValueError("weights and totals_out need totals")
+    handle = _stream_handle(dev, stream)
+    with _OnDevice(dev), _OnStream(dev, handle):
+        outs = []
+        for name, t, like in (("positions_out", positions_out, positions), ("blocks_out", blocks_out, blocks),
+                              ("totals_out", totals_out, totals)):
+            if t is None and like is not None:
+                t = torch.empty_like(like)
+            elif t is not None:
+                _need(name, t, tuple(like.shape), like.dtype, dev)
+            outs.append(t)
+        # an empty node list (T == 1) has no address, and is not read
+        _check(load_library().spec_verify_commit(
+            k_new.data_ptr(), v_new.data_ptr(), kv[0], kv[1], T, num_accepted.data_ptr(), _p(nodes) or None, stride,
+            cache._ref, positions.data_ptr(), blocks.data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), _p(weights),
+            _p(totals), _p(outs[2]), handle))
+    return tuple(outs) if totals is not None else tuple(outs[:2])
+
+
+def cache_evict(block_table, totals, blocks, budget, *, keep_first=0, keep_last=0, table_out=None, totals_out=None,
+                blocks_out=None, evicted=None, stream=None):
+    """spec_verify_evict: where a row has more than ``budget`` blocks, those of
+    least totals leave it (see the header).
+
+    block_table [B, max_blocks] int32 (a KVCache's, which table_out may be
+    too), totals [B, max_blocks] fp32, blocks [B] int32.
+
+    Returns (table, totals, blocks, evicted): new tensors, or the given outs;
+    table_out, totals_out and blocks_out may be the inputs themselves.
+    """
+    dev = _gpu(block_table, "block_table")
+    if block_table.dim() != 2 or 0 in block_table.shape:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, most = block_table.shape
+    _need("block_table", block_table, (B, most), torch.int32, dev)
+    _need("totals", totals, (B, most), torch.float32, dev)
+    _need("blocks", blocks, (B,), torch.int32, dev)
+    handle = _stream_handle(dev, stream)
+    with _OnDevice(dev), _OnStream(dev, handle):
+        outs = []
+        for name, t, like in (("table_out", table_out, block_table), ("totals_out", totals_out, totals),
+                              ("blocks_out", blocks_out, blocks), ("evicted", evicted, blocks)):
+            if t is None:
+                t = torch.empty_like(like)
+            else:
+                _need(name, t, tuple(like.shape), like.dtype, dev)
+            outs.append(t)
+        _check(load_library().spec_verify_evict(
+            totals.data_ptr(), block_table.data_ptr(), blocks.data_ptr(), B, most, budget, keep_first, keep_last,
+            outs[1].data_ptr(), outs[0].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), handle))
+    return tuple(outs)

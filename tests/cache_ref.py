@@ -142,3 +142,94 @@ def attention(s, q, k_new, v_new, scale, parents=None, query_lens=None):
 
 def as_numpy(t):
     return t.detach().cpu().double().numpy() if t.is_floating_point() else np.asarray(t.detach().cpu())
+
+
+def scale_of(top, kind):
+    """A block's scale for its largest magnitude (a float), as float64's value."""
+    if not np.isfinite(top):
+        return float("nan")
+    if top == 0:
+        return 1.0
+    if kind == "int8":
+        return max(float(np.float32(np.float64(top) / 127)), 2.0 ** -126)
+    e = -126
+    while top > 448 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def quantise(x, kind):
+    """x: float64 [page, D] -> (values the codes stand for / scale, scale); ties to even, by exact rationals."""
+    top = float(x.abs().max()) if torch.isfinite(x).all() else float("inf")
+    scale = scale_of(top, kind)
+    if not np.isfinite(top):
+        return torch.zeros_like(x), scale
+    if kind == "int8":
+        # bf16 / float32 in float64 is off by 2^-53: no tie is missed or made up, as 2 x / scale is an odd
+        # integer only where the division is exact, and near ones differ from it by 2^-32 at least
+        return torch.round(x / scale), scale
+    y = x / scale
+    step = torch.exp2((torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -30))) - 3).clamp(min=-9))
+    return torch.round(y / step) * step, scale
+
+
+def commit(s, k_new, v_new, num_accepted, nodes=None, weights=None, totals=None):
+    """The state after a commit (a new dict), with totals.  Pages as values / scale (float64) in k_values, v_values:
+    those written; NaN for the others."""
+    page, D, Hkv, B = s["page"], s["D"], s["Hkv"], s["B"]
+    T, most, pages, R = k_new.shape[1], s["table"].shape[1], s["k_pages"].shape[0], s["k_tail"].shape[1]
+    new = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in s.items()}
+    vals = {x: torch.full((pages, Hkv, page, D), float("nan"), dtype=torch.float64) for x in "kv"}
+    tot = None if totals is None else torch.zeros_like(totals, dtype=torch.float64)
+    for b in range(B):
+        pos, blocks, n = int(s["positions"][b]), int(s["blocks"][b]), int(num_accepted[b]) + 1
+        ok = 1 <= n <= T and 0 <= pos <= 2 ** 31 - 1 - n and 0 <= blocks <= most
+        path = []
+        if ok:
+            path = [0] + [int(nodes[b, i]) if nodes is not None else i + 1 for i in range(n - 1)]
+            ok = all(0 <= c < T for c in path)
+            tail = pos % page
+            filled = (tail + n) // page
+            for m in range(filled):
+                j = blocks + m
+                ok = ok and j < most and 0 <= int(s["table"][b, j]) < pages
+        if not ok:
+            path, filled, n = [], 0, 0
+        if tot is not None:
+            keep = min(max(blocks, 0), most) if ok or 0 <= blocks <= most else (0 if blocks < 0 else most)
+            tot[b, :keep] = totals[b, :keep].double()
+            if weights is not None and path:
+                tot[b, :keep] += weights[b, path, :keep].double().sum(0)
+        if not ok:
+            continue
+        start = pos - tail
+        for x, fresh in (("k", k_new), ("v", v_new)):
+            seq = torch.cat([s[x + "_tail"][b, [(start + j) % R for j in range(tail)]].reshape(tail, Hkv, D),
+                             fresh[b, path]])
+            for m in range(filled):
+                pid = int(s["table"][b, blocks + m])
+                for h in range(Hkv):
+                    y, scale = quantise(seq[m * page:(m + 1) * page, h].double(), s["kind"])
+                    vals[x][pid, h] = y
+                    new[x + "_scale"][pid, h] = scale
+            for j in range(max(tail, filled * page), tail + n):
+                new[x + "_tail"][b, (start + j) % R] = seq[j]
+        new["positions"][b], new["blocks"][b] = pos + n, blocks + filled
+    return new, vals, tot
+
+
+def evict(table, totals, blocks, budget, first=0, last=0):
+    table, totals, blocks = (t.clone().numpy() for t in (table, totals, blocks))
+    gone = np.zeros_like(blocks)
+    for b in range(table.shape[0]):
+        n = min(max(int(blocks[b]), 0), table.shape[1])
+        may = [j for j in range(n) if first <= j < n - last]
+        e = min(max(0, n - budget), len(may))
+        order = sorted(may, key=lambda j: ((1, 0.0) if np.isnan(totals[b, j]) else (0, float(totals[b, j])), j))
+        away = set(order[:e])
+        keep = [j for j in range(n) if j not in away]
+        table[b, :n] = table[b, keep + sorted(away)]
+        totals[b, :n - e] = totals[b, keep]
+        totals[b, n - e:] = 0
+        blocks[b], gone[b] = n - e, e
+    return table, totals, blocks, gone

@@ -1,0 +1,245 @@
+"""cache_commit against its definition, on the GPU.  Codes, scales and copies
+are compared exactly.  Totals are float32: a sum of at most 65 weights and the
+old total, each addition off by at most 2^-24 of its result, all terms
+positive, so |totals - ref| <= 66 * 2^-24 ref."""
+
+from __future__ import annotations
+
+import pytest
+import torch
+
+import rejection_sampling_verifier_amd as rsv
+from tests import cache_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+KINDS = ["e4m3", "int8"]
+
+
+def state_with_reserve(seed, reserve, **kw):
+    """A random state whose rows have `reserve` pages each past their blocks."""
+    B = kw["B"]
+    page = kw["page"]
+    most = max(c // page for c in kw["contexts"]) + reserve
+    s = R.random_state(seed, max_blocks=most, spare=B * reserve + 1, **kw)
+    used = set(int(p) for p in s["table"].flatten() if p >= 0)
+    free = [p for p in range(s["k_pages"].shape[0]) if p not in used]
+    for b in range(B):
+        for m in range(reserve):
+            s["table"][b, int(s["blocks"][b]) + m] = free.pop()
+    return s
+
+
+def random_new(seed, B, T, Hkv, D, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    kv = torch.randn((B, T, 2, Hkv, D), generator=g) * torch.exp(spread * torch.randn((Hkv, D), generator=g))
+    return kv.to(BF16)
+
+
+def random_nodes(seed, B, T, num):
+    g = torch.Generator().manual_seed(seed)
+    nodes = torch.full((B, T), -1, dtype=torch.int32)
+    for b in range(B):
+        n = min(max(int(num[b]), 0), T - 1)
+        nodes[b, :n] = (1 + torch.randperm(T - 1, generator=g)[:n]).sort().values.to(torch.int32)
+    return nodes
+
+
+def check(s, kv, num, cache, outs, nodes=None, weights=None, totals=None):
+    want, vals, tot = R.commit(s, kv[:, :, 0], kv[:, :, 1], num, nodes, weights, totals)
+    assert torch.equal(outs[0].cpu(), want["positions"])
+    assert torch.equal(outs[1].cpu(), want["blocks"])
+    for x in "kv":
+        codes = getattr(cache, x + "_pages").cpu()
+        written = ~torch.isnan(vals[x][:, 0, 0, 0])
+        value = vals[x] if x == "k" else vals[x].transpose(2, 3)
+        assert torch.equal(R.decode(codes[written], s["kind"]), value[written]), x
+        assert torch.equal(codes[~written], s[x + "_pages"][~written]), x
+        assert torch.equal(getattr(cache, x + "_scale").cpu().nan_to_num(-1), want[x + "_scale"].nan_to_num(-1)), x
+        tail = getattr(cache, x + "_tail").cpu()
+        assert torch.equal(tail.view(torch.int16), want[x + "_tail"].view(torch.int16)), x
+    if totals is not None:
+        err = (outs[2].cpu().double() - tot).abs()
+        assert (err <= 66 * 2.0 ** -24 * tot).all()
+    return want
+
+
+def case(seed, contexts, num, T, Hkv, D, page, kind, tree=False, reserve=8, totals=True, spread=1.0, edit=None, **kw):
+    B = len(contexts)
+    s = state_with_reserve(seed, reserve, B=B, Hkv=Hkv, D=D, page=page, kind=kind, contexts=contexts, **kw)
+    kv = random_new(seed + 1, B, T, Hkv, D, spread)
+    if edit:
+        edit(s, kv)
+    num = torch.tensor(num, dtype=torch.int32)
+    nodes = random_nodes(seed + 2, B, T, num) if tree else None
+    g = torch.Generator().manual_seed(seed + 3)
+    most = s["table"].shape[1]
+    w, t = (torch.rand((B, T, most), generator=g), torch.rand((B, most), generator=g) * 9) if totals else (None, None)
+    dev = lambda x: None if x is None else x.cuda()  # noqa: E731
+    cache, positions, blocks = R.to_gpu(s)
+    kvd = kv.cuda()
+    args = dict(nodes=dev(nodes), weights=dev(w), totals=dev(t))
+    outs = rsv.cache_commit(cache, kvd[:, :, 0], kvd[:, :, 1], dev(num), positions, blocks, **args)
+    check(s, kv, num, cache, outs, nodes, w, t)
+    # the counters before are untouched, and the same round again gives the same state (a round can be redone)
+    assert torch.equal(positions.cpu(), s["positions"]) and torch.equal(blocks.cpu(), s["blocks"])
+    rsv.cache_commit(cache, kvd[:, :, 0], kvd[:, :, 1], dev(num), positions, blocks, **args)
+    check(s, kv, num, cache, outs, nodes, w, t)
+    # in place
+    cache2, pos2, blk2 = R.to_gpu(s)
+    t2 = dev(t)
+    res = rsv.cache_commit(cache2, kvd[:, :, 0], kvd[:, :, 1], dev(num), pos2, blk2, nodes=dev(nodes), weights=dev(w),
+                           totals=t2, positions_out=pos2, blocks_out=blk2, totals_out=t2)
+    check(s, kv, num, cache2, res, nodes, w, t)
+    assert res[0] is pos2 and res[1] is blk2
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_and_lengths(D, page, kind):
+    contexts = [0, 1, page - 1, page - 1, page, 2 * page + page // 2, page - 3, 3 * page - 1]
+    case(1, contexts, [0, 2, 0, 4, 4, 1, 1, 3], 5, 2, D, page, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 17, 64])
+def test_up_to_the_longest_rounds(T, tree, kind):
+    """A round may complete several blocks; every row accepts another number."""
+    if T == 1 and tree:
+        pytest.skip("a tree of the root alone is a chain of one token")
+    case(2 + T, [15, 0, 40, 33], [T - 1, T // 2, 0, T - 1], T, 3, 64, 16, kind, tree=tree)
+
+
+def test_chain_of_65():
+    case(3, [15, 16, 14], [64, 64, 64], 65, 1, 128, 16, "e4m3")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_evicted_rows_and_wrapped_rings(kind):
+    case(4, [47, 31, 63], [3, 1, 5], 6, 2, 64, 16, kind, evicted=[5, 3, 1000])
+
+
+def test_without_totals():
+    case(5, [30, 15], [1, 0], 3, 2, 64, 16, "e4m3", totals=False)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_values_of_every_size(kind):
+    """Spreads of many powers of two, subnormals, zeros, and blocks of zeros alone."""
+    def edit(s, kv):
+        kv[0] = 0
+        s["k_tail"][0] = 0
+        s["v_tail"][0] = 0
+        kv[1] *= 2.0 ** -120
+        kv[2] *= 2.0 ** 100
+        kv[3, :, :, 0] = 2.0 ** -130
+        s["k_tail"][3, :, 0] = 2.0 ** -131
+    case(6, [15, 16, 16, 15, 10], [15, 15, 15, 15, 15], 16, 2, 64, 16, kind, spread=3.0, edit=edit)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_ties_and_range_ends(kind):
+    """Values half way between codes, with the largest at the end of the range: scale 1, then scale 2^-7 / 3."""
+    def edit(s, kv):
+        v = torch.arange(64, dtype=torch.float32)
+        if kind == "int8":
+            kv[0, :, :, 0] = (v - 32 + 0.5).to(BF16)
+            kv[0, 0, :, 0, 0] = 127.0
+            kv[1, :, :, 0] = ((v - 32) * 2 + 1).to(BF16) * 2.0 ** -8
+            kv[1, 3, :, 0, 1] = -127 * 2.0 ** -7
+        else:
+            kv[0, :, :, 0] = (64 + 4 * v).to(BF16)            # steps of 8 and 16 above 64: ties between them
+            kv[0, 0, :, 0, 0] = 448.0
+            kv[1, :, :, 0] = (v * 2.0 ** -10).to(BF16)        # around the smallest code, 2^-9
+            kv[1, 3, :, 0, 1] = -300.0
+        kv[2, :, :, 0] = 449.0 if kind == "e4m3" else 3.0
+    case(7, [0, 0, 0], [15, 15, 15], 16, 2, 64, 16, kind, edit=edit)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_blocks_with_infinities_or_nan_get_a_nan_scale(kind, bad):
+    def edit(s, kv):
+        kv[0, 2, 0, 1, 5] = bad      # K, head 1
+        kv[1, 0, 1, 0, 63] = bad     # V, head 0
+    case(8, [15, 12, 14], [3, 5, 2], 6, 2, 64, 16, kind, edit=edit)
+
+
+def test_rows_left_as_they_were():
+    """Timed-out, idle and impossible rows; rows without a page for what they complete."""
+    def edit(s, kv):
+        s["table"][4, int(s["blocks"][4])] = -1
+        s["table"][5, int(s["blocks"][5])] = 10 ** 6
+        s["positions"][7] = -5
+        s["blocks"][8] = 100
+        s["blocks"][9] = -1
+        s["positions"][10] = 2 ** 31 - 3
+    case(9, [15] * 11, [-1, 6, 5, -2 ** 31, 0, 2, 0, 0, 0, 0, 4], 6, 2, 64, 16, "e4m3", edit=edit)
+
+
+def test_full_tables_and_bad_nodes():
+    s = state_with_reserve(10, 1, B=3, Hkv=1, D=64, page=16, kind="e4m3", contexts=[15, 15, 15])
+    kv = random_new(11, 3, 20, 1, 64)
+    num = torch.tensor([19, 3, 3], dtype=torch.int32)      # row 0 completes two blocks, and has room for one
+    nodes = torch.tensor([list(range(1, 20)), [1, 2, 20] + [0] * 16, [4, 4, 4] + [-1] * 16], dtype=torch.int32)
+    cache, positions, blocks = R.to_gpu(s)
+    outs = rsv.cache_commit(cache, kv.cuda()[:, :, 0], kv.cuda()[:, :, 1], num.cuda(), positions, blocks, nodes=nodes.cuda())
+    want = check(s, kv, num, cache, outs, nodes)
+    assert want["positions"].tolist() == [15, 15, 19]
+
+
+def test_graph_replays_advance_in_place():
+    B, T, Hkv, D, page = 3, 5, 2, 64, 16
+    s = state_with_reserve(12, 6, B=B, Hkv=Hkv, D=D, page=page, kind="e4m3", contexts=[3, 15, 30])
+    cache, positions, blocks = R.to_gpu(s)
+    kv = random_new(13, B, T, Hkv, D).cuda()
+    num = torch.zeros(B, dtype=torch.int32, device="cuda")
+    totals = torch.rand((B, cache.max_blocks), device="cuda")
+    w = torch.rand((B, T, cache.max_blocks), device="cuda")
+    def step():  # noqa: E306
+        rsv.cache_commit(cache, kv[:, :, 0], kv[:, :, 1], num, positions, blocks, weights=w, totals=totals,
+                         positions_out=positions, blocks_out=blocks, totals_out=totals)
+    num.fill_(-1)
+    step()                                     # leaves every row as it was
+    torch.cuda.synchronize()
+    totals0 = totals.cpu()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(6):
+        kv.copy_(random_new(20 + i, B, T, Hkv, D))
+        num.copy_(torch.tensor([i % T, (2 * i) % T, -1 if i == 2 else 4]))
+        before = dict(s, **{k: getattr(cache, "block_table" if k == "table" else k).cpu() for k in R.TENSORS},
+                      positions=positions.cpu(), blocks=blocks.cpu())
+        totals0 = totals.cpu()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(before, kv.cpu(), num.cpu(), cache, (positions, blocks, totals), None, w.cpu(), totals0)
+
+
+def test_refusals_on_device_tensors():
+    s = state_with_reserve(14, 2, B=2, Hkv=2, D=64, page=16, kind="e4m3", contexts=[5, 15])
+    cache, positions, blocks = R.to_gpu(s)
+    kv = random_new(15, 2, 3, 2, 64).cuda()
+    num = torch.zeros(2, dtype=torch.int32, device="cuda")
+    def refused(err=ValueError, k=kv[:, :, 0], v=kv[:, :, 1], num=num, positions=positions, blocks=blocks, **kw):  # noqa: E306
+        with pytest.raises(err):
+            rsv.cache_commit(cache, k, v, num, positions, blocks, **kw)
+    refused(k=kv[:, :, 0].float())
+    refused(v=kv[:, :, 1].contiguous())
+    refused(num=num.long())
+    refused(num=num[:1])
+    refused(nodes=torch.zeros((2, 1), dtype=torch.int32, device="cuda"))
+    refused(weights=torch.zeros((2, 3, cache.max_blocks), device="cuda"))          # no totals
+    refused(totals=torch.zeros((2, 1), device="cuda"))
+    refused(totals_out=torch.zeros((2, cache.max_blocks), device="cuda"))
+    refused(rsv.SpecVerifyError, positions_out=positions)                           # one counter in place alone
+    refused(rsv.SpecVerifyError, positions_out=blocks, blocks_out=positions)
+    big = random_new(16, 2, 40, 2, 64).cuda()                                       # the ring is sized for 65 tokens
+    small = rsv.new_cache(2, 8, 2, 64, page=16, max_new=4)
+    with pytest.raises(rsv.SpecVerifyError):
+        rsv.cache_commit(small, big[:, :, 0], big[:, :, 1], num, positions, blocks)

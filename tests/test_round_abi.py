@@ -121,3 +121,58 @@ def test_cache_attention_takes_gpu_tensors_only():
         rsv.KVCache(*(torch.zeros(1, 1, 16, 64, dtype=torch.uint8),) * 7)
     with pytest.raises(ValueError):
         rsv.new_cache(1, 1, 1, 64, device="cpu")
+
+
+def commit(**kw):
+    a = dict(kn=P[10], vn=P[11], kv_row=3 * 512, kv_tok=512, T=3, num=P[12], nodes=None, stride=0, c=cache(),
+             positions=P[13], blocks=P[14], positions_out=P[15], blocks_out=P[16], weights=None, totals=None,
+             totals_out=None)
+    a.update(kw)
+    if a["c"] is not None:
+        a["c"] = ctypes.byref(a["c"])
+    return B.load_library().spec_verify_commit(*a.values(), None)
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES + [dict(tail=16)])   # 16 slots, and 15 + 3 tokens
+def test_commit_refuses_bad_caches(bad):
+    assert commit(c=cache(**bad)) == B.SV_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", UNSUPPORTED_CACHES)
+def test_commit_refuses_unsupported_caches(bad):
+    assert commit(c=cache(**bad)) == B.SV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("bad", [
+    dict(c=None), dict(kn=None), dict(vn=None), dict(num=None), dict(positions=None), dict(blocks=None),
+    dict(positions_out=None), dict(blocks_out=None), dict(T=0), dict(kn=P[10] + 8), dict(kv_tok=4), dict(kv_row=-8),
+    dict(positions_out=P[13]), dict(blocks_out=P[14]), dict(positions_out=P[16]), dict(positions_out=P[14]),
+    dict(positions_out=P[13] + 4), dict(blocks_out=P[14] + 4), dict(nodes=P[17], stride=1),
+    dict(weights=P[18]), dict(totals=P[18]), dict(totals_out=P[18]), dict(totals=P[18], totals_out=P[18] + 40)])
+def test_commit_refuses(bad):
+    assert commit(**bad) == B.SV_ERR_ARG
+
+
+def test_commit_limits():
+    assert commit(T=B.SV_MAX_K + 2, c=cache(tail=128)) == B.SV_ERR_UNSUPPORTED
+
+
+def evict(**kw):
+    a = dict(totals=P[0], table=P[1], blocks=P[2], B=4, most=100, budget=10, first=1, last=1, totals_out=P[3],
+             table_out=P[4], blocks_out=P[5], evicted=P[6])
+    a.update(kw)
+    return B.load_library().spec_verify_evict(*a.values(), None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(totals=None), dict(table=None), dict(blocks=None), dict(totals_out=None), dict(table_out=None),
+    dict(blocks_out=None), dict(evicted=None), dict(B=0), dict(most=0), dict(budget=-1), dict(first=-1), dict(last=-1),
+    dict(totals_out=P[0] + 4), dict(table_out=P[1] + 400), dict(totals_out=P[1]), dict(table_out=P[0]),
+    dict(table_out=P[3] + 8), dict(blocks_out=P[2] + 4), dict(evicted=P[2]), dict(evicted=P[5] + 12)])
+def test_evict_refuses(bad):
+    assert evict(**bad) == B.SV_ERR_ARG
+
+
+def test_evict_limits():
+    assert evict(most=B.SV_MAX_BLOCKS + 1) == B.SV_ERR_UNSUPPORTED
+    assert evict(most=16385, table_out=P[1]) == B.SV_ERR_UNSUPPORTED   # in place, beyond what LDS can hold
