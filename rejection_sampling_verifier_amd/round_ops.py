@@ -18,19 +18,40 @@ from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, _check, _
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
 
 
-class _OnDevice:
-    """Makes `dev` the current device for a call if another one is."""
+class _Elsewhere:
+    """Makes the device current and puts allocations on the stream, for a call
+    that runs on another device or stream than the current ones."""
 
-    def __init__(self, dev):
-        self.ctx = None if dev.index is None or dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    def __init__(self, dev, handle):
+        self.device, self.stream = torch.cuda.device(dev), _OnStream(dev, handle)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.device.__enter__()
+        self.stream.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _scope(dev, stream):
+    """(stream handle, context to allocate and launch in)."""
+    if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device():
+        return _raw_stream(dev.index), _HERE
+    handle = _stream_handle(dev, stream)
+    return handle, _Elsewhere(dev, handle)
 
 
 def _gpu(t, name):
@@ -41,7 +62,11 @@ def _gpu(t, name):
 
 def _need(name, t, shape, dtype, dev):
     """A contiguous tensor of this shape (None: any size there), type and device."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or t.dim() != len(shape)
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return
+    if (t.dtype != dtype or t.device != dev or t.dim() != len(shape)
             or any(w is not None and n != w for n, w in zip(t.shape, shape)) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
                          f"({', '.join('any' if w is None else str(w) for w in shape)}) on {dev}")
@@ -67,9 +92,12 @@ def _p(t):
 def _logit_strides(name, t):
     """(row, position) strides of a [B, P, V] tensor with contiguous logits."""
     B, P, V = t.shape
-    pos = t.stride(1) if P > 1 else V
-    row = t.stride(0) if B > 1 else P * pos
-    if (V > 1 and t.stride(2) != 1) or pos < V or row < (P - 1) * pos + V:
+    row, pos, one = t.stride()
+    if P == 1:
+        pos = V
+    if B == 1:
+        row = P * pos
+    if (V > 1 and one != 1) or pos < V or row < (P - 1) * pos + V:
         raise ValueError(f"{name} must have contiguous, non-overlapping rows of logits")
     return row, pos
 
@@ -130,15 +158,17 @@ def adjust_logits(logits, tokens=None, *, parents=None, history=None, history_le
         if mask_rows is None and mask.shape[0] < B * P:
             raise ValueError(f"mask must hold {B * P} rows without mask_rows")
         c.mask, c.mask_rows, c.num_masks = mask.data_ptr(), _p(mask_rows), mask.shape[0]
-    handle = _stream_handle(dev, stream)
+    handle, scope = _scope(dev, stream)
     if out is None:
-        with _OnStream(dev, handle):
+        with scope:
             out = torch.empty((B, P, V), dtype=logits.dtype, device=dev)
+        out_row, out_pos = P * V, V
     elif (not isinstance(out, torch.Tensor) or tuple(out.shape) != (B, P, V) or out.dtype != logits.dtype
           or out.device != dev):
         raise ValueError(f"out must be a {logits.dtype} tensor of shape {(B, P, V)} on {dev}")
-    out_row, out_pos = _logit_strides("out", out)
-    with _OnDevice(dev):
+    else:
+        out_row, out_pos = _logit_strides("out", out)
+    with scope:
         _check(load_library().spec_verify_adjust_logits(
             logits.data_ptr(), in_row, in_pos, _p(tokens), tok_stride, _p(parents), ctypes.byref(c), B, P, V, dt,
             out.data_ptr(), out_row, out_pos, handle))
@@ -199,11 +229,15 @@ def new_cache(B, num_pages, Hkv, D, page=64, max_blocks=None, max_new=SV_MAX_K +
 def _token_strides(name, t, shape, dev):
     """(row, token) strides of a bf16 [B, T, heads, D] view whose heads lie side by side."""
     B, T, n, D = shape
-    if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != dev
-            or t.stride(3) != 1 or (n > 1 and t.stride(2) != D)):
-        raise ValueError(f"{name} must be a bfloat16 tensor of shape {shape} on {dev}, its heads side by side")
-    tok = t.stride(1) if T > 1 else n * D
-    row = t.stride(0) if B > 1 else T * tok
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not torch.bfloat16 or t.device != dev:
+        raise ValueError(f"{name} must be a bfloat16 tensor of shape {shape} on {dev}")
+    row, tok, head, one = t.stride()
+    if one != 1 or (n > 1 and head != D):
+        raise ValueError(f"the heads of {name} must lie side by side")
+    if T == 1:
+        tok = n * D
+    if B == 1:
+        row = T * tok
     if tok % 8 or row % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name} must be 16-byte aligned in every token")
     return row, tok
@@ -255,9 +289,9 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
     _need("blocks", blocks, (B,), torch.int32, dev)
     _maybe("parents", parents, (B, T), torch.int32, dev)
     _maybe("query_lens", query_lens, (B,), torch.int32, dev)
-    handle = _stream_handle(dev, stream)
+    handle, scope = _scope(dev, stream)
     need = _attention_bytes(cache, T, H, parents is not None, weights is not None and weights is not False)
-    with _OnDevice(dev), _OnStream(dev, handle):
+    with scope:
         make = torch.empty if query_lens is None else torch.zeros
         if weights is True:
             weights = make((B, T, cache.max_blocks), dtype=torch.float32, device=dev)
@@ -316,8 +350,8 @@ def cache_commit(cache, k_new, v_new, num_accepted, positions, blocks, *, nodes=
     _maybe("totals", totals, (B, cache.max_blocks), torch.float32, dev)
     if totals is None and (weights is not None or totals_out is not None):
         raise ValueError("weights and totals_out need totals")
-    handle = _stream_handle(dev, stream)
-    with _OnDevice(dev), _OnStream(dev, handle):
+    handle, scope = _scope(dev, stream)
+    with scope:
         outs = []
         for name, t, like in (("positions_out", positions_out, positions), ("blocks_out", blocks_out, blocks),
                               ("totals_out", totals_out, totals)):
@@ -352,8 +386,8 @@ def cache_evict(block_table, totals, blocks, budget, *, keep_first=0, keep_last=
     _need("block_table", block_table, (B, most), torch.int32, dev)
     _need("totals", totals, (B, most), torch.float32, dev)
     _need("blocks", blocks, (B,), torch.int32, dev)
-    handle = _stream_handle(dev, stream)
-    with _OnDevice(dev), _OnStream(dev, handle):
+    handle, scope = _scope(dev, stream)
+    with scope:
         outs = []
         for name, t, like in (("table_out", table_out, block_table), ("totals_out", totals_out, totals),
                               ("blocks_out", blocks_out, blocks), ("evicted", evicted, blocks)):
