@@ -36,8 +36,9 @@ namespace {
 
 constexpr int TARGET = 1024;   // splits x heads x row tiles that fill the chip
 constexpr int CMIN = 4;        // tiles of a split at least: one per wave
-constexpr int MAX_SPLITS = TARGET + 1;
 constexpr float GROW = 8.f;    // a maximum may lag this much (a factor of 256) before the sums are rescaled
+constexpr float UP = 6.f;      // probabilities are held 2^6 up: with GROW, f16 takes them from 2^14 down to 2^-24
+constexpr float VMIN = 0x1p-90f;  // smallest value scale told apart (see spec_verify.h)
 
 struct AttnArgs {
   const uint16_t* q;
@@ -55,6 +56,7 @@ struct AttnArgs {
   float* weights;
   float* part_o;   // [slots][MT][D] sums of unfinished rows, against their maximum
   float2* part_ml; // [slots][MT] {m, l}
+  int2* info;      // [B][HM] the row's first split and their count
   float* lse;      // [B][Hkv][mtiles * MT] log2 of the softmax denominator
   float* mass;     // [B][Hkv][sub-blocks][mtiles * MT] log2 of a sub-block's sum
   int sub;         // keys of a sub-block: min(page, 64)
@@ -77,17 +79,14 @@ struct Split {
   int tiles;                   // c
 };
 
-// The splits of all rows.  BY_ROW: finds row `want`'s.  Otherwise the one of
-// this work-group: units (split, head, row tile) are dealt so that the row
-// tiles of one head, which read the same keys, run on one XCD next to each
-// other (hardware deals work-groups to the 8 XCDs in turn); `want` is set to
-// the unit's place among the split's heads and row tiles.  Every work-group
-// does this for itself: the lengths are on the device.
-template <bool BY_ROW>
-__device__ __forceinline__ bool find_split(const AttnArgs& a, int& want, Split& out) {
+// The splits of all rows, and this work-group's unit of (split, head, row
+// tile): dealt so that the row tiles of one head, which read the same keys,
+// run on one XCD next to each other (hardware deals work-groups to the 8
+// XCDs in turn).  hm: its head and row tile.  False past the last unit.  Every
+// work-group does this for itself: the lengths are on the device.
+__device__ __forceinline__ bool find_split(const AttnArgs& a, int& hm, Split& out) {
   __shared__ int sums[NWAVE];
   __shared__ Split found;
-  __shared__ int ok;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int per = (a.c.B + WG - 1) / WG;
   const int r0 = min(t * per, a.c.B), r1 = min(r0 + per, a.c.B);
@@ -97,7 +96,6 @@ __device__ __forceinline__ bool find_split(const AttnArgs& a, int& want, Split& 
 #pragma unroll
   for (int o = 32; o; o >>= 1) all += __shfl_xor(all, o, 64);
   if (lane == 0) sums[w] = all;
-  if (t == 0) ok = 0;
   __syncthreads();
   int total = 0;
 #pragma unroll
@@ -125,20 +123,16 @@ __device__ __forceinline__ bool find_split(const AttnArgs& a, int& want, Split& 
     if (k < w) at += sums[k];
     splits += sums[k];
   }
-  int split = 0;
-  if (!BY_ROW) {
-    const int live = splits * a.HM, each = (live + 7) / 8;
-    const int unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= each || unit >= live) return false;
-    split = unit / a.HM;
-    want = unit % a.HM;
-  }
-  if (BY_ROW ? (want >= r0 && want < r1) : (split >= at && split < at + n)) {
+  const int live = splits * a.HM, each = (live + 7) / 8;
+  const int unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= each || unit >= live) return false;
+  const int split = unit / a.HM;
+  hm = unit % a.HM;
+  if (split >= at && split < at + n) {
     for (int r = r0; r < r1; ++r) {
       const int k = (per > 1 ? row_tiles(a, r) + c - 1 : mine + c - 1) / c;
-      if (BY_ROW ? r == want : split < at + k) {
-        found = Split{r, BY_ROW ? 0 : split - at, k, at, c};
-        ok = 1;
+      if (split < at + k) {
+        found = Split{r, split - at, k, at, c};
         break;
       }
       at += k;
@@ -146,7 +140,7 @@ __device__ __forceinline__ bool find_split(const AttnArgs& a, int& want, Split& 
   }
   __syncthreads();
   out = found;
-  return ok != 0;
+  return true;
 }
 
 // ---- lanes 16 and 32 apart --------------------------------------------------
@@ -171,8 +165,9 @@ __device__ __forceinline__ float groups_max(float x) {
   return fmaxf(u, v);
 }
 
-// ---- codes to bf16 ------------------------------------------------------------
-// Eight codes (two words) as a matrix operand.
+// ---- codes to 16 bits -----------------------------------------------------------
+// Eight codes (two words) as a matrix operand: bf16 beside the queries, f16
+// beside the probabilities.  Both kinds are exact in either.
 template <int KIND>
 __device__ __forceinline__ bf16x8 widen(uint32_t w0, uint32_t w1) {
   union { bf16x2 p[4]; uint32_t u[4]; bf16x8 v; } r;
@@ -193,6 +188,26 @@ __device__ __forceinline__ bf16x8 widen(uint32_t w0, uint32_t w1) {
   }
   return r.v;
 }
+template <int KIND>
+__device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
+  union { f16x2 p[4]; f16x8 v; } r;
+  if (KIND == SV_E4M3) {
+    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false);
+    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true);
+    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false);
+    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true);
+  } else {
+    // 0x6400 + u is the f16 1024 + u: with u = code + 128, minus 1152.
+    const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = (k < 2 ? w0 : w1) ^ 0x80808080u;
+      const uint32_t m = __builtin_amdgcn_perm(0x64646464u, w, (k & 1) ? 0x04030402u : 0x04010400u);
+      r.p[k] = __builtin_bit_cast(f16x2, m) - off;
+    }
+  }
+  return r.v;
+}
 __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 template <int D, int NQ>
@@ -201,15 +216,18 @@ struct State {
   float m[NQ], l[NQ];   // l: of the lane's own keys
 };
 
-// Softmax of a tile whose lane holds N scores per query (raw, times c), and
-// the state's rescaling.  p: the probabilities against the running maximum.
+// A tile's softmax; the lane holds N scores of one query, raw, and their keys
+// share the factor c and the value scale 2^lv.  The running maximum m is that
+// of s c + lv, so the p = 2^(s c + lv - m + UP) that come out are the
+// probabilities times the value scale, and need no product with it; l takes
+// p / 2^lv.  any: the lane's keys exist.
 template <int D, int NQ, int N>
-__device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const float (&s)[N], float c, bool any,
-                                             float (&p)[N], float& psum, float& mu) {
+__device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const float (&s)[N], float c, float lv,
+                                             float inv, bool any, float (&p)[N], float& psum) {
   float mx = s[0];
 #pragma unroll
   for (int i = 1; i < N; ++i) mx = fmaxf(mx, s[i]);
-  mx = groups_max(any ? mx * c : NEG_INF);
+  mx = groups_max(any ? fmaf(mx, c, lv) : NEG_INF);
   if (__any(mx > st.m[n] + GROW || (st.m[n] == NEG_INF && mx > NEG_INF))) {
     const float m = fmaxf(st.m[n], mx);
     const float f = m == NEG_INF ? 1.f : exp2_fast(st.m[n] - m);
@@ -218,24 +236,16 @@ __device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const floa
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= f;
   }
-  mu = st.m[n] == NEG_INF ? 0.f : st.m[n];
+  const float off = any ? lv + UP - (st.m[n] == NEG_INF ? 0.f : st.m[n]) : NEG_INF;
+  const float k = any ? c : 0.f;
   psum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    p[i] = exp2_fast(fmaf(s[i], c, -mu));
-    if (!any) p[i] = 0.f;
+    p[i] = exp2_fast(fmaf(s[i], k, off));
     psum += p[i];
   }
+  psum *= inv;
   st.l[n] += psum;
-}
-
-template <int N>
-__device__ __forceinline__ bf16x8 pack_p(const float (&p)[N], int at, float f) {
-  union { bf16x2 h[4]; bf16x8 v; } r;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    r.h[k] = __builtin_convertvector(f32x2{p[at + 2 * k] * f, p[at + 2 * k + 1] * f}, bf16x2);
-  return r.v;
 }
 
 constexpr int VPAD = 8;  // bf16 between the rows of the transposing buffer
@@ -302,7 +312,7 @@ struct Loader {
 };
 
 template <int KIND, int D, int NQ, bool SMALL>
-__global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void cache_attention_kernel(AttnArgs a) {
   constexpr int MT = 16 * NQ;
   __shared__ Lds<D, NQ> sh;
   const int t = threadIdx.x, lane = t & 63, g = lane >> 4, col = lane & 15;
@@ -310,7 +320,7 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
 
   int hm = 0;
   Split sp;
-  if (!find_split<false>(a, hm, sp)) return;
+  if (!find_split(a, hm, sp)) return;
   const int h = hm / a.mtiles, mt = hm % a.mtiles;
   const int b = sp.b;
   const int nq = query_len(a, b);
@@ -393,23 +403,34 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
 #pragma unroll
           for (int n = 0; n < NQ; ++n) s[ut][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[n][ks], s[ut][n], 0, 0, 0);
         }
-      const float c = r.ks * a.scale2, vs = r.ok ? r.vs : 0.f;
+      const float c = r.ks * a.scale2, vs = r.vs < VMIN ? VMIN : r.vs;
+      const float lv = __builtin_amdgcn_logf(vs), inv = __builtin_amdgcn_rcpf(vs);
       const bool ok = r.ok;
       if (!__all(ok)) {
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt)
           if (!ok) r.v[dt] = u32x4{0, 0, 0, 0};  // a code may be NaN
+#pragma unroll
+        for (int ut = 0; ut < 4; ++ut)
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+            if (!ok) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
       ld.load_k(r, in, next);
-      bf16x8 p8[2][NQ];
+      f16x8 p8[2][NQ];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float x[16], p[16], psum, mu;
+        float x[16], p[16], psum;
 #pragma unroll
         for (int j = 0; j < 16; ++j) x[j] = s[j >> 2][n][j & 3];
-        softmax_tile<D, NQ, 16>(st, n, x, c, ok, p, psum, mu);
-        p8[0][n] = pack_p(p, 0, vs);
-        p8[1][n] = pack_p(p, 8, vs);
+        softmax_tile<D, NQ, 16>(st, n, x, c, lv, ok ? inv : 0.f, ok, p, psum);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          union { f16x2 h[4]; f16x8 v; } y;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y.h[j] = __builtin_convertvector(f32x2{p[8 * u + 2 * j], p[8 * u + 2 * j + 1]}, f16x2);
+          p8[u][n] = y.v;
+        }
         if (a.mass) {
           float z = psum;
           if (a.sub > 16) z = sum16(z);
@@ -417,17 +438,17 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
           const int at = (i * 64 + g * 16) / a.sub;
           if ((g * 16) % a.sub == 0 && i * 64 + g * 16 < row.blocks * a.c.page)
             a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + at) * (a.mtiles * MT) + mt * MT + n * 16 + col] =
-                mu + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
+                st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
         }
       }
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const bf16x8 v8 = widen<KIND>(r.v[dt][2 * u], r.v[dt][2 * u + 1]);
+          const f16x8 v8 = widen_f16<KIND>(r.v[dt][2 * u], r.v[dt][2 * u + 1]);
 #pragma unroll
           for (int n = 0; n < NQ; ++n)
-            st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, p8[u][n], st.o[dt][n], 0, 0, 0);
+            st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p8[u][n], st.o[dt][n], 0, 0, 0);
         }
       ld.load_v(r, in, next);
       next = ld.pages(min(i + 2 * NWAVE, end8 - 1));
@@ -471,10 +492,12 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
         for (int ks = 0; ks < D / 32; ++ks)
           s[ut][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(kk[ut][ks]), q[n][ks], s[ut][n], 0, 0, 0);
       }
-    bf16x8 p8[NQ];
+    // Values may be anything that bf16 holds, so probabilities enter in bf16
+    // too, each as the sum of two (16 bits together).
+    bf16x8 hi[NQ], lo[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float x[8], p[8], psum, mu;
+      float x[8], p[8], psum;
       // Seen: the tail (node < 0) and, of the new tokens, a chain's up to the
       // query's own or those of its path.  Plain bit operations: the compiler
       // made wrong code of the same condition written with branches.
@@ -486,8 +509,16 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
         const bool see = (key < have) & ((node <= last) | (bool)((path >> (node & 63)) & 1));
         x[j] = see ? s[j >> 2][n][j & 3] : NEG_INF;
       }
-      softmax_tile<D, NQ, 8>(st, n, x, a.scale2, true, p, psum, mu);
-      p8[n] = pack_p(p, 0, 1.f);
+      softmax_tile<D, NQ, 8>(st, n, x, a.scale2, 0.f, 1.f, true, p, psum);
+      union { bf16x2 h[4]; bf16x8 v; } y, z;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 e = {p[2 * j], p[2 * j + 1]};
+        y.h[j] = __builtin_convertvector(e, bf16x2);
+        z.h[j] = __builtin_convertvector(e - __builtin_convertvector(y.h[j], f32x2), bf16x2);
+      }
+      hi[n] = y.v;
+      lo[n] = z.v;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -497,7 +528,10 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v8.e[j] = vt[(g * 8 + j) * (D + VPAD) + dt * 16 + col];
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8.v, p8[n], st.o[dt][n], 0, 0, 0);
+      for (int n = 0; n < NQ; ++n) {
+        st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8.v, lo[n], st.o[dt][n], 0, 0, 0);
+        st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8.v, hi[n], st.o[dt][n], 0, 0, 0);
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -531,11 +565,12 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
   }
   const int64_t slot = (int64_t)sp.first + sp.index;
   const int64_t part = (slot * a.HM + hm) * MT;
+  if (t == 0 && sp.index == 0) a.info[b * a.HM + hm] = make_int2(sp.first, sp.count);
   if (t < MT) {
     float m, l;
     joined(t, m, l);
     if (sp.count > 1) a.part_ml[part + t] = make_float2(m, l);
-    else if (a.mass) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + mt * MT + t] = m + __builtin_amdgcn_logf(l);
+    else if (a.mass) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + mt * MT + t] = m - UP + __builtin_amdgcn_logf(l);
   }
 #pragma unroll
   for (int dt = 0; dt < D / 16; ++dt) {
@@ -565,19 +600,18 @@ __global__ __launch_bounds__(WG) void cache_attention_kernel(AttnArgs a) {
 template <int D, int NQ>
 __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
   constexpr int MT = 16 * NQ;
-  __shared__ float fac[MAX_SPLITS][16];
+  extern __shared__ float fac[];  // [count][16]
   __shared__ float2 part[16][16];
   const int t = threadIdx.x;
   const int n = blockIdx.x % NQ, unit = blockIdx.x / NQ;
-  const int hm = unit % a.HM, h = hm / a.mtiles, mt = hm % a.mtiles;
-  int b = unit / a.HM;
+  const int hm = unit % a.HM, b = unit / a.HM, h = hm / a.mtiles, mt = hm % a.mtiles;
   const int r0 = mt * MT + n * 16, nq = query_len(a, b);
   if (r0 >= nq * a.G) return;
-  Split sp;
-  if (!find_split<true>(a, b, sp) || sp.count < 2) return;
-  const int count = min(sp.count, MAX_SPLITS);
-  const float2* ml = a.part_ml + ((int64_t)sp.first * a.HM + hm) * MT + n * 16;
-  const float* po = a.part_o + (((int64_t)sp.first * a.HM + hm) * MT + n * 16) * D;
+  const int2 sp = a.info[unit];
+  const int first = sp.x, count = sp.y;
+  if (count < 2) return;
+  const float2* ml = a.part_ml + ((int64_t)first * a.HM + hm) * MT + n * 16;
+  const float* po = a.part_o + (((int64_t)first * a.HM + hm) * MT + n * 16) * D;
   const int64_t step = (int64_t)a.HM * MT;
   const int r = t & 15, k = t >> 4;
   float m = NEG_INF, l = 0.f;
@@ -598,9 +632,9 @@ __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
   for (int j = 0; j < 16; ++j) l += part[j][r].x == NEG_INF ? 0.f : part[j][r].y * exp2_fast(part[j][r].x - m);
   for (int s = k; s < count; s += 16) {
     const float x = ml[s * step + r].x;
-    fac[s][r] = x == NEG_INF ? 0.f : exp2_fast(x - m) / l;
+    fac[s * 16 + r] = x == NEG_INF ? 0.f : exp2_fast(x - m) / l;
   }
-  if (a.mass && k == 0) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + r0 + r] = m + __builtin_amdgcn_logf(l);
+  if (a.mass && k == 0) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + r0 + r] = m - UP + __builtin_amdgcn_logf(l);
   __syncthreads();
   constexpr int V4 = 16 * D / 4 / WG;  // float4 per thread
 #pragma unroll
@@ -608,7 +642,7 @@ __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
     const int e = (v * WG + t) * 4, row = e / D, d = e % D, qr = r0 + row;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int s = 0; s < count; ++s) x += *reinterpret_cast<const f32x4*>(po + s * step * D + e) * fac[s][row];
+    for (int s = 0; s < count; ++s) x += *reinterpret_cast<const f32x4*>(po + s * step * D + e) * fac[s * 16 + row];
     if (qr < nq * a.G) {
       union { bf16x2 p[2]; uint2 u; } y;
       y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
@@ -618,8 +652,11 @@ __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
   }
 }
 
-// weights[b][t][j] = sum over heads and sub-blocks of exp2(mass - lse).
+// weights[b][t][j] = sum over heads and sub-blocks of exp2(mass - lse); the G
+// heads of a kv head lie side by side (V of them a load).
+template <int V>
 __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int mpad) {
+  typedef float vec __attribute__((ext_vector_type(V)));
   const int64_t e = (int64_t)blockIdx.x * WG + threadIdx.x;
   const int t = (int)(e % a.T);
   const int j = (int)(e / a.T % a.c.max_blocks), b = (int)(e / a.T / a.c.max_blocks);
@@ -627,19 +664,25 @@ __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int m
   float x = 0.f;
   if (j < row_state(a.c, a.positions, a.blocks, b).blocks) {
     const int per = a.c.page / a.sub;
-    for (int h = 0; h < a.c.Hkv; ++h) {
-      const float* lse = a.lse + ((int64_t)b * a.c.Hkv + h) * mpad + t * a.G;
-      const float* mass = a.mass + (((int64_t)b * a.c.Hkv + h) * a.nsub + (int64_t)j * per) * mpad + t * a.G;
-      for (int s = 0; s < per; ++s)
-        for (int k = 0; k < a.G; ++k) x += exp2_fast(mass[(int64_t)s * mpad + k] - lse[k]);
-    }
+    const float* lse = a.lse + (int64_t)b * a.c.Hkv * mpad + t * a.G;
+    const float* mass = a.mass + ((int64_t)b * a.c.Hkv * a.nsub + (int64_t)j * per) * mpad + t * a.G;
+    for (int s = 0; s < per; ++s)
+#pragma unroll 4
+      for (int h = 0; h < a.c.Hkv; ++h)
+#pragma unroll 2
+        for (int k = 0; k < a.G; k += V) {
+          const vec p = *reinterpret_cast<const vec*>(mass + ((int64_t)h * a.nsub + s) * mpad + k);
+          const vec q = *reinterpret_cast<const vec*>(lse + (int64_t)h * mpad + k);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x += exp2_fast(p[i] - q[i]);
+        }
   }
   a.weights[((int64_t)b * a.T + t) * a.c.max_blocks + j] = x;
 }
 
 struct Plan {
   int nq, mtiles, grid, nsub, sub;
-  size_t o, ml, lse, mass, total;
+  size_t o, ml, info, lse, mass, total;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -663,6 +706,8 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   off = align256(off + sizeof(float) * (size_t)pl.grid * mt * c.D);
   pl.ml = off;
   off = align256(off + sizeof(float2) * (size_t)pl.grid * mt);
+  pl.info = off;
+  off = align256(off + sizeof(int2) * (size_t)c.B * hm);
   if (weights) {
     const size_t rows = (size_t)c.B * c.Hkv, mpad = (size_t)pl.mtiles * mt;
     pl.lse = off;
@@ -681,11 +726,15 @@ int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
       a.c.page < 64 ? cache_attention_kernel<KIND, D, NQ, true> : cache_attention_kernel<KIND, D, NQ, false>;
   hipLaunchKernelGGL(k, dim3(pl.grid), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
-  hipLaunchKernelGGL((attention_combine_kernel<D, NQ>), dim3(a.c.B * a.HM * NQ), dim3(WG), 0, st, a);
+  hipLaunchKernelGGL((attention_combine_kernel<D, NQ>), dim3(a.c.B * a.HM * NQ), dim3(WG),
+                     (TARGET / a.HM + 2) * 16 * sizeof(float), st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   if (a.weights) {
     const int64_t n = (int64_t)a.c.B * a.T * a.c.max_blocks;
-    hipLaunchKernelGGL(attention_weights_kernel, dim3((uint32_t)((n + WG - 1) / WG)), dim3(WG), 0, st, a,
+    void (*const wk)(AttnArgs, int) = a.G % 4 == 0   ? attention_weights_kernel<4>
+                                      : a.G % 2 == 0 ? attention_weights_kernel<2>
+                                                     : attention_weights_kernel<1>;
+    hipLaunchKernelGGL(wk, dim3((uint32_t)((n + WG - 1) / WG)), dim3(WG), 0, st, a,
                        a.mtiles * 16 * NQ);
     if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   }
@@ -756,6 +805,7 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   char* ws = static_cast<char*>(workspace);
   a.part_o = reinterpret_cast<float*>(ws + pl.o);
   a.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
+  a.info = reinterpret_cast<int2*>(ws + pl.info);
   a.lse = weights ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
   a.mass = weights ? reinterpret_cast<float*>(ws + pl.mass) : nullptr;
   a.sub = pl.sub;
