@@ -566,7 +566,7 @@ typedef struct {
  *              tokens.  What lies behind them in q, k_new and v_new is not
  *              read, and in out and weights not written; a row of 0 is idle.
  * T in [1, SV_MAX_K + 1] ([1, SV_MAX_NODES] with parents), H a multiple of
- * Hkv, scale positive and finite.
+ * Hkv (at most 256 times it), scale positive and finite.
  * out          [B, T, H, D] bf16 contiguous.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
  *              not have.

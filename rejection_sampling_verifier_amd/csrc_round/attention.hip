@@ -5,14 +5,15 @@
 // per query, base 2), O = sum exp2(S - m) V.  The rows of one product are
 // the M = T * H / Hkv queries that share a kv head, in tiles of 16 NQ.
 //
-// Work is cut along the keys as well: a row's keys come in tiles (64 cached
-// tokens, or 32 tail or new tokens), and a split is a run of c tiles.  c is
-// chosen on the device, from all rows' lengths, so that the splits fill the
-// chip whatever the lengths; the grid is its upper bound, and work-groups
-// past the last split leave.  A work-group takes one (split, kv head, row
-// tile); its four waves take the split's tiles in turn, each with a softmax
-// state of its own, without a barrier, and join at the end.  Splits of the
-// same row are joined by a second kernel.
+// Work is cut along the keys as well: a row's keys come in tiles (32 tail or
+// new tokens, then 64 cached ones each); for each row tile of queries the
+// tiles of all rows that have such queries stand in a line, and each
+// work-group takes a run of c of them for one kv head, whatever rows they
+// belong to.  c is found on the device, from the rows' lengths, so that the
+// work-groups fill the chip once and get equal work.  The four waves take a segment's tiles in turn, each with a
+// softmax state of its own, without a barrier, and join at the segment's end.
+// The parts of a row that several work-groups hold are joined by a second
+// kernel.
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T, and tile rows
 // are dealt to the matrix instruction so that nothing is shuffled: lane
@@ -34,8 +35,15 @@ using namespace svr;
 
 namespace {
 
-constexpr int TARGET = 1024;   // splits x heads x row tiles that fill the chip
-constexpr int CMIN = 4;        // tiles of a split at least: one per wave
+constexpr int CUS = 256;
+constexpr int MAX_GROUP = 256;   // query heads per kv head
+constexpr int MAX_MTILES = (MAX_GROUP * (SV_MAX_K + 1) + 15) / 16;
+constexpr int CMIN = 4;        // tiles of a run at least: one per wave
+
+// Work-groups of the attention kernel per CU: waves per SIMD by its registers.
+// Two, each with a whole tile on its way, beat three of half the registers
+// (16 rows of up to 16k tokens, one query each, D = 128: 76 against 83 us).
+constexpr int RESIDENT = 2;
 constexpr float GROW = 8.f;    // a maximum may lag this much (a factor of 256) before the sums are rescaled
 constexpr float UP = 6.f;      // probabilities are held 2^6 up: with GROW, f16 takes them from 2^14 down to 2^-24
 constexpr float VMIN = 0x1p-90f;  // smallest value scale told apart (see spec_verify.h)
@@ -50,13 +58,15 @@ struct AttnArgs {
   const int32_t* blocks;
   const int32_t* parents;
   const int32_t* qlens;
-  int T, H, G, M, mtiles, HM;  // HM: kv heads x row tiles
+  int T, H, G, mtiles;
+  int runs;                    // runs of all row tiles' lines, per head, that fill the chip
+  int even;                    // runs if no line ended with a part of one: the sum over lines is at most runs
   float scale2;                // scale * log2(e)
   uint16_t* out;
   float* weights;
-  float* part_o;   // [slots][MT][D] sums of unfinished rows, against their maximum
-  float2* part_ml; // [slots][MT] {m, l}
-  int2* info;      // [B][HM] the row's first split and their count
+  float* part_o;   // [parts][Hkv][mtiles][MT][D] sums of a part of a row, against its maximum
+  float2* part_ml; // [parts][Hkv][mtiles][MT] {m, l}
+  int2* info;      // [B][Hkv][mtiles] the row's first part and their count
   float* lse;      // [B][Hkv][mtiles * MT] log2 of the softmax denominator
   float* mass;     // [B][Hkv][sub-blocks][mtiles * MT] log2 of a sub-block's sum
   int sub;         // keys of a sub-block: min(page, 64)
@@ -66,77 +76,144 @@ struct AttnArgs {
 __device__ __forceinline__ int query_len(const AttnArgs& a, int b) {
   return a.qlens ? min(max(a.qlens[b], 0), a.T) : a.T;
 }
-__device__ __forceinline__ int cached_tiles(const AttnArgs& a, int blocks) { return (blocks * a.c.page + 63) / 64; }
-__device__ __forceinline__ int row_tiles(const AttnArgs& a, int b) {
-  const int nq = query_len(a, b);
-  if (nq == 0) return 0;
+// A row as the lines of tiles have it.
+struct Row {
+  int n;      // its tiles: near, then cached
+  int near;   // those of the tail and the new tokens
+  int reps;   // row tiles that hold queries
+  int nq, blocks, tail, start;
+};
+template <int MT>
+__device__ __forceinline__ Row row_of(const AttnArgs& a, int b) {
+  Row r;
   const RowState s = row_state(a.c, a.positions, a.blocks, b);
-  return cached_tiles(a, s.blocks) + (s.tail + nq + 31) / 32;
+  r.nq = query_len(a, b);
+  r.blocks = s.blocks;
+  r.tail = s.tail;
+  r.start = s.start;
+  r.near = (s.tail + r.nq + 31) / 32;
+  r.n = r.near + (s.blocks * a.c.page + 63) / 64;
+  r.reps = (r.nq * a.G + MT - 1) / MT;
+  return r;
 }
 
-struct Split {
-  int b, index, count, first;  // row, number within the row, the row's splits and the first one's number
-  int tiles;                   // c
+// A work-group's run: tiles [at, end) of row tile mt's line for head h, the
+// first of them in row b, whose tiles begin at `begin`; c tiles per run.
+struct Run {
+  int b, begin, at, end, c, h, mt;
 };
 
-// The splits of all rows, and this work-group's unit of (split, head, row
-// tile): dealt so that the row tiles of one head, which read the same keys,
-// run on one XCD next to each other (hardware deals work-groups to the 8
-// XCDs in turn).  hm: its head and row tile.  False past the last unit.  Every
-// work-group does this for itself: the lengths are on the device.
-__device__ __forceinline__ bool find_split(const AttnArgs& a, int& hm, Split& out) {
-  __shared__ int sums[NWAVE];
-  __shared__ Split found;
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const int per = (a.c.B + WG - 1) / WG;
-  const int r0 = min(t * per, a.c.B), r1 = min(r0 + per, a.c.B);
-  int mine = 0;
-  for (int r = r0; r < r1; ++r) mine += row_tiles(a, r);
-  int all = mine;
-#pragma unroll
-  for (int o = 32; o; o >>= 1) all += __shfl_xor(all, o, 64);
-  if (lane == 0) sums[w] = all;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int k = 0; k < NWAVE; ++k) total += sums[k];
-  __syncthreads();
-  const int c = max(CMIN, (int)(((int64_t)total * a.HM + TARGET - 1) / TARGET));
-  int n = mine;
-  if (per > 1) {
-    n = 0;
-    for (int r = r0; r < r1; ++r) n += (row_tiles(a, r) + c - 1) / c;
-  } else {
-    n = (mine + c - 1) / c;
-  }
-  int inc = n;
+// Inclusive prefix over the work-group's threads, and the total.
+__device__ __forceinline__ int scan(int v, int* sums, int& total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += u;
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
   }
-  if (lane == 63) sums[w] = inc;
+  if (lane == 63) sums[w] = v;
   __syncthreads();
-  int at = inc - n, splits = 0;
+  total = 0;
 #pragma unroll
   for (int k = 0; k < NWAVE; ++k) {
-    if (k < w) at += sums[k];
-    splits += sums[k];
+    if (k < w) v += sums[k];
+    total += sums[k];
   }
-  const int live = splits * a.HM, each = (live + 7) / 8;
-  const int unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= each || unit >= live) return false;
-  const int split = unit / a.HM;
-  hm = unit % a.HM;
-  if (split >= at && split < at + n) {
+  __syncthreads();
+  return v;
+}
+
+// This work-group's run.  With U(mt) runs in row tile mt's line (fewer the
+// larger mt, as rows with fewer queries have fewer row tiles), units are
+// numbered by run, then head, then row tile, and dealt so that neighbours,
+// which read the same keys, are on one XCD (hardware deals work-groups to the
+// 8 XCDs in turn).  False past the last unit.  Every work-group does this for
+// itself: the lengths are on the device.
+template <int MT>
+__device__ __forceinline__ bool find_run(const AttnArgs& a, Run& out) {
+  __shared__ int sums[NWAVE];
+  __shared__ int lines[MAX_MTILES + 1];  // tiles of row tile mt's line
+  __shared__ int place[2];
+  __shared__ Run found;
+  const int t = threadIdx.x;
+  const int per = (a.c.B + WG - 1) / WG;
+  const int r0 = min(t * per, a.c.B), r1 = min(r0 + per, a.c.B);
+  int total, begin = 0, mine = 0, c, run, mt = 0;
+  int n1 = 0, reps1 = 0;  // of the thread's row, where it has one
+  if (a.mtiles == 1) {
     for (int r = r0; r < r1; ++r) {
-      const int k = (per > 1 ? row_tiles(a, r) + c - 1 : mine + c - 1) / c;
-      if (split < at + k) {
-        found = Split{r, split - at, k, at, c};
-        break;
-      }
-      at += k;
+      const Row x = row_of<MT>(a, r);
+      mine += x.reps > 0 ? x.n : 0;
     }
+    begin = scan(mine, sums, total) - mine;
+    c = max(CMIN, (total + a.even - 1) / a.even);
+  } else {
+    for (int k = t; k <= a.mtiles; k += WG) lines[k] = 0;
+    __syncthreads();
+    for (int r = r0; r < r1; ++r) {
+      const Row x = row_of<MT>(a, r);
+      if (x.reps > 0) atomicAdd(&lines[x.reps - 1], x.n);
+      n1 = x.n;
+      reps1 = x.reps;
+      mine += x.n * x.reps;
+    }
+    scan(mine, sums, total);
+    c = max(CMIN, (total + a.even - 1) / a.even);
+    if (t == 0)
+      for (int k = a.mtiles - 2; k >= 0; --k) lines[k] += lines[k + 1];
+    __syncthreads();
+    total = lines[0];
+  }
+  // Units of the runs before `run`, per head: the sum over mt of min(U(mt), run).
+  auto before = [&](int r) {
+    if (a.mtiles == 1) return min((total + c - 1) / c, r);
+    int n = 0;
+    for (int k = 0; k < a.mtiles; ++k) n += min((lines[k] + c - 1) / c, r);
+    return n;
+  };
+  const int u0 = (total + c - 1) / c;
+  const int units = before(u0) * a.c.Hkv, each = (units + 7) / 8;
+  const int unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= each || unit >= units) return false;
+  int h;
+  if (a.mtiles == 1) {
+    run = unit / a.c.Hkv;
+    h = unit % a.c.Hkv;
+  } else {
+    for (int r = t; r < u0; r += WG) {
+      const int lo = before(r) * a.c.Hkv, hi = before(r + 1) * a.c.Hkv;
+      if (unit >= lo && unit < hi) {
+        place[0] = r;
+        place[1] = unit - lo;
+      }
+    }
+    __syncthreads();
+    run = place[0];
+    const int live = before(run + 1) - before(run);  // row tiles that have this run
+    h = place[1] / live;
+    mt = place[1] % live;
+    total = lines[mt];
+    mine = 0;
+    if (per == 1) mine = reps1 > mt ? n1 : 0;
+    else
+      for (int r = r0; r < r1; ++r) {
+        const Row x = row_of<MT>(a, r);
+        mine += x.reps > mt ? x.n : 0;
+      }
+    int all;
+    begin = scan(mine, sums, all) - mine;
+  }
+  const int at = run * c;
+  if (at >= begin && at < begin + mine) {
+    int r = r0;
+    if (per > 1)
+      for (; r < r1; ++r) {
+        const Row x = row_of<MT>(a, r);
+        const int n = x.reps > mt ? x.n : 0;
+        if (at < begin + n) break;
+        begin += n;
+      }
+    found = Run{r, begin, at, min(at + c, total), c, h, mt};
   }
   __syncthreads();
   out = found;
@@ -250,15 +327,18 @@ __device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const floa
 
 constexpr int VPAD = 8;  // bf16 between the rows of the transposing buffer
 
+constexpr int ROWS = 64;  // rows of a run that are looked up at once
+
 template <int D, int NQ>
 struct Lds {
   static constexpr int MT = 16 * NQ;
   union {
     uint16_t v[NWAVE][32 * (D + VPAD)];  // a wave's 32 tail or new values
-    float slab[2][NWAVE][MT * 20];       // joining: 16 channels of every query, twice
+    float o[NWAVE][MT * (D + 4)];        // joining: the waves' sums
   };
   float m[NWAVE][MT], l[NWAVE][MT];
   uint64_t path[64];
+  Row rows[ROWS];
 };
 
 // The codes of one 64-key tile in a wave's registers.
@@ -271,6 +351,9 @@ struct Codes {
 };
 
 // SMALL: page < 64, so the lane groups of a tile may lie in different pages.
+// V is read past the caches where whole lines of it are used once (64 or more
+// keys to a page, one row tile): 6.9 against 6.1 TB/s in a probe of this
+// pattern; a load instruction of K takes halves of lines, and needs them.
 template <int D, bool SMALL>
 struct Loader {
   const AttnArgs& a;
@@ -305,30 +388,80 @@ struct Loader {
     const int in = SMALL ? (g * 16) % page : (tile * 64) % page + g * 16;
     const int64_t at = (int64_t)clamp(pg.y) * a.c.Hkv + h;
     const uint8_t* p = a.c.v_pages + (at * D + (lane & 15)) * page + in;
+    if (!SMALL && a.mtiles == 1) {
 #pragma unroll
-    for (int dt = 0; dt < D / 16; ++dt) r.v[dt] = *reinterpret_cast<const u32x4*>(p + dt * 16 * page);
+      for (int dt = 0; dt < D / 16; ++dt)
+        r.v[dt] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + dt * 16 * page));
+    } else {
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) r.v[dt] = *reinterpret_cast<const u32x4*>(p + dt * 16 * page);
+    }
     r.vs = a.c.v_scale[at];
   }
 };
 
+template <int D>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int b, int h, int qr, int d, f32x4 x) {
+  union { bf16x2 p[2]; uint2 u; } y;
+  y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
+  y.p[1] = __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2);
+  *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.T + qr / a.G) * a.H + h * a.G + qr % a.G) * D + d) = y.u;
+}
+
 template <int KIND, int D, int NQ, bool SMALL>
-__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void cache_attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RESIDENT))) void cache_attention_kernel(AttnArgs a) {
   constexpr int MT = 16 * NQ;
+  constexpr bool LATE = false;  // too few registers to hold a cached tile beside the new tokens
   __shared__ Lds<D, NQ> sh;
-  const int t = threadIdx.x, lane = t & 63, g = lane >> 4, col = lane & 15;
+  Run run;
+  if (!find_run<MT>(a, run)) return;
+  const int h = run.h, mt = run.mt;
+  int b = run.b, begin = run.begin, at = run.at, base = b - ROWS;
+
+  while (at < run.end) {
+  // Made anew for each segment: what the compiler derives from them would
+  // otherwise be kept in registers across the loop, beyond what there are.
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  const int lane = t & 63, g = lane >> 4, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
 
-  int hm = 0;
-  Split sp;
-  if (!find_split(a, hm, sp)) return;
-  const int h = hm / a.mtiles, mt = hm % a.mtiles;
-  const int b = sp.b;
-  const int nq = query_len(a, b);
-  if (mt * MT >= nq * a.G) return;  // a row tile of queries past the row's own
-  const RowState row = row_state(a.c, a.positions, a.blocks, b);
-  const int n8 = cached_tiles(a, row.blocks);
-  const int nall = n8 + (row.tail + nq + 31) / 32;
-  const int t0 = sp.index * sp.tiles, t1 = min(t0 + sp.tiles, nall);
+  if (b - base >= ROWS) {
+    base = b;
+    __syncthreads();  // idle rows are passed without one
+    if (t < ROWS && b + t < a.c.B) sh.rows[t] = row_of<MT>(a, b + t);
+    __syncthreads();
+  }
+  Row row = sh.rows[b - base];
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(Row) / 4); ++k)
+    reinterpret_cast<int*>(&row)[k] = __builtin_amdgcn_readfirstlane(reinterpret_cast<int*>(&row)[k]);
+  if (row.reps <= mt) row.n = 0;
+  if (at >= begin + row.n) {  // the row has no such queries, or ended
+    begin += row.n;
+    ++b;
+    continue;
+  }
+  const int t0 = at - begin, t1 = min(row.n, run.end - begin);
+  // The row's parts: one for each run that holds some of it.  The numbers of
+  // run and row together tell the parts apart.
+  const int nparts = (begin + row.n - 1) / run.c - begin / run.c + 1;
+  const int part0 = begin / run.c + b, part = at / run.c + b;
+  at = begin + t1;
+  const int nq = row.nq;
+
+  // The wave's first cached tile is on its way while the rest is set up.
+  const Loader<D, SMALL> ld{a, a.c.block_table + (int64_t)b * a.c.max_blocks, h, row.blocks * a.c.page, g, lane};
+  int i = t0 + w;
+  int i8 = i < row.near ? i + (row.near - i + NWAVE - 1) / NWAVE * NWAVE : i;
+  Codes<D> r;
+  int2 next;
+  if (i8 < t1) {
+    const int2 pg = ld.pages(i8 - row.near);
+    ld.load_k(r, i8 - row.near, pg);
+    ld.load_v(r, i8 - row.near, pg);
+    next = ld.pages(min(i8 + NWAVE, t1 - 1) - row.near);
+  }
 
   if (a.parents && t < 64) {
     // Path masks: lane v starts with itself and its parent; each step doubles
@@ -351,7 +484,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void ca
     }
     sh.path[t] = m;
   }
-  __syncthreads();
+  if (a.parents) __syncthreads();
 
   // Q: lane (g, query) of k-step ks = 2 d + half holds channels 64 d + 16 g +
   // 8 half + 0..7, the order in which a lane's K bytes come.
@@ -377,93 +510,15 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void ca
     for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // ---- cached tiles ---------------------------------------------------------
-  int i = t0 + w;
-  const int end8 = min(t1, n8);
-  if (i < end8) {
-    const Loader<D, SMALL> ld{a, a.c.block_table + (int64_t)b * a.c.max_blocks, h, row.blocks * a.c.page, g, lane};
-    Codes<D> r;
-    int2 pg = ld.pages(i);
-    ld.load_k(r, i, pg);
-    ld.load_v(r, i, pg);
-    int2 next = ld.pages(min(i + NWAVE, end8 - 1));
-    for (; i < end8; i += NWAVE) {
-      const int in = min(i + NWAVE, end8 - 1);  // the last tile is loaded again, not used
-      f32x4 s[4][NQ];
-#pragma unroll
-      for (int ut = 0; ut < 4; ++ut)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int ut = 0; ut < 4; ++ut)
-#pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks) {
-          const u32x4 v = r.k[ut][ks >> 1];
-          const bf16x8 k8 = (ks & 1) ? widen<KIND>(v[2], v[3]) : widen<KIND>(v[0], v[1]);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) s[ut][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[n][ks], s[ut][n], 0, 0, 0);
-        }
-      const float c = r.ks * a.scale2, vs = r.vs < VMIN ? VMIN : r.vs;
-      const float lv = __builtin_amdgcn_logf(vs), inv = __builtin_amdgcn_rcpf(vs);
-      const bool ok = r.ok;
-      if (!__all(ok)) {
-#pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt)
-          if (!ok) r.v[dt] = u32x4{0, 0, 0, 0};  // a code may be NaN
-#pragma unroll
-        for (int ut = 0; ut < 4; ++ut)
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-            if (!ok) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-      ld.load_k(r, in, next);
-      f16x8 p8[2][NQ];
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) {
-        float x[16], p[16], psum;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = s[j >> 2][n][j & 3];
-        softmax_tile<D, NQ, 16>(st, n, x, c, lv, ok ? inv : 0.f, ok, p, psum);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          union { f16x2 h[4]; f16x8 v; } y;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y.h[j] = __builtin_convertvector(f32x2{p[8 * u + 2 * j], p[8 * u + 2 * j + 1]}, f16x2);
-          p8[u][n] = y.v;
-        }
-        if (a.mass) {
-          float z = psum;
-          if (a.sub > 16) z = sum16(z);
-          if (a.sub > 32) z = sum32(z);
-          const int at = (i * 64 + g * 16) / a.sub;
-          if ((g * 16) % a.sub == 0 && i * 64 + g * 16 < row.blocks * a.c.page)
-            a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + at) * (a.mtiles * MT) + mt * MT + n * 16 + col] =
-                st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const f16x8 v8 = widen_f16<KIND>(r.v[dt][2 * u], r.v[dt][2 * u + 1]);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-            st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p8[u][n], st.o[dt][n], 0, 0, 0);
-        }
-      ld.load_v(r, in, next);
-      next = ld.pages(min(i + 2 * NWAVE, end8 - 1));
-    }
-  }
-
   // ---- tail and new tokens: 32 keys a tile, key 8 g + j of a tile at lane
   // group g; values are transposed through LDS ----------------------------------
-  for (; i < t1; i += NWAVE) {
-    const int j0 = (i - n8) * 32, have = row.tail + nq;
+  for (; i < min(t1, row.near); i += NWAVE) {
+    const int j0 = i * 32, have = row.tail + nq;
     auto address = [&](int j, bool val) -> const uint16_t* {
       j = min(j, have - 1);
       if (j < row.tail)
         return (val ? a.c.v_tail : a.c.k_tail) +
-               (((int64_t)b * a.c.tail + (row.start + j) % a.c.tail) * a.c.Hkv + h) * D;
+               (((int64_t)b * a.c.tail + row.start + j) * a.c.Hkv + h) * D;  // a block does not wrap
       return (val ? a.vn : a.kn) + b * a.kv_row + (j - row.tail) * a.kv_tok + (int64_t)h * D;
     };
     u32x4 kk[2][D / 32];
@@ -537,6 +592,74 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void ca
     __builtin_amdgcn_wave_barrier();
   }
 
+  // ---- cached tiles ---------------------------------------------------------
+  for (; i8 < t1; i8 += NWAVE) {
+    const int tile = i8 - row.near, in = min(i8 + NWAVE, t1 - 1) - row.near;  // the last tile is loaded again, not used
+    f32x4 s[4][NQ];
+#pragma unroll
+    for (int ut = 0; ut < 4; ++ut)
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ut = 0; ut < 4; ++ut)
+#pragma unroll
+      for (int ks = 0; ks < D / 32; ++ks) {
+        const u32x4 v = r.k[ut][ks >> 1];
+        const bf16x8 k8 = (ks & 1) ? widen<KIND>(v[2], v[3]) : widen<KIND>(v[0], v[1]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) s[ut][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[n][ks], s[ut][n], 0, 0, 0);
+      }
+    const float c = r.ks * a.scale2, vs = r.vs < VMIN ? VMIN : r.vs;
+    const float lv = __builtin_amdgcn_logf(vs), inv = __builtin_amdgcn_rcpf(vs);
+    const bool ok = r.ok;
+    if (!__all(ok)) {
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+        if (!ok) r.v[dt] = u32x4{0, 0, 0, 0};  // a code may be NaN
+#pragma unroll
+      for (int ut = 0; ut < 4; ++ut)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          if (!ok) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    ld.load_k(r, in, next);
+    f16x8 p8[2][NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float x[16], p[16], psum;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = s[j >> 2][n][j & 3];
+      softmax_tile<D, NQ, 16>(st, n, x, c, lv, ok ? inv : 0.f, ok, p, psum);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        union { f16x2 h[4]; f16x8 v; } y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.h[j] = __builtin_convertvector(f32x2{p[8 * u + 2 * j], p[8 * u + 2 * j + 1]}, f16x2);
+        p8[u][n] = y.v;
+      }
+      if (a.mass) {
+        float z = psum;
+        if (a.sub > 16) z = sum16(z);
+        if (a.sub > 32) z = sum32(z);
+        const int at = (tile * 64 + g * 16) / a.sub;
+        if ((g * 16) % a.sub == 0 && tile * 64 + g * 16 < row.blocks * a.c.page)
+          a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + at) * (a.mtiles * MT) + mt * MT + n * 16 + col] =
+              st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f16x8 v8 = widen_f16<KIND>(r.v[dt][2 * u], r.v[dt][2 * u + 1]);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p8[u][n], st.o[dt][n], 0, 0, 0);
+      }
+    ld.load_v(r, in, next);
+    next = ld.pages(min(i8 + 2 * NWAVE, t1 - 1) - row.near);
+  }
+
   // ---- the four waves join ------------------------------------------------------
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
@@ -546,57 +669,43 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(2))) void ca
       sh.l[w][n * 16 + col] = l;
     }
   }
+  __syncthreads();  // every wave is past its use of the transposing buffer
+#pragma unroll
+  for (int n = 0; n < NQ; ++n)
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt)
+      *reinterpret_cast<f32x4*>(&sh.o[w][(n * 16 + col) * (D + 4) + dt * 16 + g * 4]) = st.o[dt][n];
   __syncthreads();
-  auto joined = [&](int r, float& m, float& l) {
-    m = sh.m[0][r];
+  const int64_t slot = (((int64_t)part * a.c.Hkv + h) * a.mtiles + mt) * MT;
+  const int64_t tile = ((int64_t)b * a.c.Hkv + h) * a.mtiles + mt;
+  if (t == 0 && part == part0) a.info[tile] = make_int2(part0, nparts);
 #pragma unroll
-    for (int k = 1; k < NWAVE; ++k) m = fmaxf(m, sh.m[k][r]);
-    l = 0.f;
+  for (int v = 0; v < MT * D / 4 / WG; ++v) {
+    const int e = v * WG + t, rr = e / (D / 4), d = e % (D / 4) * 4;
+    float m = sh.m[0][rr], l = 0.f;
 #pragma unroll
-    for (int k = 0; k < NWAVE; ++k) l += sh.m[k][r] == NEG_INF ? 0.f : sh.l[k][r] * exp2_fast(sh.m[k][r] - m);
-  };
-  float f[NQ];
+    for (int k = 1; k < NWAVE; ++k) m = fmaxf(m, sh.m[k][rr]);
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float m, l;
-    joined(n * 16 + col, m, l);
-    f[n] = st.m[n] == NEG_INF ? 0.f : exp2_fast(st.m[n] - m);
-    if (sp.count == 1) f[n] /= l;
-  }
-  const int64_t slot = (int64_t)sp.first + sp.index;
-  const int64_t part = (slot * a.HM + hm) * MT;
-  if (t == 0 && sp.index == 0) a.info[b * a.HM + hm] = make_int2(sp.first, sp.count);
-  if (t < MT) {
-    float m, l;
-    joined(t, m, l);
-    if (sp.count > 1) a.part_ml[part + t] = make_float2(m, l);
-    else if (a.mass) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + mt * MT + t] = m - UP + __builtin_amdgcn_logf(l);
-  }
-#pragma unroll
-  for (int dt = 0; dt < D / 16; ++dt) {
-    float* slab = sh.slab[dt & 1][w];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) *reinterpret_cast<f32x4*>(slab + (n * 16 + col) * 20 + g * 4) = st.o[dt][n] * f[n];
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int r = n * 16 + (t >> 4), d = t & 15;
-      float x = 0.f;
-#pragma unroll
-      for (int k = 0; k < NWAVE; ++k) x += sh.slab[dt & 1][k][r * 20 + d];
-      if (sp.count > 1) {
-        a.part_o[(part + r) * D + dt * 16 + d] = x;
-      } else {
-        const int qr = mt * MT + r;
-        if (qr < nq * a.G)
-          a.out[(((int64_t)b * a.T + qr / a.G) * a.H + h * a.G + qr % a.G) * D + dt * 16 + d] =
-              __builtin_bit_cast(uint16_t, (__bf16)x);
-      }
+    for (int k = 0; k < NWAVE; ++k) {
+      const float f = sh.m[k][rr] == NEG_INF ? 0.f : exp2_fast(sh.m[k][rr] - m);
+      l += sh.l[k][rr] * f;
+      x += *reinterpret_cast<const f32x4*>(&sh.o[k][rr * (D + 4) + d]) * f;
     }
+    if (nparts > 1) {
+      *reinterpret_cast<f32x4*>(a.part_o + (slot + rr) * D + d) = x;
+      if (d == 0) a.part_ml[slot + rr] = make_float2(m, l);
+    } else {
+      const int qr = mt * MT + rr;
+      if (qr < nq * a.G) store_out<D>(a, b, h, qr, d, x * (1.f / l));
+      if (a.mass && d == 0) a.lse[tile * MT + rr] = m - UP + __builtin_amdgcn_logf(l);
+    }
+  }
+  __syncthreads();  // the shared arrays are free for the next segment
   }
 }
 
-// Joins the splits of one row, kv head and 16 queries.
+// Joins the parts of one row, kv head and 16 queries.
 template <int D, int NQ>
 __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
   constexpr int MT = 16 * NQ;
@@ -604,15 +713,15 @@ __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
   __shared__ float2 part[16][16];
   const int t = threadIdx.x;
   const int n = blockIdx.x % NQ, unit = blockIdx.x / NQ;
-  const int hm = unit % a.HM, b = unit / a.HM, h = hm / a.mtiles, mt = hm % a.mtiles;
+  const int mt = unit % a.mtiles, h = unit / a.mtiles % a.c.Hkv, b = unit / a.mtiles / a.c.Hkv;
   const int r0 = mt * MT + n * 16, nq = query_len(a, b);
   if (r0 >= nq * a.G) return;
   const int2 sp = a.info[unit];
-  const int first = sp.x, count = sp.y;
+  const int count = sp.y;
   if (count < 2) return;
-  const float2* ml = a.part_ml + ((int64_t)first * a.HM + hm) * MT + n * 16;
-  const float* po = a.part_o + (((int64_t)first * a.HM + hm) * MT + n * 16) * D;
-  const int64_t step = (int64_t)a.HM * MT;
+  const int64_t first = ((int64_t)sp.x * a.c.Hkv + h) * a.mtiles + mt, step = (int64_t)a.c.Hkv * a.mtiles * MT;
+  const float2* ml = a.part_ml + first * MT + n * 16;
+  const float* po = a.part_o + (first * MT + n * 16) * D;
   const int r = t & 15, k = t >> 4;
   float m = NEG_INF, l = 0.f;
   for (int s = k; s < count; s += 16) {
@@ -643,12 +752,7 @@ __global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int s = 0; s < count; ++s) x += *reinterpret_cast<const f32x4*>(po + s * step * D + e) * fac[s * 16 + row];
-    if (qr < nq * a.G) {
-      union { bf16x2 p[2]; uint2 u; } y;
-      y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
-      y.p[1] = __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2);
-      *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.T + qr / a.G) * a.H + h * a.G + qr % a.G) * D + d) = y.u;
-    }
+    if (qr < nq * a.G) store_out<D>(a, b, h, qr, d, x);
   }
 }
 
@@ -681,7 +785,7 @@ __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int m
 }
 
 struct Plan {
-  int nq, mtiles, grid, nsub, sub;
+  int nq, mtiles, grid, runs, even, nsub, sub;
   size_t o, ml, info, lse, mass, total;
 };
 
@@ -689,25 +793,33 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   const int M = T * (H / c.Hkv);
-  pl.nq = M <= 16 ? 1 : 2;
+  // 64 rows beside D = 128 would leave one wave per SIMD (61-node trees over
+  // up to 4k tokens: 261 against 181 us); beside D = 64 they halve the reads
+  // and conversions (64 rows over 131k int8 tokens: 114 against 131 us).
+  pl.nq = M <= 16 ? 1 : M <= 32 || c.D == 128 ? 2 : 4;
   const int mt = 16 * pl.nq;
   pl.mtiles = (M + mt - 1) / mt;
-  const int64_t hm = (int64_t)c.Hkv * pl.mtiles;
+  const int64_t tiles = (int64_t)c.B * pl.mtiles, heads = tiles * c.Hkv;
   const int64_t most = ((int64_t)c.max_blocks * c.page + 63) / 64 + (c.page - 1 + T + 31) / 32;
-  if (most * c.B > INT_MAX || hm > INT_MAX / 64) return SV_ERR_UNSUPPORTED;
-  const int64_t units = std::min((int64_t)TARGET + c.B * hm, c.B * ((most + CMIN - 1) / CMIN) * hm);
-  if (units > INT_MAX / 2 || c.B * hm * pl.nq > INT_MAX) return SV_ERR_UNSUPPORTED;
-  pl.grid = (int)((units + 7) / 8 * 8);
+  if (most * tiles > INT_MAX || heads * pl.nq > INT_MAX) return SV_ERR_UNSUPPORTED;
+  // Runs that the chip holds at once (see the kernel's registers).  Each row
+  // tile's line may end with a part of a run, so the length of a run is
+  // chosen for that many fewer (half of them where row tiles are many).
+  const int64_t room = std::max<int64_t>(1, CUS * RESIDENT / c.Hkv);
+  pl.even = (int)std::max<int64_t>(room - (pl.mtiles - 1), (room + 1) / 2);
+  pl.runs = (int)std::min<int64_t>(pl.even, (most * tiles + CMIN - 1) / CMIN) + pl.mtiles - 1;
+  pl.grid = (pl.runs * c.Hkv + 7) / 8 * 8;
+  const int64_t parts = ((int64_t)pl.runs + c.B) * c.Hkv * pl.mtiles;
   pl.sub = std::min(c.page, 64);
   const int64_t nsub = (int64_t)c.max_blocks * (c.page / pl.sub);
   pl.nsub = (int)nsub;
   size_t off = 0;
   pl.o = off;
-  off = align256(off + sizeof(float) * (size_t)pl.grid * mt * c.D);
+  off = align256(off + sizeof(float) * (size_t)parts * mt * c.D);
   pl.ml = off;
-  off = align256(off + sizeof(float2) * (size_t)pl.grid * mt);
+  off = align256(off + sizeof(float2) * (size_t)parts * mt);
   pl.info = off;
-  off = align256(off + sizeof(int2) * (size_t)c.B * hm);
+  off = align256(off + sizeof(int2) * (size_t)heads);
   if (weights) {
     const size_t rows = (size_t)c.B * c.Hkv, mpad = (size_t)pl.mtiles * mt;
     pl.lse = off;
@@ -726,8 +838,8 @@ int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
       a.c.page < 64 ? cache_attention_kernel<KIND, D, NQ, true> : cache_attention_kernel<KIND, D, NQ, false>;
   hipLaunchKernelGGL(k, dim3(pl.grid), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
-  hipLaunchKernelGGL((attention_combine_kernel<D, NQ>), dim3(a.c.B * a.HM * NQ), dim3(WG),
-                     (TARGET / a.HM + 2) * 16 * sizeof(float), st, a);
+  hipLaunchKernelGGL((attention_combine_kernel<D, NQ>), dim3(a.c.B * a.c.Hkv * a.mtiles * NQ), dim3(WG),
+                     (a.runs + 1) * 16 * sizeof(float), st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   if (a.weights) {
     const int64_t n = (int64_t)a.c.B * a.T * a.c.max_blocks;
@@ -742,6 +854,8 @@ int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
 }
 template <int KIND, int D>
 int launch_rows(const AttnArgs& a, const Plan& pl, hipStream_t st) {
+  if constexpr (D == 64)
+    if (pl.nq == 4) return launch<KIND, D, 4>(a, pl, st);
   return pl.nq == 1 ? launch<KIND, D, 1>(a, pl, st) : launch<KIND, D, 2>(a, pl, st);
 }
 template <int KIND>
@@ -761,7 +875,7 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   if (bad != SV_OK) return bad;
   const sv_cache& c = *cache;
   if (T < 1 || H < 1 || H % c.Hkv) return SV_ERR_ARG;
-  if (T > (parents ? SV_MAX_NODES : SV_MAX_K + 1) || H > (1 << 16)) return SV_ERR_UNSUPPORTED;
+  if (T > (parents ? SV_MAX_NODES : SV_MAX_K + 1) || H / c.Hkv > MAX_GROUP) return SV_ERR_UNSUPPORTED;
   Plan pl;
   const int rc = make_plan(c, T, H, weights != nullptr, pl);
   if (rc != SV_OK) return rc;
@@ -796,9 +910,9 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   a.T = T;
   a.H = H;
   a.G = H / c.Hkv;
-  a.M = T * a.G;
   a.mtiles = pl.mtiles;
-  a.HM = c.Hkv * pl.mtiles;
+  a.runs = pl.runs;
+  a.even = pl.even;
   a.scale2 = scale * LOG2E;
   a.out = static_cast<uint16_t*>(out);
   a.weights = weights;
