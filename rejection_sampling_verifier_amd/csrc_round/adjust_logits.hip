@@ -10,13 +10,21 @@
 // first counts the row's history inside its chunk: a direct-addressed table
 // of counts in LDS, built by integer atomics, so the order of the tokens
 // does not matter and there is nothing to sort or to clear in memory.  The
-// history is read again by each of a row's chunks, out of L2.  Then it
-// streams its chunk of every position, 16 bytes per lane; a bit per id says
-// which vectors hold a counted or biased token and take the slow path.
-// Drafted tokens are not counted in the table: a position's own are those
-// of its path (a 64-bit mask over the drafted tokens) that fall into the
-// chunk, usually none or one, and the slow path adds them, so positions
-// need no barrier between them.
+// history is read again by each of a row's chunks, out of L2.  A bit per id
+// tells which ids are counted, drafted or biased, and their list is made of
+// it.  Then it streams its chunk of every position, 16 bytes per lane and
+// eight such loads at once.  A wave whose window of 64 vectors holds listed
+// ids puts those vectors into LDS, changes the ids there, one lane each, and
+// takes the vectors back: doing it in place, all lanes for all ids of a
+// vector, made the kernel bound by its arithmetic (538 against 450 us on 256
+// rows of 8 positions of 201,088 ids with every control).  The next positions'
+// loads are issued before the present ones are changed, the first before the
+// tables are made (450 -> 402 us), and loads and stores pass the caches by
+// (402 -> 391 us; 64 rows of 6 positions of 151,936 ids: 57 -> 51 us, 4.6 TB/s,
+// where a large copy reaches 4.9).  Drafted tokens are
+// not counted in the table: a position's own are those of its path (a 64-bit
+// mask over the drafted tokens) that fall into the chunk, usually none or
+// one, so positions need no barrier between them.
 
 #include <cstdint>
 
@@ -29,7 +37,9 @@ namespace {
 
 constexpr int CH = 4096;                 // token ids per chunk
 constexpr int GRID_WANTED = 1024;        // work-groups that fill the chip; below, positions are split too
-constexpr uint32_t IN_PROMPT = 1u << 31; // table entry: occurs in the prompt; the rest counts n(x)
+constexpr uint32_t IN_PROMPT = 1u << 31; // table entry: occurs in the prompt;
+constexpr uint32_t BIASED = 1u << 30;    // has a bias; the rest counts n(x)
+constexpr int BIASES = 1024;             // bias entries of a chunk that LDS holds
 
 struct AdjustArgs {
   const void* in;
@@ -49,18 +59,12 @@ struct AdjustArgs {
 typedef u32x4 u32x4_u __attribute__((aligned(2)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef i32x4 i32x4_u __attribute__((aligned(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <typename ET> struct Out;
 template <> struct Out<uint16_t> {
-  static constexpr uint16_t NEG = 0xFF80u;
+  __device__ __forceinline__ static float widen(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
   // Round to nearest even, the conversion's own rounding.
-  __device__ __forceinline__ static void pack(u32x4& v, const float (&x)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      v[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * k], x[2 * k + 1]}, bf16x2));
-  }
+  __device__ __forceinline__ static uint16_t narrow(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
   __device__ __forceinline__ static uint16_t one(const u32x4& v, int k) { return (uint16_t)(v[k >> 1] >> (16 * (k & 1))); }
   // Words whose two tokens are cut by the allowed bits.
   __device__ __forceinline__ static void cut(u32x4& v, uint32_t allow) {
@@ -74,11 +78,8 @@ template <> struct Out<uint16_t> {
   }
 };
 template <> struct Out<float> {
-  static constexpr float NEG = NEG_INF;
-  __device__ __forceinline__ static void pack(u32x4& v, const float (&x)[4]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __float_as_uint(x[k]);
-  }
+  __device__ __forceinline__ static float widen(float x) { return x; }
+  __device__ __forceinline__ static float narrow(float x) { return x; }
   __device__ __forceinline__ static float one(const u32x4& v, int k) { return __uint_as_float(v[k]); }
   __device__ __forceinline__ static void cut(u32x4& v, uint32_t allow) {
 #pragma unroll
@@ -87,16 +88,19 @@ template <> struct Out<float> {
   }
 };
 
-// LDS: the chunk's tables.  `bias` holds 1 + the number of the last entry of
-// the bias list for the id.
-template <bool BIAS>
+// LDS: the chunk's tables.
 struct Tables {
   alignas(16) uint32_t count[CH];
-  alignas(16) int32_t bias[BIAS ? CH : 1];
+  alignas(16) u32x4 stage[WG];  // a wave's window, while listed ids change
   uint32_t touched[CH / 32];
-  int32_t local[64];     // drafted tokens' places in the chunk
-  uint64_t path[64];     // tree: nodes on the path root .. v
-  uint64_t here;         // drafted tokens inside the chunk
+  int before[CH / 32 + 1];      // listed ids before each word of `touched`
+  uint16_t list[CH];
+  uint16_t bias_at[BIASES];     // bias entries in the chunk: place and number
+  int bias_no[BIASES];
+  int biases;
+  int local[64];                // drafted tokens' places in the chunk
+  uint64_t path[64];            // tree: nodes on the path root .. v
+  uint64_t here[CH / 256];      // drafted tokens inside each window of a wave's 64 vectors
 };
 
 // The path masks of a tree, by one wave: lane v starts with itself and its
@@ -123,22 +127,72 @@ __device__ __forceinline__ uint64_t path_mask(const int32_t* par, int N) {
   return m;
 }
 
-template <typename ET, bool BIAS>
-__global__ __launch_bounds__(WG) void adjust_logits_kernel(AdjustArgs a) {
+// Vectors of U positions, NV per thread each.
+template <int NV, int U>
+struct Group {
+  u32x4 v[U][NV];
+  uint32_t allow[U][NV];
+};
+
+template <typename ET>
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void adjust_logits_kernel(AdjustArgs a) {
   constexpr int VEC = Tr<ET>::VEC;
   constexpr int NV = CH / (WG * VEC);  // vectors per thread and position
-  __shared__ Tables<BIAS> sh;
-  const int t = threadIdx.x;
+  constexpr int U = 8 / NV;            // positions at once
+  __shared__ Tables sh;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int pg = blockIdx.x % a.PG;
   const int chunk = (blockIdx.x / a.PG) % a.C;
   const int b = blockIdx.x / a.PG / a.C;
   const int lo = chunk * CH, len = min(CH, a.V - lo);
 
-  for (int i = t; i < CH / 4; i += WG) {
-    reinterpret_cast<u32x4*>(sh.count)[i] = u32x4{0, 0, 0, 0};
-    if (BIAS) reinterpret_cast<u32x4*>(sh.bias)[i] = u32x4{0, 0, 0, 0};
-  }
+  constexpr uint32_t ALL = (1u << VEC) - 1;
+  const int p0 = (int)((int64_t)a.P * pg / a.PG), p1 = (int)((int64_t)a.P * (pg + 1) / a.PG);
+
+  // The vectors of positions i0 .. i0 + U - 1 that are needed, and what their
+  // masks allow.
+  auto fetch = [&](Group<NV, U>& r, int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      const uint32_t* mask = nullptr;
+      if (a.c.mask && i < p1) {
+        const int64_t row = a.c.mask_rows ? (int64_t)a.c.mask_rows[(int64_t)b * a.P + i] : (int64_t)b * a.P + i;
+        if (row >= 0 && row < a.c.num_masks) mask = a.c.mask + row * a.words + lo / 32;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * WG + t) * VEC;
+        r.allow[u][j] = mask && e < len ? (mask[e >> 5] >> (e & 31)) & ALL : ALL;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const ET* src = static_cast<const ET*>(a.in) + b * a.in_row + (i0 + u) * a.in_pos + lo;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * WG + t) * VEC;
+        bool need = i0 + u < p1 && e < len && r.allow[u][j];
+        if (a.inplace && r.allow[u][j] == ALL) need = need && ((sh.touched[e >> 5] >> (e & 31)) & ALL);
+        if (!need) continue;
+        if (e + VEC <= len) r.v[u][j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_u*>(src + e));
+        else {
+          r.v[u][j] = u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int k = 0; k < VEC; ++k)
+            if (e + k < len) Tr<ET>::set(r.v[u][j], k, src + e + k);
+        }
+      }
+    }
+  };
+  // The first of them are on their way while the tables are made (in place,
+  // what is needed depends on the tables).
+  Group<NV, U> now;
+  if (!a.inplace) fetch(now, p0);
+
+  for (int i = t; i < CH / 4; i += WG) reinterpret_cast<u32x4*>(sh.count)[i] = u32x4{0, 0, 0, 0};
   if (t < CH / 32) sh.touched[t] = 0;
+  if (t == 0) sh.biases = 0;
   const int drafted = a.penalties && a.tokens ? (a.parents ? a.P : a.P - 1) : 0;
   if (t < 64) {
     int at = -1;
@@ -147,17 +201,20 @@ __global__ __launch_bounds__(WG) void adjust_logits_kernel(AdjustArgs a) {
       at = d < (uint32_t)len ? (int)d : -1;
     }
     sh.local[t] = at;
-    const uint64_t m = __ballot(at >= 0);
-    if (t == 0) sh.here = m;
+#pragma unroll
+    for (int k = 0; k < CH / (64 * VEC); ++k) {
+      const uint64_t m = __ballot(at >= 0 && at / (64 * VEC) == k);
+      if (t == 0) sh.here[k] = m;
+    }
     if (a.parents) sh.path[t] = path_mask(a.parents + (int64_t)b * a.P, a.P);
   }
   __syncthreads();
   if (t < 64 && sh.local[t] >= 0) atomicOr(&sh.touched[sh.local[t] >> 5], 1u << (sh.local[t] & 31));
   if (a.penalties && a.c.history) {
     const int32_t* h = a.c.history + b * a.c.history_stride;
-    const int64_t n = min((int64_t)max(a.c.history_lens[b], 0), a.c.history_stride);
-    const int64_t np = a.c.prompt_lens ? (int64_t)max(a.c.prompt_lens[b], 0) : 0;
-    auto take = [&](int tok, int64_t j) {
+    const int n = (int)min((int64_t)max(a.c.history_lens[b], 0), a.c.history_stride);
+    const int np = a.c.prompt_lens ? max(a.c.prompt_lens[b], 0) : 0;
+    auto take = [&](int tok, int j) {
       const uint32_t d = (uint32_t)tok - (uint32_t)lo;
       if (d < (uint32_t)len) {
         if (j < np) atomicOr(&sh.count[d], IN_PROMPT);
@@ -165,110 +222,140 @@ __global__ __launch_bounds__(WG) void adjust_logits_kernel(AdjustArgs a) {
         atomicOr(&sh.touched[d >> 5], 1u << (d & 31));
       }
     };
-    const int64_t n4 = n / 4;
-    for (int64_t j = t; j < n4; j += WG) {
-      const i32x4 w = *reinterpret_cast<const i32x4_u*>(h + 4 * j);
+    const int n4 = n / 4;
+    for (int j = t; j < n4; j += 4 * WG) {
+      i32x4 x[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) take(w[k], 4 * j + k);
+      for (int s = 0; s < 4; ++s)
+        x[s] = j + s * WG < n4 ? *reinterpret_cast<const i32x4_u*>(h + 4 * (int64_t)(j + s * WG)) : i32x4{-1, -1, -1, -1};
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) take(x[s][k], 4 * (j + s * WG) + k);
     }
     if (4 * n4 + t < n) take(h[4 * n4 + t], 4 * n4 + t);
   }
-  if (BIAS) {
-    const int32_t* ids = a.c.bias_ids + b * a.c.bias_stride;
-    const int n = (int)(a.c.bias_lens ? min((int64_t)max(a.c.bias_lens[b], 0), a.c.bias_stride) : a.c.bias_stride);
-    for (int e = t; e < n; e += WG) {
-      const uint32_t d = (uint32_t)ids[e] - (uint32_t)lo;
-      if (d < (uint32_t)len) {
-        atomicMax(&sh.bias[d], e + 1);
-        atomicOr(&sh.touched[d >> 5], 1u << (d & 31));
+  const int32_t* bias_ids = a.c.bias_ids + b * a.c.bias_stride;
+  const float* bias_values = a.c.bias_values + b * a.c.bias_stride;
+  const int nbias = !a.c.bias_ids ? 0
+                    : (int)(a.c.bias_lens ? min((int64_t)max(a.c.bias_lens[b], 0), a.c.bias_stride) : a.c.bias_stride);
+  for (int e = t; e < nbias; e += WG) {
+    const uint32_t d = (uint32_t)bias_ids[e] - (uint32_t)lo;
+    if (d < (uint32_t)len) {
+      atomicOr(&sh.count[d], BIASED);
+      atomicOr(&sh.touched[d >> 5], 1u << (d & 31));
+      const int k = atomicAdd(&sh.biases, 1);  // in any order: the search below takes the last entry by its number
+      if (k < BIASES) {
+        sh.bias_at[k] = (uint16_t)d;
+        sh.bias_no[k] = e;
       }
     }
+  }
+  __syncthreads();
+
+  // The list of touched ids.
+  if (t < 64) {
+    const uint32_t w0 = sh.touched[2 * t], w1 = sh.touched[2 * t + 1];
+    const int n0 = __popc(w0), n = n0 + __popc(w1);
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc, o, 64);
+      if (t >= o) inc += u;
+    }
+    sh.before[2 * t] = inc - n;
+    sh.before[2 * t + 1] = inc - n + n0;
+    if (t == 63) sh.before[128] = inc;
+  }
+  __syncthreads();
+  if (t < CH / 32) {
+    int k = sh.before[t];
+    for (uint32_t m = sh.touched[t]; m; m &= m - 1) sh.list[k++] = (uint16_t)(t * 32 + __ffs(m) - 1);
   }
   __syncthreads();
 
   const float r = a.c.repetition ? a.c.repetition[b] : 1.f;
   const float freq = a.c.frequency ? a.c.frequency[b] : 0.f;
   const float pres = a.c.presence ? a.c.presence[b] : 0.f;
-  const uint64_t here = sh.here;
-  constexpr uint32_t ALL = (1u << VEC) - 1;
-  const int p0 = (int)((int64_t)a.P * pg / a.PG), p1 = (int)((int64_t)a.P * (pg + 1) / a.PG);
-
-  for (int i = p0; i < p1; ++i) {
-    const ET* src = static_cast<const ET*>(a.in) + b * a.in_row + i * a.in_pos + lo;
-    ET* dst = static_cast<ET*>(a.out) + b * a.out_row + i * a.out_pos + lo;
-    const uint32_t* mask = nullptr;
-    if (a.c.mask) {
-      const int64_t row = a.c.mask_rows ? (int64_t)a.c.mask_rows[(int64_t)b * a.P + i] : (int64_t)b * a.P + i;
-      if (row >= 0 && row < a.c.num_masks) mask = a.c.mask + row * a.words + lo / 32;
-    }
-    const uint64_t path = here & (a.parents ? sh.path[i & 63] : i >= 64 ? ~0ull : (1ull << i) - 1);
-
-    u32x4 v[NV];
-    uint32_t allow[NV], touch[NV];
+  // For each of the thread's vectors: its listed ids, and its wave's window:
+  // the part of the list and the drafted tokens in it.
+  uint32_t touch[NV];
+  int k0[NV], k1[NV];
+  uint64_t here[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = (j * WG + t) * VEC;
-      allow[j] = ALL;
-      touch[j] = 0;
-      if (e < len) {
-        if (mask) allow[j] = (mask[e >> 5] >> (e & 31)) & ALL;
-        touch[j] = (sh.touched[e >> 5] >> (e & 31)) & ALL;
+  for (int j = 0; j < NV; ++j) {
+    const int e = (j * WG + t) * VEC, win = __builtin_amdgcn_readfirstlane((j * WG + w * 64) * VEC);
+    touch[j] = (sh.touched[e >> 5] >> (e & 31)) & ALL;
+    k0[j] = __builtin_amdgcn_readfirstlane(sh.before[win / 32]);
+    k1[j] = __builtin_amdgcn_readfirstlane(sh.before[win / 32 + 2 * VEC]);
+    here[j] = sh.here[win / (64 * VEC)];
+  }
+  const int nb = sh.biases;
+  // Listed id d's logit; path: the position's drafted tokens near it.
+  auto adjusted = [&](float x, int d, uint64_t path) {
+    const uint32_t c = sh.count[d];
+    uint32_t n = c & ~(IN_PROMPT | BIASED);
+    for (uint64_t m = path; m; m &= m - 1) n += sh.local[__builtin_ctzll(m)] == d;
+    if (n | (c & IN_PROMPT)) x = x > 0.f ? x / r : x * r;
+    if (n) x = (x - freq * (float)n) - pres;
+    if (c & BIASED) {
+      int last = -1;
+      if (nb <= BIASES) {
+        for (int k = 0; k < nb; ++k)
+          if (sh.bias_at[k] == d) last = max(last, sh.bias_no[k]);
+      } else {
+        for (int k = 0; k < nbias; ++k)
+          if (bias_ids[k] == lo + d) last = k;
       }
+      x = x + bias_values[last];
     }
+    return x;
+  };
+
+  if (a.inplace) fetch(now, p0);
+  for (int i0 = p0; i0 < p1; i0 += U) {
+    Group<NV, U> next;
+    if (i0 + U < p1) fetch(next, i0 + U);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = (j * WG + t) * VEC;
-      const bool need = allow[j] && (!a.inplace || touch[j] || allow[j] != ALL);
-      if (need) {
-        if (e + VEC <= len) v[j] = *reinterpret_cast<const u32x4_u*>(src + e);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u;
+      if (i >= p1) break;
+      ET* dst = static_cast<ET*>(a.out) + b * a.out_row + i * a.out_pos + lo;
+      const uint64_t path = a.parents ? sh.path[i & 63] : i >= 64 ? ~0ull : (1ull << i) - 1;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int e = (j * WG + t) * VEC;
+        const int win = (j * WG + w * 64) * VEC;
+        if (k1[j] > k0[j]) {
+          const uint64_t on = path & here[j];
+          ET* stage = reinterpret_cast<ET*>(sh.stage + w * 64);
+          if (touch[j]) sh.stage[t] = now.v[u][j];
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          for (int k = k0[j] + lane; k < k1[j]; k += 64) {
+            const int d = sh.list[k];
+            stage[d - win] = Out<ET>::narrow(adjusted(Out<ET>::widen(stage[d - win]), d, on));
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+          if (touch[j]) now.v[u][j] = sh.stage[t];
+        }
+        if (e >= len || (a.inplace && !touch[j] && now.allow[u][j] == ALL)) continue;
+        if (!now.allow[u][j]) {
+          const uint32_t f = Tr<ET>::NEG_INF_WORD;
+          now.v[u][j] = u32x4{f, f, f, f};
+        } else if (now.allow[u][j] != ALL) {
+          Out<ET>::cut(now.v[u][j], now.allow[u][j]);
+        }
+        if (e + VEC <= len) __builtin_nontemporal_store(now.v[u][j], reinterpret_cast<u32x4_u*>(dst + e));
         else {
-          v[j] = u32x4{0, 0, 0, 0};
 #pragma unroll
           for (int k = 0; k < VEC; ++k)
-            if (e + k < len) Tr<ET>::set(v[j], k, src + e + k);
+            if (e + k < len) dst[e + k] = Out<ET>::one(now.v[u][j], k);
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = (j * WG + t) * VEC;
-      if (e >= len || (a.inplace && !touch[j] && allow[j] == ALL)) continue;
-      if (!allow[j]) {
-        const uint32_t f = Tr<ET>::NEG_INF_WORD;
-        v[j] = u32x4{f, f, f, f};
-      } else {
-        if (touch[j]) {
-          float x[VEC];
-          uint64_t more = 0;  // drafted tokens: a byte per id of the vector
-          for (uint64_t m = path; m; m &= m - 1) {
-            const uint32_t d = (uint32_t)sh.local[__builtin_ctzll(m)] - (uint32_t)e;
-            if (d < (uint32_t)VEC) more += 1ull << (8 * d);
-          }
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            x[k] = Tr<ET>::at(v[j], k);
-            if (!((touch[j] >> k) & 1)) continue;
-            const uint32_t c = sh.count[e + k];
-            const uint32_t d = (uint32_t)(more >> (8 * k)) & 0xFFu;
-            const uint32_t n = (c & ~IN_PROMPT) + d;
-            if (c | d) x[k] = x[k] > 0.f ? x[k] / r : x[k] * r;
-            if (n) x[k] = (x[k] - freq * (float)n) - pres;
-            if (BIAS) {
-              const int at = sh.bias[e + k];
-              if (at) x[k] = x[k] + a.c.bias_values[b * a.c.bias_stride + at - 1];
-            }
-          }
-          Out<ET>::pack(v[j], x);
-        }
-        if (allow[j] != ALL) Out<ET>::cut(v[j], allow[j]);
-      }
-      if (e + VEC <= len) *reinterpret_cast<u32x4_u*>(dst + e) = v[j];
-      else {
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-          if (e + k < len) dst[e + k] = Out<ET>::one(v[j], k);
-      }
-    }
+    now = next;
   }
 }
 
@@ -329,10 +416,8 @@ extern "C" int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
   a.PG = (int)(groups >= GRID_WANTED ? 1 : (GRID_WANTED + groups - 1) / groups);
   if (a.PG > P) a.PG = P;
   if (groups * a.PG > INT32_MAX) return SV_ERR_UNSUPPORTED;
-  const bool bias = a.c.bias_ids && a.c.bias_stride > 0;
-  void (*const k)(AdjustArgs) =
-      dtype == SV_BF16 ? (bias ? adjust_logits_kernel<uint16_t, true> : adjust_logits_kernel<uint16_t, false>)
-                       : (bias ? adjust_logits_kernel<float, true> : adjust_logits_kernel<float, false>);
+  if (a.c.bias_stride <= 0) a.c.bias_ids = nullptr;
+  void (*const k)(AdjustArgs) = dtype == SV_BF16 ? adjust_logits_kernel<uint16_t> : adjust_logits_kernel<float>;
   (void)hipGetLastError();
   hipLaunchKernelGGL(k, dim3((uint32_t)(groups * a.PG)), dim3(WG), 0, stream, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
