@@ -570,10 +570,11 @@ typedef struct {
  * out          [B, T, H, D] bf16 contiguous.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
  *              not have.
- * workspace    at least *workspace_bytes bytes, 256-byte aligned; NULL asks for
- *              the size.  It need not be cleared.  Calls that overlap in time
- *              must use different workspaces.
- * Two kernels, three with weights.
+ * workspace, workspace_bytes  as spec_verify: zero-filled before its first use
+ *              with a given shape (B, T, H and Hkv, parents or not, weights or
+ *              not, and the cache's D, page, max_blocks), left ready for the
+ *              next call of that shape, not to be used by two calls at once.
+ * One kernel, two with weights.
  */
 int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
                           const void* k_new, const void* v_new, int64_t kv_row,

@@ -43,5 +43,6 @@ from .round_ops import (  # noqa: F401
     cache_attention,
     cache_commit,
     cache_evict,
+    new_attention_workspace,
     new_cache,
 )

@@ -12,8 +12,10 @@
 // belong to.  c is found on the device, from the rows' lengths, so that the
 // work-groups fill the chip once and get equal work.  The four waves take a segment's tiles in turn, each with a
 // softmax state of its own, without a barrier, and join at the segment's end.
-// The parts of a row that several work-groups hold are joined by a second
-// kernel.
+// The parts of a row that several work-groups hold are joined by the last of
+// them to arrive, in the order of the parts, so that the result does not
+// depend on who that is.  Parts go through write-through stores and counters
+// that are zero between calls (see sv_device.h).
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T, and tile rows
 // are dealt to the matrix instruction so that nothing is shuffled: lane
@@ -64,12 +66,13 @@ struct AttnArgs {
   float scale2;                // scale * log2(e)
   uint16_t* out;
   float* weights;
-  float* part_o;   // [parts][Hkv][mtiles][MT][D] sums of a part of a row, against its maximum
-  float2* part_ml; // [parts][Hkv][mtiles][MT] {m, l}
-  int2* info;      // [B][Hkv][mtiles] the row's first part and their count
+  unsigned* arrived; // [B][Hkv][mtiles] parts that are there; zero between calls
+  float* part_o;     // [parts][Hkv][mtiles][MT][D] sums of a part of a row, against its maximum
+  float* part_ml;    // [parts][Hkv][mtiles][MT][2] {m, l}
   float* lse;      // [B][Hkv][mtiles * MT] log2 of the softmax denominator
   float* mass;     // [B][Hkv][sub-blocks][mtiles * MT] log2 of a sub-block's sum
-  int sub;         // keys of a sub-block: min(page, 64)
+  int pshift;      // log2 page
+  int sshift;      // log2 of a sub-block's keys: min(page, 64)
   int nsub;        // sub-blocks of a row's table: max_blocks * page / sub
 };
 
@@ -130,7 +133,30 @@ __device__ __forceinline__ int scan(int v, int* sums, int& total) {
 // 8 XCDs in turn).  False past the last unit.  Every work-group does this for
 // itself: the lengths are on the device.
 template <int MT>
-__device__ __forceinline__ bool find_run(const AttnArgs& a, Run& out) {
+__device__ __forceinline__ bool find_run(const AttnArgs& a, Row* rows, Run& out) {
+  if (a.c.B <= 64 && a.mtiles == 1) {
+    // A row per lane, by every wave for itself: no barriers.
+    const int lane = threadIdx.x & 63;
+    Row x = {};
+    if (lane < a.c.B) x = row_of<MT>(a, lane);
+    if (threadIdx.x < 64) rows[lane] = x;
+    const int n = x.reps > 0 ? x.n : 0;
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += u;
+    }
+    const int total = __builtin_amdgcn_readlane(inc, 63);
+    const int c = max(CMIN, (total + a.even - 1) / a.even);
+    const int units = (total + c - 1) / c * a.c.Hkv, each = (units + 7) / 8;
+    const int unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= each || unit >= units) return false;
+    const int at = unit / a.c.Hkv * c;
+    const int b = __builtin_ctzll(__ballot(at < inc));
+    out = Run{b, __builtin_amdgcn_readlane(inc - n, b), at, min(at + c, total), c, unit % a.c.Hkv, 0};
+    return true;
+  }
   __shared__ int sums[NWAVE];
   __shared__ int lines[MAX_MTILES + 1];  // tiles of row tile mt's line
   __shared__ int place[2];
@@ -218,6 +244,16 @@ __device__ __forceinline__ bool find_run(const AttnArgs& a, Run& out) {
   __syncthreads();
   out = found;
   return true;
+}
+
+// Two neighbouring words published, and read, at once.
+__device__ __forceinline__ void pub_store2(float* p, float x, float y) {
+  const uint64_t v = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 pub_load2(const float* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
 // ---- lanes 16 and 32 apart --------------------------------------------------
@@ -327,7 +363,7 @@ __device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const floa
 
 constexpr int VPAD = 8;  // bf16 between the rows of the transposing buffer
 
-constexpr int ROWS = 64;  // rows of a run that are looked up at once
+constexpr int ROWS = 64;  // rows that are looked up at once
 
 template <int D, int NQ>
 struct Lds {
@@ -339,6 +375,7 @@ struct Lds {
   float m[NWAVE][MT], l[NWAVE][MT];
   uint64_t path[64];
   Row rows[ROWS];
+  int last;
 };
 
 // The codes of one 64-key tile in a wave's registers.
@@ -362,31 +399,29 @@ struct Loader {
 
   __device__ __forceinline__ int page_of(int group) const {
     if (group * 16 >= keys) return -1;
-    return table[group * 16 / a.c.page];
+    return table[group * 16 >> a.pshift];
   }
-  // Pages of the lane's K rows and of its V keys (and scales).
-  __device__ __forceinline__ int2 pages(int tile) const {
-    if (SMALL) return make_int2(page_of(tile * 4 + ((lane & 15) >> 2)), page_of(tile * 4 + g));
-    const int p = page_of(tile * 4);
-    return make_int2(p, p);
-  }
+  // Page of the lane's K rows.
+  __device__ __forceinline__ int pages(int tile) const { return page_of(tile * 4 + (SMALL ? (lane & 15) >> 2 : 0)); }
+  // Page of its V keys and of its scales: lanes 4 g .. 4 g + 3 have K rows of group g.
+  __device__ __forceinline__ int v_page(int pg) const { return SMALL ? __shfl(pg, g * 4, 64) : pg; }
   __device__ __forceinline__ int clamp(int p) const { return (uint32_t)p < (uint32_t)a.c.num_pages ? p : 0; }
-  __device__ __forceinline__ void load_k(Codes<D>& r, int tile, int2 pg) const {
+  __device__ __forceinline__ void load_k(Codes<D>& r, int tile, int pg) const {
     const int page = a.c.page, group = (lane & 15) >> 2;
-    const int in = (SMALL ? (group * 16) % page : (tile * 64) % page + group * 16) + (lane & 3);
-    const uint8_t* p = a.c.k_pages + (((int64_t)clamp(pg.x) * a.c.Hkv + h) * page + in) * D + g * 16;
+    const int in = (SMALL ? (group * 16) & (page - 1) : ((tile * 64) & (page - 1)) + group * 16) + (lane & 3);
+    const uint8_t* p = a.c.k_pages + (((int64_t)clamp(pg) * a.c.Hkv + h) * page + in) * D + g * 16;
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut)
 #pragma unroll
       for (int d = 0; d < D / 64; ++d) r.k[ut][d] = *reinterpret_cast<const u32x4*>(p + ut * 4 * D + d * 64);
-    const int64_t at = (int64_t)clamp(pg.y) * a.c.Hkv + h;
-    r.ks = a.c.k_scale[at];
-    r.ok = (uint32_t)pg.y < (uint32_t)a.c.num_pages;
+    const int mine = v_page(pg);
+    r.ks = a.c.k_scale[(int64_t)clamp(mine) * a.c.Hkv + h];
+    r.ok = (uint32_t)mine < (uint32_t)a.c.num_pages;
   }
-  __device__ __forceinline__ void load_v(Codes<D>& r, int tile, int2 pg) const {
+  __device__ __forceinline__ void load_v(Codes<D>& r, int tile, int pg) const {
     const int page = a.c.page;
-    const int in = SMALL ? (g * 16) % page : (tile * 64) % page + g * 16;
-    const int64_t at = (int64_t)clamp(pg.y) * a.c.Hkv + h;
+    const int in = SMALL ? (g * 16) & (page - 1) : ((tile * 64) & (page - 1)) + g * 16;
+    const int64_t at = (int64_t)clamp(v_page(pg)) * a.c.Hkv + h;
     const uint8_t* p = a.c.v_pages + (at * D + (lane & 15)) * page + in;
     if (!SMALL && a.mtiles == 1) {
 #pragma unroll
@@ -399,6 +434,16 @@ struct Loader {
     r.vs = a.c.v_scale[at];
   }
 };
+
+// The kernel's arguments read anew (they are its first and only parameter).
+// What only a late step needs is then not held in registers through the main
+// loop, where they are short.
+__device__ __forceinline__ const AttnArgs& args_again() {
+  typedef const AttnArgs __attribute__((address_space(4))) * KernArgs;
+  KernArgs p = (KernArgs)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs*)p;
+}
 
 template <int D>
 __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int h, int qr, int d, f32x4 x) {
@@ -414,9 +459,11 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   constexpr bool LATE = false;  // too few registers to hold a cached tile beside the new tokens
   __shared__ Lds<D, NQ> sh;
   Run run;
-  if (!find_run<MT>(a, run)) return;
+  if (!find_run<MT>(a, sh.rows, run)) return;
   const int h = run.h, mt = run.mt;
-  int b = run.b, begin = run.begin, at = run.at, base = b - ROWS;
+  // Rows base .. base + ROWS - 1 are looked up; find_run did so for few rows.
+  int b = run.b, begin = run.begin, at = run.at, base = a.c.B <= ROWS && a.mtiles == 1 ? 0 : b - ROWS;
+  __syncthreads();
 
   while (at < run.end) {
   // Made anew for each segment: what the compiler derives from them would
@@ -455,9 +502,9 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   int i = t0 + w;
   int i8 = i < row.near ? i + (row.near - i + NWAVE - 1) / NWAVE * NWAVE : i;
   Codes<D> r;
-  int2 next;
+  int next;
   if (i8 < t1) {
-    const int2 pg = ld.pages(i8 - row.near);
+    const int pg = ld.pages(i8 - row.near);
     ld.load_k(r, i8 - row.near, pg);
     ld.load_v(r, i8 - row.near, pg);
     next = ld.pages(min(i8 + NWAVE, t1 - 1) - row.near);
@@ -639,10 +686,10 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       }
       if (a.mass) {
         float z = psum;
-        if (a.sub > 16) z = sum16(z);
-        if (a.sub > 32) z = sum32(z);
-        const int at = (tile * 64 + g * 16) / a.sub;
-        if ((g * 16) % a.sub == 0 && tile * 64 + g * 16 < row.blocks * a.c.page)
+        if (a.sshift > 4) z = sum16(z);
+        if (a.sshift > 5) z = sum32(z);
+        const int at = (tile * 64 + g * 16) >> a.sshift;
+        if (((g * 16) & ((1 << a.sshift) - 1)) == 0 && tile * 64 + g * 16 < row.blocks * a.c.page)
           a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + at) * (a.mtiles * MT) + mt * MT + n * 16 + col] =
               st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
       }
@@ -676,11 +723,13 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     for (int dt = 0; dt < D / 16; ++dt)
       *reinterpret_cast<f32x4*>(&sh.o[w][(n * 16 + col) * (D + 4) + dt * 16 + g * 4]) = st.o[dt][n];
   __syncthreads();
-  const int64_t slot = (((int64_t)part * a.c.Hkv + h) * a.mtiles + mt) * MT;
-  const int64_t tile = ((int64_t)b * a.c.Hkv + h) * a.mtiles + mt;
-  if (t == 0 && part == part0) a.info[tile] = make_int2(part0, nparts);
+  const AttnArgs& z = args_again();
+  const int64_t step = (int64_t)z.c.Hkv * z.mtiles * MT, at0 = ((int64_t)h * z.mtiles + mt) * MT;
+  const int64_t slot = part * step + at0;
+  const int64_t tile = ((int64_t)b * z.c.Hkv + h) * z.mtiles + mt;
+  constexpr int V4 = MT * D / 4 / WG;  // float4 per thread
 #pragma unroll
-  for (int v = 0; v < MT * D / 4 / WG; ++v) {
+  for (int v = 0; v < V4; ++v) {
     const int e = v * WG + t, rr = e / (D / 4), d = e % (D / 4) * 4;
     float m = sh.m[0][rr], l = 0.f;
 #pragma unroll
@@ -693,66 +742,87 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       x += *reinterpret_cast<const f32x4*>(&sh.o[k][rr * (D + 4) + d]) * f;
     }
     if (nparts > 1) {
-      *reinterpret_cast<f32x4*>(a.part_o + (slot + rr) * D + d) = x;
-      if (d == 0) a.part_ml[slot + rr] = make_float2(m, l);
+      pub_store2(z.part_o + (slot + rr) * D + d, x[0], x[1]);
+      pub_store2(z.part_o + (slot + rr) * D + d + 2, x[2], x[3]);
+      if (d == 0) pub_store2(z.part_ml + (slot + rr) * 2, m, l);
     } else {
       const int qr = mt * MT + rr;
-      if (qr < nq * a.G) store_out<D>(a, b, h, qr, d, x * (1.f / l));
-      if (a.mass && d == 0) a.lse[tile * MT + rr] = m - UP + __builtin_amdgcn_logf(l);
+      if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x * (1.f / l));
+      if (z.mass && d == 0) z.lse[tile * MT + rr] = m - UP + __builtin_amdgcn_logf(l);
+    }
+  }
+  if (nparts > 1) {
+    wait_vmem();
+    __syncthreads();
+    if (t == 0) {
+      const unsigned n = __hip_atomic_fetch_add(z.arrived + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      sh.last = n == (unsigned)nparts - 1;
+      if (sh.last) __hip_atomic_store(z.arrived + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (sh.last) {
+      // Every part's {m, l}: thread (row, k) takes parts k, k + K, ...
+      constexpr int K = WG / MT;
+      const float* ml = z.part_ml + (part0 * step + at0) * 2;
+      const int r0 = t % MT, k0 = t / MT;
+      float m = NEG_INF, l = 0.f;
+      for (int s = k0; s < nparts; s += K) {
+        const float2 y = pub_load2(ml + (s * step + r0) * 2);
+        if (y.x == NEG_INF) continue;
+        const float big = fmaxf(m, y.x);
+        l = l * (m == NEG_INF ? 0.f : exp2_fast(m - big)) + y.y * exp2_fast(y.x - big);
+        m = big;
+      }
+      float2* ends = reinterpret_cast<float2*>(sh.o);  // [K][MT]; the sums have been taken
+      ends[k0 * MT + r0] = make_float2(m, l);
+      __syncthreads();
+      f32x4 x[V4];
+      float big[V4], sum[V4];
+#pragma unroll
+      for (int v = 0; v < V4; ++v) {
+        const int rr = (v * WG + t) / (D / 4);
+        big[v] = NEG_INF;
+        sum[v] = 0.f;
+        x[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) big[v] = fmaxf(big[v], ends[k * MT + rr].x);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          sum[v] += ends[k * MT + rr].x == NEG_INF ? 0.f : ends[k * MT + rr].y * exp2_fast(ends[k * MT + rr].x - big[v]);
+      }
+      // Parts whose loads go out at once: more make the largest state spill.
+      constexpr int J = SMALL && D * NQ == 256 ? 1 : 8 / V4;
+      const float* po = z.part_o + (part0 * step + at0) * D + t * 4;
+      for (int s0 = 0; s0 < nparts; s0 += J) {
+        float2 y[J][V4][2];
+        float f[J][V4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int64_t s = min(s0 + j, nparts - 1) * step;
+#pragma unroll
+          for (int v = 0; v < V4; ++v) {
+            y[j][v][0] = pub_load2(po + s * D + v * WG * 4);
+            y[j][v][1] = pub_load2(po + s * D + v * WG * 4 + 2);
+            f[j][v] = pub_load2(ml + (s + (v * WG + t) / (D / 4)) * 2).x;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int v = 0; v < V4; ++v) {
+            const float g4 = s0 + j >= nparts || f[j][v] == NEG_INF ? 0.f : exp2_fast(f[j][v] - big[v]);
+            x[v] += f32x4{y[j][v][0].x, y[j][v][0].y, y[j][v][1].x, y[j][v][1].y} * g4;
+          }
+      }
+#pragma unroll
+      for (int v = 0; v < V4; ++v) {
+        const int e = v * WG + t, rr = e / (D / 4), d = e % (D / 4) * 4, qr = mt * MT + rr;
+        if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x[v] * (1.f / sum[v]));
+        if (z.mass && d == 0) z.lse[tile * MT + rr] = big[v] - UP + __builtin_amdgcn_logf(sum[v]);
+      }
     }
   }
   __syncthreads();  // the shared arrays are free for the next segment
-  }
-}
-
-// Joins the parts of one row, kv head and 16 queries.
-template <int D, int NQ>
-__global__ __launch_bounds__(WG) void attention_combine_kernel(AttnArgs a) {
-  constexpr int MT = 16 * NQ;
-  extern __shared__ float fac[];  // [count][16]
-  __shared__ float2 part[16][16];
-  const int t = threadIdx.x;
-  const int n = blockIdx.x % NQ, unit = blockIdx.x / NQ;
-  const int mt = unit % a.mtiles, h = unit / a.mtiles % a.c.Hkv, b = unit / a.mtiles / a.c.Hkv;
-  const int r0 = mt * MT + n * 16, nq = query_len(a, b);
-  if (r0 >= nq * a.G) return;
-  const int2 sp = a.info[unit];
-  const int count = sp.y;
-  if (count < 2) return;
-  const int64_t first = ((int64_t)sp.x * a.c.Hkv + h) * a.mtiles + mt, step = (int64_t)a.c.Hkv * a.mtiles * MT;
-  const float2* ml = a.part_ml + first * MT + n * 16;
-  const float* po = a.part_o + (first * MT + n * 16) * D;
-  const int r = t & 15, k = t >> 4;
-  float m = NEG_INF, l = 0.f;
-  for (int s = k; s < count; s += 16) {
-    const float2 x = ml[s * step + r];
-    if (x.x == NEG_INF) continue;
-    const float big = fmaxf(m, x.x);
-    l = l * (m == NEG_INF ? 0.f : exp2_fast(m - big)) + x.y * exp2_fast(x.x - big);
-    m = big;
-  }
-  part[k][r] = make_float2(m, l);
-  __syncthreads();
-  m = NEG_INF;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) m = fmaxf(m, part[j][r].x);
-  l = 0.f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) l += part[j][r].x == NEG_INF ? 0.f : part[j][r].y * exp2_fast(part[j][r].x - m);
-  for (int s = k; s < count; s += 16) {
-    const float x = ml[s * step + r].x;
-    fac[s * 16 + r] = x == NEG_INF ? 0.f : exp2_fast(x - m) / l;
-  }
-  if (a.mass && k == 0) a.lse[((int64_t)b * a.c.Hkv + h) * (a.mtiles * MT) + r0 + r] = m - UP + __builtin_amdgcn_logf(l);
-  __syncthreads();
-  constexpr int V4 = 16 * D / 4 / WG;  // float4 per thread
-#pragma unroll
-  for (int v = 0; v < V4; ++v) {
-    const int e = (v * WG + t) * 4, row = e / D, d = e % D, qr = r0 + row;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int s = 0; s < count; ++s) x += *reinterpret_cast<const f32x4*>(po + s * step * D + e) * fac[s * 16 + row];
-    if (qr < nq * a.G) store_out<D>(a, b, h, qr, d, x);
   }
 }
 
@@ -767,7 +837,7 @@ __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int m
   if (b >= a.c.B || t >= query_len(a, b)) return;
   float x = 0.f;
   if (j < row_state(a.c, a.positions, a.blocks, b).blocks) {
-    const int per = a.c.page / a.sub;
+    const int per = a.c.page >> a.sshift;
     const float* lse = a.lse + (int64_t)b * a.c.Hkv * mpad + t * a.G;
     const float* mass = a.mass + ((int64_t)b * a.c.Hkv * a.nsub + (int64_t)j * per) * mpad + t * a.G;
     for (int s = 0; s < per; ++s)
@@ -785,8 +855,8 @@ __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int m
 }
 
 struct Plan {
-  int nq, mtiles, grid, runs, even, nsub, sub;
-  size_t o, ml, info, lse, mass, total;
+  int nq, mtiles, grid, runs, even, nsub;
+  size_t o, ml, lse, mass, total;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -801,7 +871,7 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   pl.mtiles = (M + mt - 1) / mt;
   const int64_t tiles = (int64_t)c.B * pl.mtiles, heads = tiles * c.Hkv;
   const int64_t most = ((int64_t)c.max_blocks * c.page + 63) / 64 + (c.page - 1 + T + 31) / 32;
-  if (most * tiles > INT_MAX || heads * pl.nq > INT_MAX) return SV_ERR_UNSUPPORTED;
+  if (most * tiles > INT_MAX || heads > INT_MAX) return SV_ERR_UNSUPPORTED;
   // Runs that the chip holds at once (see the kernel's registers).  Each row
   // tile's line may end with a part of a run, so the length of a run is
   // chosen for that many fewer (half of them where row tiles are many).
@@ -810,16 +880,14 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   pl.runs = (int)std::min<int64_t>(pl.even, (most * tiles + CMIN - 1) / CMIN) + pl.mtiles - 1;
   pl.grid = (pl.runs * c.Hkv + 7) / 8 * 8;
   const int64_t parts = ((int64_t)pl.runs + c.B) * c.Hkv * pl.mtiles;
-  pl.sub = std::min(c.page, 64);
-  const int64_t nsub = (int64_t)c.max_blocks * (c.page / pl.sub);
+  const int64_t nsub = (int64_t)c.max_blocks * (c.page / std::min(c.page, 64));
   pl.nsub = (int)nsub;
-  size_t off = 0;
+  // The counters come first: they are what must be zero.
+  size_t off = align256(sizeof(unsigned) * (size_t)heads);
   pl.o = off;
   off = align256(off + sizeof(float) * (size_t)parts * mt * c.D);
   pl.ml = off;
   off = align256(off + sizeof(float2) * (size_t)parts * mt);
-  pl.info = off;
-  off = align256(off + sizeof(int2) * (size_t)heads);
   if (weights) {
     const size_t rows = (size_t)c.B * c.Hkv, mpad = (size_t)pl.mtiles * mt;
     pl.lse = off;
@@ -837,9 +905,6 @@ int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
   void (*const k)(AttnArgs) =
       a.c.page < 64 ? cache_attention_kernel<KIND, D, NQ, true> : cache_attention_kernel<KIND, D, NQ, false>;
   hipLaunchKernelGGL(k, dim3(pl.grid), dim3(WG), 0, st, a);
-  if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
-  hipLaunchKernelGGL((attention_combine_kernel<D, NQ>), dim3(a.c.B * a.c.Hkv * a.mtiles * NQ), dim3(WG),
-                     (a.runs + 1) * 16 * sizeof(float), st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   if (a.weights) {
     const int64_t n = (int64_t)a.c.B * a.T * a.c.max_blocks;
@@ -917,12 +982,13 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   a.out = static_cast<uint16_t*>(out);
   a.weights = weights;
   char* ws = static_cast<char*>(workspace);
+  a.arrived = reinterpret_cast<unsigned*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + pl.o);
-  a.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
-  a.info = reinterpret_cast<int2*>(ws + pl.info);
+  a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
   a.lse = weights ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
   a.mass = weights ? reinterpret_cast<float*>(ws + pl.mass) : nullptr;
-  a.sub = pl.sub;
+  for (a.pshift = 4; 1 << a.pshift < c.page; ++a.pshift) {}
+  a.sshift = std::min(a.pshift, 6);
   a.nsub = pl.nsub;
   (void)hipGetLastError();
   return c.kind == SV_E4M3 ? launch_dim<SV_E4M3>(a, pl, stream) : launch_dim<SV_INT8>(a, pl, stream);

@@ -25,7 +25,7 @@ __device__ __forceinline__ RowState row_state(const sv_cache& c, const int32_t* 
   RowState s;
   s.blocks = min(max(blocks[b], 0), c.max_blocks);
   const int pos = max(positions[b], 0);
-  s.tail = pos % c.page;
+  s.tail = pos & (c.page - 1);
   s.start = (pos - s.tail) % c.tail;
   return s;
 }

@@ -12,8 +12,8 @@ import ctypes
 
 import torch
 
-from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, _check, _dtype_code, _OnStream, _stream_handle,
-                      load_library)
+from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, _cached_workspace, _check, _dtype_code,
+                      _OnStream, _stream_handle, load_library)
 
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
 
@@ -261,6 +261,11 @@ def attention_workspace_bytes(cache, T, H, *, tree=False, weights=False):
     return _attention_bytes(cache, T, H, tree, weights)
 
 
+def new_attention_workspace(cache, T, H, *, tree=False, weights=False):
+    """A zero-filled workspace for cache_attention at this shape."""
+    return torch.zeros(_attention_bytes(cache, T, H, tree, weights), dtype=torch.uint8, device=cache.device)
+
+
 def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, query_lens=None, scale=None,
                     weights=None, out=None, workspace=None, stream=None):
     """spec_verify_attention: attention of a round's new tokens over the cache
@@ -273,7 +278,9 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
     get every block's attention mass.
 
     Returns out [B, T, H, D], or (out, weights).  Tensors made here hold zeros
-    behind query_lens.
+    behind query_lens.  A call given no workspace uses one cached for its
+    shape, device and stream; under graph capture it makes and clears one that
+    belongs to the graph.
     """
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
@@ -304,7 +311,12 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
         else:
             _need("out", out, (B, T, H, D), torch.bfloat16, dev)
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            if torch.cuda.is_current_stream_capturing():
+                # a workspace of the graph's own, cleared in it: graphs replayed at once must not share one
+                workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+            else:
+                key = (B, T, H, cache.Hkv, D, cache.page, cache.max_blocks, parents is not None, weights is not None)
+                workspace = _cached_workspace("attention", key, need, dev, handle)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         n = ctypes.c_size_t(workspace.numel() * workspace.element_size())

@@ -228,8 +228,8 @@ def test_given_outputs_workspace_and_streams():
     q, kn, vn = views(qkv.cuda(), 4, 2)
     out = torch.full((3, 5, 4, 64), 7.0, dtype=BF16, device="cuda")
     w = torch.full((3, 5, cache.max_blocks), 7.0, device="cuda")
-    n = rsv.attention_workspace_bytes(cache, 5, 4, weights=True)
-    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")     # NaN everywhere: it needs no clearing
+    ws = rsv.new_attention_workspace(cache, 5, 4, weights=True)
+    assert ws.numel() == rsv.attention_workspace_bytes(cache, 5, 4, weights=True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
@@ -238,6 +238,32 @@ def test_given_outputs_workspace_and_streams():
     side.synchronize()
     assert got[0] is out and got[1] is w
     check(s, *views(qkv, 4, 2), out, w, query_lens=ql, fill=7.0)
+
+
+def test_a_workspace_serves_calls_of_its_shape_one_after_the_other():
+    """Lengths and idle rows change between calls; the counters come back to zero whatever the last call was."""
+    B, T, H, Hkv, D, page = 4, 3, 4, 1, 64, 64
+    ws = None
+    for i, (contexts, lens) in enumerate([([9000, 10, 0, 4000], None), ([100, 8000, 5000, 1], [3, 0, 2, 3]),
+                                          ([9999, 0, 9999, 77], [0, 0, 1, 3]), ([9000, 10, 0, 4000], None)]):
+        s = R.random_state(60 + i, B=B, Hkv=Hkv, D=D, page=page, kind="e4m3", contexts=contexts, max_blocks=160)
+        qkv = make_qkv(70 + i, B, T, H, Hkv, D)
+        lens = None if lens is None else torch.tensor(lens, dtype=torch.int32)
+        cache, _, _ = R.to_gpu(s)
+        ws = rsv.new_attention_workspace(cache, T, H, weights=True) if ws is None else ws
+        out, w = run(s, qkv, H, query_lens=lens, workspace=ws)
+        check(s, *views(qkv, H, Hkv), out, w, query_lens=lens)
+        assert not ws[:B * Hkv * 4].any()
+
+
+def test_many_query_heads_per_kv_head():
+    case(80, [70, 0, 5], 3, 256, 1, 64, 16, "e4m3")
+    case(81, [70, 200], 2, 400, 2, 128, 64, "int8", query_lens=[2, 1])
+
+
+def test_more_rows_than_a_wave_and_trees_of_all_sizes():
+    contexts = [(53 * b) % 300 for b in range(70)]
+    case(82, contexts, 33, 4, 2, 64, 16, "e4m3", tree=True, query_lens=[(7 * b) % 34 for b in range(70)])
 
 
 def test_graph_replays_follow_the_lengths():

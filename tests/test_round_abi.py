@@ -108,6 +108,7 @@ def test_attention_refuses(bad):
 def test_attention_limits_and_workspace():
     assert attention(T=B.SV_MAX_K + 2) == B.SV_ERR_UNSUPPORTED
     assert attention(T=B.SV_MAX_NODES + 1, parents=P[16]) == B.SV_ERR_UNSUPPORTED
+    assert attention(H=2 * 257) == B.SV_ERR_UNSUPPORTED
     rc, n = attention(ws=None)
     assert rc == B.SV_OK and n > 0 and n % 256 == 0
     rc, more = attention(ws=None, weights=P[16])
