@@ -10,8 +10,9 @@
 // tiles of all rows that have such queries stand in a line, and each
 // work-group takes a run of c of them for one kv head, whatever rows they
 // belong to.  c is found on the device, from the rows' lengths, so that the
-// work-groups fill the chip once and get equal work.  The four waves take a segment's tiles in turn, each with a
-// softmax state of its own, without a barrier, and join at the segment's end.
+// work-groups fill the chip once and get equal work.  The four waves take a
+// segment's tiles in turn, each with a softmax state and a part of LDS of its
+// own, without a barrier, and join at the segment's end.
 // The parts of a row that several work-groups hold are joined by the last of
 // them to arrive, in the order of the parts, so that the result does not
 // depend on who that is.  Parts go through write-through stores and counters
@@ -22,8 +23,9 @@
 // group g = lane / 16 holds, for query lane % 16, the scores of keys 16 g ..
 // 16 g + 15 of the tile, which is just the operand that O^T needs, and the
 // keys of one lane lie in one block (16 <= page), so a block's scales are a
-// factor per lane.  Codes go from memory to registers 16 bytes at a time
-// and are widened to bf16 there (exact for e4m3 and int8).
+// factor per lane.  Codes go from memory to LDS 16 bytes a lane and are
+// widened in the operands' registers, K's to bf16 and V's to f16 (both exact
+// for e4m3 and int8); the next tile's are on their way meanwhile.
 
 #include <algorithm>
 #include <cmath>
@@ -369,7 +371,13 @@ template <int D, int NQ>
 struct Lds {
   static constexpr int MT = 16 * NQ;
   union {
-    uint16_t v[NWAVE][32 * (D + VPAD)];  // a wave's 32 tail or new values
+    struct {
+      u32x4 k[4 * D];  // a wave's codes of a cached tile,
+      union {
+        u32x4 v[4 * D];
+        uint16_t near[32 * (D + VPAD)];  // or its 32 tail or new values
+      };
+    } wave[NWAVE];
     float o[NWAVE][MT * (D + 4)];        // joining: the waves' sums
   };
   float m[NWAVE][MT], l[NWAVE][MT];
@@ -387,12 +395,19 @@ struct Codes {
   bool ok;       // the lane's keys exist
 };
 
+// Brings a wave's tiles: from memory into its own part of LDS, in pieces of
+// 16 bytes with four neighbouring lanes 64 bytes side by side, and from there
+// into the operands' registers, where 16 lanes hold 16 keys.  Loads straight
+// into those registers take the vector cache four times the cycles, and can
+// begin only when the registers are free (trees of 64 nodes: 174 us against
+// 160; chains that read 623 MB: 139 against 120).
+// K has D / 16 pieces to a key, V four to a channel.  Piece p lies at place
+// p ^ twist, so that the eight lanes that LDS serves together differ in
+// their banks.
 // SMALL: page < 64, so the lane groups of a tile may lie in different pages.
-// V is read past the caches where whole lines of it are used once (64 or more
-// keys to a page, one row tile): 6.9 against 6.1 TB/s in a probe of this
-// pattern; a load instruction of K takes halves of lines, and needs them.
 template <int D, bool SMALL>
 struct Loader {
+  static constexpr int KP = D / 16;  // pieces of a key, and copies of 64 pieces, of K and of V
   const AttnArgs& a;
   const int32_t* table;
   int h, keys, g, lane;
@@ -401,37 +416,74 @@ struct Loader {
     if (group * 16 >= keys) return -1;
     return table[group * 16 >> a.pshift];
   }
-  // Page of the lane's K rows.
-  __device__ __forceinline__ int pages(int tile) const { return page_of(tile * 4 + (SMALL ? (lane & 15) >> 2 : 0)); }
-  // Page of its V keys and of its scales: lanes 4 g .. 4 g + 3 have K rows of group g.
-  __device__ __forceinline__ int v_page(int pg) const { return SMALL ? __shfl(pg, g * 4, 64) : pg; }
+  // The pages of a tile: lane l has that of 16-key group l / 16.
+  __device__ __forceinline__ int pages(int tile) const { return page_of(tile * 4 + (SMALL ? g : 0)); }
   __device__ __forceinline__ int clamp(int p) const { return (uint32_t)p < (uint32_t)a.c.num_pages ? p : 0; }
-  __device__ __forceinline__ void load_k(Codes<D>& r, int tile, int pg) const {
-    const int page = a.c.page, group = (lane & 15) >> 2;
-    const int in = (SMALL ? (group * 16) & (page - 1) : ((tile * 64) & (page - 1)) + group * 16) + (lane & 3);
-    const uint8_t* p = a.c.k_pages + (((int64_t)clamp(pg) * a.c.Hkv + h) * page + in) * D + g * 16;
+  __device__ __forceinline__ static int twist_k(int key) {
+    return KP == 8 ? (key & 3) | (key >> 4 & 1) << 2 : (key >> 1 & 1) | (key >> 4 & 1) << 1;
+  }
+  __device__ __forceinline__ static int twist_v(int d) { return d >> 1 & 3; }
+  template <int CPOL>
+  __device__ __forceinline__ static void bring(const uint8_t* from, u32x4* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, CPOL);
+  }
+  template <int CPOL>
+  __device__ __forceinline__ void copy_k(u32x4* to, int tile, int pg) const {
+    const int page = a.c.page, base = (tile * 64) & (page - 1);
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+      const int s = k * 64 + lane, key = s / KP, p = (s % KP) ^ twist_k(key);
+      const int own = __builtin_amdgcn_readlane(pg, SMALL ? k * 4 / KP * 16 : 0);
+      const int in = SMALL ? key & (page - 1) : key;
+      bring<CPOL>(a.c.k_pages + (((int64_t)clamp(own) * a.c.Hkv + h) * page + (SMALL ? 0 : base)) * D + (in * D + p * 16),
+                  to + k * 64);
+    }
+  }
+  template <int CPOL>
+  __device__ __forceinline__ void copy_v(u32x4* to, int tile, int pg) const {
+    const int page = a.c.page, base = (tile * 64) & (page - 1);
+    const int p = (lane & 3) ^ twist_v(lane / 4);
+    const int own = SMALL ? __shfl(pg, p * 16, 64) : __builtin_amdgcn_readfirstlane(pg);
+    const uint8_t* at = a.c.v_pages + ((int64_t)clamp(own) * a.c.Hkv + h) * D * page + (SMALL ? 0 : base);
+    const int in = lane / 4 * page + (SMALL ? (p * 16) & (page - 1) : p * 16);
+#pragma unroll
+    for (int k = 0; k < KP; ++k) bring<CPOL>(at + in + k * 16 * page, to + 64 * KP + k * 64);
+  }
+  __device__ __forceinline__ void scales(Codes<D>& r, int pg) const {
+    const int64_t at = (int64_t)clamp(pg) * a.c.Hkv + h;
+    r.ks = a.c.k_scale[at];
+    r.vs = a.c.v_scale[at];
+    r.ok = (uint32_t)pg < (uint32_t)a.c.num_pages;
+  }
+  // Past the caches (NT) where whole lines are used once: one row tile and,
+  // for V, no page in which 64 keys of a channel are half a line.  Chains
+  // that read 623 MB in pages of 64: 120 us with both past the caches, 125 with
+  // V alone, 136 with neither; 32 rows of 8192 tokens in pages of 128: 118 us
+  // with K alone, 138 with both.
+  static constexpr int NT = 2;
+  __device__ __forceinline__ void copy_k(u32x4* to, int tile, int pg) const {
+    if (a.mtiles == 1) copy_k<NT>(to, tile, pg);
+    else copy_k<0>(to, tile, pg);
+  }
+  __device__ __forceinline__ void copy_v(u32x4* to, int tile, int pg) const {
+    if (a.mtiles == 1 && a.c.page <= 64) copy_v<NT>(to, tile, pg);
+    else copy_v<0>(to, tile, pg);
+  }
+  __device__ __forceinline__ void take(Codes<D>& r, const u32x4* from) const {
+    const int col = lane & 15;
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut)
 #pragma unroll
-      for (int d = 0; d < D / 64; ++d) r.k[ut][d] = *reinterpret_cast<const u32x4*>(p + ut * 4 * D + d * 64);
-    const int mine = v_page(pg);
-    r.ks = a.c.k_scale[(int64_t)clamp(mine) * a.c.Hkv + h];
-    r.ok = (uint32_t)mine < (uint32_t)a.c.num_pages;
-  }
-  __device__ __forceinline__ void load_v(Codes<D>& r, int tile, int pg) const {
-    const int page = a.c.page;
-    const int in = SMALL ? (g * 16) & (page - 1) : ((tile * 64) & (page - 1)) + g * 16;
-    const int64_t at = (int64_t)clamp(v_page(pg)) * a.c.Hkv + h;
-    const uint8_t* p = a.c.v_pages + (at * D + (lane & 15)) * page + in;
-    if (!SMALL && a.mtiles == 1) {
+      for (int d = 0; d < D / 64; ++d) {
+        const int key = (col >> 2) * 16 + ut * 4 + (col & 3);
+        r.k[ut][d] = from[key * KP + ((d * 4 + g) ^ twist_k(key))];
+      }
 #pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt)
-        r.v[dt] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + dt * 16 * page));
-    } else {
-#pragma unroll
-      for (int dt = 0; dt < D / 16; ++dt) r.v[dt] = *reinterpret_cast<const u32x4*>(p + dt * 16 * page);
+    for (int dt = 0; dt < D / 16; ++dt) {
+      const int d = dt * 16 + col;
+      r.v[dt] = from[64 * KP + d * 4 + (g ^ twist_v(d))];
     }
-    r.vs = a.c.v_scale[at];
   }
 };
 
@@ -456,7 +508,6 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int h, int q
 template <int KIND, int D, int NQ, bool SMALL>
 __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RESIDENT))) void cache_attention_kernel(AttnArgs a) {
   constexpr int MT = 16 * NQ;
-  constexpr bool LATE = false;  // too few registers to hold a cached tile beside the new tokens
   __shared__ Lds<D, NQ> sh;
   Run run;
   if (!find_run<MT>(a, sh.rows, run)) return;
@@ -501,12 +552,15 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   const Loader<D, SMALL> ld{a, a.c.block_table + (int64_t)b * a.c.max_blocks, h, row.blocks * a.c.page, g, lane};
   int i = t0 + w;
   int i8 = i < row.near ? i + (row.near - i + NWAVE - 1) / NWAVE * NWAVE : i;
-  Codes<D> r;
-  int next;
+  Codes<D> r, ahead;
+  u32x4* const codes = sh.wave[w].k;
+  int next, first;
+  const bool has_near = i < min(t1, row.near);
   if (i8 < t1) {
-    const int pg = ld.pages(i8 - row.near);
-    ld.load_k(r, i8 - row.near, pg);
-    ld.load_v(r, i8 - row.near, pg);
+    first = ld.pages(i8 - row.near);
+    ld.copy_k(codes, i8 - row.near, first);
+    if (!has_near) ld.copy_v(codes, i8 - row.near, first);
+    ld.scales(ahead, first);
     next = ld.pages(min(i8 + NWAVE, t1 - 1) - row.near);
   }
 
@@ -575,7 +629,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
       for (int ks = 0; ks < D / 32; ++ks) kk[ut][ks] = *reinterpret_cast<const u32x4*>(p + (ks >> 1) * 64 + (ks & 1) * 8);
     }
-    uint16_t* vt = sh.v[w];
+    uint16_t* vt = sh.wave[w].near;
     constexpr int PER = D / 8;  // 16-byte pieces of a value
 #pragma unroll
     for (int e = 0; e < 32 * PER / 64; ++e) {
@@ -640,8 +694,36 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   }
 
   // ---- cached tiles ---------------------------------------------------------
+  if (has_near && i8 < t1) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values have left their place
+    ld.copy_v(codes, i8 - row.near, first);
+  }
+  // A tile's sums are written when the next one's loads are on their way, so
+  // that no wait for loads waits for these too.
+  float sums[NQ];
+  int told = -1;
+  auto tell = [&]() {
+    const int key = told * 64 + g * 16;
+    if (told >= 0 && (key & ((1 << a.sshift) - 1)) == 0 && key < row.blocks * a.c.page)
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+        a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + (key >> a.sshift)) * (a.mtiles * MT) + mt * MT + n * 16 + col] = sums[n];
+  };
   for (; i8 < t1; i8 += NWAVE) {
-    const int tile = i8 - row.near, in = min(i8 + NWAVE, t1 - 1) - row.near;  // the last tile is loaded again, not used
+    const int tile = i8 - row.near;
+    wait_vmem();  // the tile is in LDS
+    ld.take(r, codes);
+    r.ks = ahead.ks;
+    r.vs = ahead.vs;
+    r.ok = ahead.ok;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // and in registers: the next may come
+    if (a.mass) tell();
+    if (i8 + NWAVE < t1) {
+      ld.copy_k(codes, i8 + NWAVE - row.near, next);
+      ld.copy_v(codes, i8 + NWAVE - row.near, next);
+      ld.scales(ahead, next);
+      next = ld.pages(min(i8 + 2 * NWAVE, t1 - 1) - row.near);
+    }
     f32x4 s[4][NQ];
 #pragma unroll
     for (int ut = 0; ut < 4; ++ut)
@@ -669,7 +751,6 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         for (int n = 0; n < NQ; ++n)
           if (!ok) s[ut][n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    ld.load_k(r, in, next);
     f16x8 p8[2][NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -688,12 +769,10 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         float z = psum;
         if (a.sshift > 4) z = sum16(z);
         if (a.sshift > 5) z = sum32(z);
-        const int at = (tile * 64 + g * 16) >> a.sshift;
-        if (((g * 16) & ((1 << a.sshift) - 1)) == 0 && tile * 64 + g * 16 < row.blocks * a.c.page)
-          a.mass[(((int64_t)b * a.c.Hkv + h) * a.nsub + at) * (a.mtiles * MT) + mt * MT + n * 16 + col] =
-              st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
+        sums[n] = st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
       }
     }
+    told = tile;
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
@@ -703,10 +782,9 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         for (int n = 0; n < NQ; ++n)
           st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v8, p8[u][n], st.o[dt][n], 0, 0, 0);
       }
-    ld.load_v(r, in, next);
-    next = ld.pages(min(i8 + 2 * NWAVE, t1 - 1) - row.near);
   }
 
+  if (a.mass) tell();
   // ---- the four waves join ------------------------------------------------------
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
