@@ -397,9 +397,9 @@ int spec_verify_plan(int B, int K, int V, int topk_draft, int dtype,
 const char* spec_verify_status_string(int status);
 
 /* ------------------------------------------------------------------------
- * Operators around a verification round
+ * Operators around a verification step
  *
- * One round of a serving program: attention of the round's tokens (the last
+ * One step of a serving program: attention of the step's tokens (the last
  * committed token and its drafts: a chain or a tree) over the row's cache
  * (spec_verify_attention), the model's remaining layers, penalties, biases
  * and grammar masks on the logits that come of it
@@ -452,7 +452,7 @@ typedef struct {
 
 /*
  * spec_verify_adjust_logits - penalties for repeated tokens, biases and
- * grammar masks on the logits of every position of a round, before they are
+ * grammar masks on the logits of every position of a step, before they are
  * verified.
  *
  * Position i of row b follows the row's history and the drafted tokens
@@ -539,7 +539,7 @@ typedef struct {
 } sv_cache;
 
 /*
- * spec_verify_attention - attention of a round's T new tokens per row (the
+ * spec_verify_attention - attention of a step's T new tokens per row (the
  * last committed token's successor positions: the root and its drafts) over
  * the row's cache and over each other.
  *
@@ -595,7 +595,7 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
  * block table has in reserve, block_table[b][blocks[b]] first, and the
  * tokens after the last full block go to their slots of the tail ring.  The
  * tail's old tokens stay where they are and the counters are put out, so a
- * round can be undone by keeping the counters from before it.
+ * step can be undone by keeping the counters from before it.
  *
  * A block's scale is, with a the largest magnitude of its head's page * D
  * values: e4m3, the smallest power of two of at least a / 448; int8, a / 127

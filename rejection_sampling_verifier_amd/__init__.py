@@ -36,7 +36,7 @@ from .binding import (  # noqa: F401
     verify_tree,
     workspace_bytes,
 )
-from .round_ops import (  # noqa: F401
+from .serving_ops import (  # noqa: F401
     KVCache,
     adjust_logits,
     attention_workspace_bytes,

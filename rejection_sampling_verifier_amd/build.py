@@ -19,9 +19,9 @@ LIB = os.path.join(PKG, "libspecverify.so")
 # occupancy) of the last build, written next to the library.
 RESOURCES = os.path.join(PKG, "libspecverify.resources.txt")
 SOURCES = [os.path.join(PKG, "csrc", "spec_verify.hip")]
-# The operators around a verification round, one file each.
-ROUND_DIR = os.path.join(PKG, "csrc_round")
-ROUND_SOURCES = [os.path.join(ROUND_DIR, f) for f in sorted(os.listdir(ROUND_DIR)) if f.endswith(".hip")]
+# The operators around a verification step, one file each.
+SERVING_DIR = os.path.join(PKG, "csrc_serving")
+SERVING_SOURCES = [os.path.join(SERVING_DIR, f) for f in sorted(os.listdir(SERVING_DIR)) if f.endswith(".hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -54,7 +54,7 @@ def _run(cmd: list, verbose: bool) -> str:
 def build(verbose: bool = False) -> str:
     compile_flags = [f for f in FLAGS if f != "-shared"]
     with tempfile.TemporaryDirectory() as tmp:
-        sources = SOURCES + ROUND_SOURCES
+        sources = SOURCES + SERVING_SOURCES
         objects = [os.path.join(tmp, f"{i}.o") for i in range(len(sources))]
         with ThreadPoolExecutor(max_workers=4) as pool:
             reports = list(pool.map(lambda so: _run([HIPCC, *compile_flags, "-c", so[0], "-o", so[1]], verbose),

@@ -1,5 +1,5 @@
 // Penalties for repeated tokens, biases and grammar masks on the logits of a
-// verification round (spec_verify_adjust_logits), for gfx950.
+// verification step (spec_verify_adjust_logits), for gfx950.
 //
 // Mathematics: per logit at most one division or product, two subtractions
 // and one addition, on few tokens; every other logit is copied or set to

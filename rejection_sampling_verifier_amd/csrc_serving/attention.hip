@@ -1,4 +1,4 @@
-// Attention of a round's new tokens over the paged 8-bit cache, the bf16 tail
+// Attention of a step's new tokens over the paged 8-bit cache, the bf16 tail
 // and each other (spec_verify_attention), for gfx950.
 //
 // Mathematics: S = scale Q K^T, online softmax (running maximum m and sum l

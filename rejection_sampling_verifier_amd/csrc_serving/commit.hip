@@ -5,7 +5,7 @@
 // values, then code = round_half_even(x / scale).  A power-of-two scale makes
 // the e4m3 quotient exact; an int8 quotient is rounded from its float32
 // value and put right by the sign of x - (r +- 1/2) scale, which one fma
-// gives exactly.  Bytes bound it: few rows complete a block in a round, the
+// gives exactly.  Bytes bound it: few rows complete a block in a step, the
 // others copy n rows of D values; small batches are bound by latency.
 //
 // Three kinds of work-groups: one per (row, K or V) copies the committed

@@ -1,5 +1,5 @@
-"""Binding of the operators around a verification round (spec_verify.h, "Operators
-around a verification round"): torch tensors in, device pointers out.
+"""Binding of the operators around a verification step (spec_verify.h, "Operators
+around a verification step"): torch tensors in, device pointers out.
 
 As in ``binding``, every step runs in the library's HIP kernels, a call is
 enqueued on the current (or given) stream and nothing is synchronised.
@@ -106,7 +106,7 @@ def adjust_logits(logits, tokens=None, *, parents=None, history=None, history_le
                   repetition=None, presence=None, frequency=None, bias_ids=None, bias_values=None, bias_lens=None,
                   mask=None, mask_rows=None, out=None, stream=None):
     """spec_verify_adjust_logits: penalties, biases and grammar masks on the
-    logits of a round (see the header for the formulas).
+    logits of a step (see the header for the formulas).
 
     logits [B, P, V] bf16 or fp32 with contiguous rows (a slice of a padded
     vocabulary will do); tokens [B, >= P - 1] int32 of a chain, or [B, P] node
@@ -268,7 +268,7 @@ def new_attention_workspace(cache, T, H, *, tree=False, weights=False):
 
 def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, query_lens=None, scale=None,
                     weights=None, out=None, workspace=None, stream=None):
-    """spec_verify_attention: attention of a round's new tokens over the cache
+    """spec_verify_attention: attention of a step's new tokens over the cache
     and over each other (see the header).
 
     q [B, T, H, D], k_new and v_new [B, T, Hkv, D] bf16, views with D-sized

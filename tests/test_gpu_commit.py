@@ -82,7 +82,7 @@ def case(seed, contexts, num, T, Hkv, D, page, kind, tree=False, reserve=8, tota
     args = dict(nodes=dev(nodes), weights=dev(w), totals=dev(t))
     outs = rsv.cache_commit(cache, kvd[:, :, 0], kvd[:, :, 1], dev(num), positions, blocks, **args)
     check(s, kv, num, cache, outs, nodes, w, t)
-    # the counters before are untouched, and the same round again gives the same state (a round can be redone)
+    # the counters before are untouched, and the same step again gives the same state (a step can be redone)
     assert torch.equal(positions.cpu(), s["positions"]) and torch.equal(blocks.cpu(), s["blocks"])
     rsv.cache_commit(cache, kvd[:, :, 0], kvd[:, :, 1], dev(num), positions, blocks, **args)
     check(s, kv, num, cache, outs, nodes, w, t)
@@ -107,7 +107,7 @@ def test_pages_and_lengths(D, page, kind):
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("T", [1, 2, 17, 64])
 def test_up_to_the_longest_rounds(T, tree, kind):
-    """A round may complete several blocks; every row accepts another number."""
+    """A step may complete several blocks; every row accepts another number."""
     if T == 1 and tree:
         pytest.skip("a tree of the root alone is a chain of one token")
     case(2 + T, [15, 0, 40, 33], [T - 1, T // 2, 0, T - 1], T, 3, 64, 16, kind, tree=tree)

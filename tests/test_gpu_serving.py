@@ -1,5 +1,5 @@
-"""Whole serving rounds: attention over the cache, logits from its output, adjusted, verified, committed, evicted,
-round after round.  The reference follows the state from the accepted paths in float64."""
+"""Whole serving steps: attention over the cache, logits from its output, adjusted, verified, committed, evicted,
+step after step.  The reference follows the state from the accepted paths in float64."""
 
 from __future__ import annotations
 
@@ -19,7 +19,7 @@ BF16 = torch.bfloat16
 
 
 @pytest.mark.parametrize("kind, tree", [("e4m3", False), ("int8", True)])
-def test_rounds(kind, tree):
+def test_steps(kind, tree):
     B, T, H, Hkv, D, page, V, budget = 3, 7, 4, 2, 64, 16, 500, 3
     g = torch.Generator().manual_seed(5)
     cache = rsv.new_cache(B, B * 8, Hkv, D, page=page, max_blocks=8, max_new=T, kind=kind)

@@ -1,4 +1,4 @@
-"""Argument checks of the operators around a verification round, on the host:
+"""Argument checks of the operators around a verification step, on the host:
 every call here returns before it launches anything."""
 
 from __future__ import annotations
