@@ -363,6 +363,8 @@ __device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const floa
   st.l[n] += psum;
 }
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
 constexpr int VPAD = 8;  // bf16 between the rows of the transposing buffer
 
 constexpr int ROWS = 64;  // rows that are looked up at once
@@ -680,9 +682,13 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) {
-      union { uint16_t e[8]; bf16x8 v; } v8;
+      // Read transposed: of four keys' 16 channels, 4 in each of four lanes, a
+      // lane gets its channel of the four keys.
+      union { s16x4 e[2]; bf16x8 v; } v8;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v8.e[j] = vt[(g * 8 + j) * (D + VPAD) + dt * 16 + col];
+      for (int j = 0; j < 2; ++j)
+        v8.e[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+            vt + (g * 8 + j * 4 + (col >> 2)) * (D + VPAD) + dt * 16 + (col & 3) * 4));
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8.v, lo[n], st.o[dt][n], 0, 0, 0);
@@ -839,41 +845,20 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     }
     __syncthreads();
     if (sh.last) {
-      // Every part's {m, l}: thread (row, k) takes parts k, k + K, ...
-      constexpr int K = WG / MT;
+      // J parts' loads go out at once.
+      constexpr int J = 8 / V4;
       const float* ml = z.part_ml + (part0 * step + at0) * 2;
-      const int r0 = t % MT, k0 = t / MT;
-      float m = NEG_INF, l = 0.f;
-      for (int s = k0; s < nparts; s += K) {
-        const float2 y = pub_load2(ml + (s * step + r0) * 2);
-        if (y.x == NEG_INF) continue;
-        const float big = fmaxf(m, y.x);
-        l = l * (m == NEG_INF ? 0.f : exp2_fast(m - big)) + y.y * exp2_fast(y.x - big);
-        m = big;
-      }
-      float2* ends = reinterpret_cast<float2*>(sh.o);  // [K][MT]; the sums have been taken
-      ends[k0 * MT + r0] = make_float2(m, l);
-      __syncthreads();
+      const float* po = z.part_o + (part0 * step + at0) * D + t * 4;
       f32x4 x[V4];
       float big[V4], sum[V4];
 #pragma unroll
       for (int v = 0; v < V4; ++v) {
-        const int rr = (v * WG + t) / (D / 4);
         big[v] = NEG_INF;
         sum[v] = 0.f;
         x[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < K; ++k) big[v] = fmaxf(big[v], ends[k * MT + rr].x);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-          sum[v] += ends[k * MT + rr].x == NEG_INF ? 0.f : ends[k * MT + rr].y * exp2_fast(ends[k * MT + rr].x - big[v]);
       }
-      // Parts whose loads go out at once: more make the largest state spill.
-      constexpr int J = SMALL && D * NQ == 256 ? 1 : 8 / V4;
-      const float* po = z.part_o + (part0 * step + at0) * D + t * 4;
       for (int s0 = 0; s0 < nparts; s0 += J) {
-        float2 y[J][V4][2];
-        float f[J][V4];
+        float2 y[J][V4][2], e[J][V4];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           const int64_t s = min(s0 + j, nparts - 1) * step;
@@ -881,16 +866,25 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
           for (int v = 0; v < V4; ++v) {
             y[j][v][0] = pub_load2(po + s * D + v * WG * 4);
             y[j][v][1] = pub_load2(po + s * D + v * WG * 4 + 2);
-            f[j][v] = pub_load2(ml + (s + (v * WG + t) / (D / 4)) * 2).x;
+            e[j][v] = pub_load2(ml + (s + (v * WG + t) / (D / 4)) * 2);
           }
         }
 #pragma unroll
-        for (int j = 0; j < J; ++j)
+        for (int v = 0; v < V4; ++v) {
+          float top = big[v];
 #pragma unroll
-          for (int v = 0; v < V4; ++v) {
-            const float g4 = s0 + j >= nparts || f[j][v] == NEG_INF ? 0.f : exp2_fast(f[j][v] - big[v]);
-            x[v] += f32x4{y[j][v][0].x, y[j][v][0].y, y[j][v][1].x, y[j][v][1].y} * g4;
+          for (int j = 0; j < J; ++j) top = fmaxf(top, e[j][v].x);  // a part read twice is no other maximum
+          const float keep = big[v] == NEG_INF ? 0.f : exp2_fast(big[v] - top);
+          x[v] *= keep;
+          sum[v] *= keep;
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float f = s0 + j >= nparts || e[j][v].x == NEG_INF ? 0.f : exp2_fast(e[j][v].x - top);
+            sum[v] += e[j][v].y * f;
+            x[v] += f32x4{y[j][v][0].x, y[j][v][0].y, y[j][v][1].x, y[j][v][1].y} * f;
           }
+          big[v] = top;
+        }
       }
 #pragma unroll
       for (int v = 0; v < V4; ++v) {
