@@ -413,7 +413,8 @@ const char* spec_verify_status_string(int status);
  * The rules at the top of this file hold: device pointers owned by the
  * caller, no allocation, no synchronisation, kernels only on `stream`, whose
  * device must be the current one; device data is not validated, but every
- * memory access stays in bounds for any values in the arrays.
+ * memory access stays in bounds for any values in the arrays.  Rows and
+ * entries that a call's description leaves out are left as they were.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -550,6 +551,7 @@ typedef struct {
  * node).  With s = scale q.k over what it sees:
  *   out = sum softmax(s) v
  *   weights[b][t][j] = the softmax mass of block j, summed over the H heads
+ * What a query does not see does not reach it, infinities and NaN included.
  * Scores and softmax statistics are float32; q, the new tokens and the tail
  * enter as bf16 and the codes exactly; a probability (times its block's
  * v_scale) is rounded to 11 bits before its product with a code and to 16

@@ -633,12 +633,22 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     }
     uint16_t* vt = sh.wave[w].near;
     constexpr int PER = D / 8;  // 16-byte pieces of a value
+    uint32_t wild = 0;          // keys whose values are not all finite
 #pragma unroll
     for (int e = 0; e < 32 * PER / 64; ++e) {
       const int piece = e * 64 + lane, j = piece / PER, d = piece % PER * 8;
       u32x4 v = *reinterpret_cast<const u32x4*>(address(j0 + j, true) + d);
       if (j0 + j >= have) v = u32x4{0, 0, 0, 0};
       *reinterpret_cast<u32x4*>(vt + j * (D + VPAD) + d) = v;
+      // Its infinities and NaN (an exponent of ones carries into the sign's place).
+      uint32_t odd = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) odd |= (v[k] & 0x7F807F80u) + 0x00800080u;
+      const uint64_t lanes = __ballot((odd & 0x80008000u) != 0);
+      if (lanes)
+#pragma unroll
+        for (int k = 0; k < 64 / PER; ++k)
+          if (lanes >> (k * PER) & ((1ull << PER) - 1)) wild |= 1u << (e * 64 / PER + k);
     }
     f32x4 s[2][NQ];
 #pragma unroll
@@ -677,6 +687,31 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       }
       hi[n] = y.v;
       lo[n] = z.v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    // A product would take such an element to the queries that do not see it
+    // too (0 * inf): it leaves the tile, and is added to those that do.
+    while (wild) {
+      const int k = __builtin_ctz(wild), node = j0 + k - row.tail;
+      wild &= wild - 1;
+      bool see[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+        see[n] = a.parents ? (node < 0) | (bool)((sh.path[tok[n]] >> (node & 63)) & 1) : node <= tok[n];
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint16_t* e = vt + k * (D + VPAD) + dt * 16 + g * 4 + j;
+          const uint32_t v = *e;
+          if ((v & 0x7F80u) == 0x7F80u) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+              if (see[n]) st.o[dt][n][j] += __uint_as_float(v << 16);
+            *e = 0;  // by the 16 lanes that have read it
+          }
+        }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();

@@ -177,6 +177,32 @@ def test_every_code_is_its_value():
             assert torch.equal(out[b, 0, 0].cpu().double(), want), (kind, b)
 
 
+@pytest.mark.parametrize("H, Hkv, D, T", [(4, 2, 64, 12), (8, 2, 128, 40), (32, 2, 64, 9), (2, 2, 128, 5)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_infinities_and_nan_reach_only_the_queries_that_see_them(tree, H, Hkv, D, T):
+    contexts = [40, 0, 130, 700]
+    s = R.random_state(31, B=4, Hkv=Hkv, D=D, page=32, kind="e4m3", contexts=contexts)
+    qkv = make_qkv(32, 4, T, H, Hkv, D)
+    parents = random_parents(33, 4, T) if tree else None
+    v = qkv[:, :, H + Hkv:]
+    v[:, 2, 0, 3], v[:, 2, 0, D - 1], v[:, 2, 0, 17] = float("inf"), float("-inf"), float("nan")
+    v[:, T - 1, 1, :] = float("nan")
+    v[0, 1, 1, 8:12] = float("inf")
+    qkv[:, 4, H + 1, 5] = float("nan")                      # a key of the second head
+    s["v_tail"][2, int(R.tail_slots(s, 2, s["v_tail"].shape[1])[0]), 0, 9] = float("inf")
+    q, kn, vn = views(qkv, H, Hkv)
+    got = run(s, qkv, H, parents=parents, weights=None).cpu().double()
+    ref, _, av, smax = R.attention(s, q, kn, vn, D ** -0.5, parents)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)])
+    assert not torch.isinf(got[~torch.isinf(ref)]).any()
+    fine = torch.isfinite(ref)
+    assert fine[:, 0].sum() > H * D and not fine.all()
+    rel = 2 * (D + 4) * 2.0 ** -24 * smax + 2.0 ** -20
+    tol = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + rel[..., None]) * (1 + 2.0 ** -8) * av + 2.0 ** -99
+    assert ((got - ref).abs() <= tol)[fine].all()
+
+
 @pytest.mark.parametrize("which", ["k_scale", "v_scale"])
 def test_nan_scales_reach_every_query_that_sees_the_block(which):
     s = R.random_state(12, B=2, Hkv=2, D=64, page=16, kind="e4m3", contexts=[100, 100])
