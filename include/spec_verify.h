@@ -569,7 +569,8 @@ typedef struct {
  *              read, and in out and weights not written; a row of 0 is idle.
  * T in [1, SV_MAX_K + 1] ([1, SV_MAX_NODES] with parents), H a multiple of
  * Hkv (at most 256 times it), scale positive and finite.
- * out          [B, T, H, D] bf16 contiguous.
+ * out          [B, T, H, D] bf16 contiguous.  Neither it nor weights may
+ *              overlap the other or a row of q, k_new or v_new.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
  *              not have.
  * workspace, workspace_bytes  as spec_verify: zero-filled before its first use
@@ -616,7 +617,8 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
  * cache        with tail >= page - 1 + T.  No page may be in reserve for two
  *              rows.
  * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
- *              a second kernel updates them).
+ *              a second kernel updates them), but not overlap them or
+ *              num_accepted otherwise.
  * weights      [B, T, max_blocks] float32 (spec_verify_attention's) or NULL.
  * totals, totals_out [B, max_blocks] float32, both or none: totals_out[b][j]
  *              is totals[b][j] plus the weights of block j from the committed

@@ -1037,6 +1037,15 @@ int launch_dim(const AttnArgs& a, const Plan& pl, hipStream_t st) {
 
 }  // namespace
 
+// Whether any of `rows` stretches of `span` bytes, `stride` bytes apart, shares
+// a byte with the n at `out`.
+static bool crosses(const void* base, int64_t stride, int rows, int64_t span, const void* out, int64_t n) {
+  const int64_t d = reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(base);  // row k: k stride < d + n, d < k stride + span
+  if (stride == 0 || rows == 1) return 0 < d + n && d < span;
+  const int64_t first = d < span ? 0 : (d - span) / stride + 1;  // the first row that ends behind `out`'s start
+  return first < rows && first * stride < d + n;
+}
+
 extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok, const void* k_new, const void* v_new,
                                      int64_t kv_row, int64_t kv_tok, const sv_cache* cache, const int32_t* positions,
                                      const int32_t* blocks, const int32_t* parents, const int32_t* query_lens, int T,
@@ -1066,6 +1075,16 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   const int64_t strides[] = {q_row, q_tok, kv_row, kv_tok};
   for (int64_t s : strides)
     if (s < 0 || s > FAR || s % 8) return SV_ERR_ARG;
+  // The output is written while other work-groups still read.
+  const int64_t bytes = (int64_t)c.B * T * H * c.D * 2, mass = (int64_t)c.B * T * c.max_blocks * 4;
+  for (const void* p : {q, k_new, v_new}) {
+    const bool kv = p != q;
+    const int64_t row = (kv ? kv_row : q_row) * 2;
+    const int64_t span = ((T - 1) * (kv ? kv_tok : q_tok) + (int64_t)(kv ? c.Hkv : H) * c.D) * 2;
+    if (crosses(p, row, c.B, span, out, bytes) || (weights && crosses(p, row, c.B, span, weights, mass)))
+      return SV_ERR_ARG;
+  }
+  if (weights && crosses(weights, 0, 1, mass, out, bytes)) return SV_ERR_ARG;
   AttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.kn = static_cast<const uint16_t*>(k_new);

@@ -277,6 +277,7 @@ extern "C" int spec_verify_commit(const void* k_new, const void* v_new, int64_t 
   const size_t nb = (size_t)c.B * 4, nt = nb * c.max_blocks;
   if ((positions == positions_out) != (blocks == blocks_out) || overlap(positions_out, blocks_out, nb) ||
       overlap(positions, blocks_out, nb) || overlap(blocks, positions_out, nb) ||
+      overlap(num_accepted, positions_out, nb) || overlap(num_accepted, blocks_out, nb) ||
       (positions != positions_out && (overlap(positions, positions_out, nb) || overlap(blocks, blocks_out, nb))))
     return SV_ERR_ARG;
   if (totals && totals != totals_out && overlap(totals, totals_out, nt)) return SV_ERR_ARG;

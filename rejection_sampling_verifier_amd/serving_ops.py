@@ -182,7 +182,8 @@ class KVCache:
     uint8 codes, k_scale and v_scale [num_pages, Hkv] fp32, k_tail and v_tail
     [B, tail, Hkv, D] bf16, block_table [B, max_blocks] int32; kind "e4m3" or
     "int8".  A row's counters (positions, blocks) are passed to each call.
-    The handle keeps the tensors; their storage must not be replaced.
+    The handle keeps the tensors: copy into them, their storage must not be
+    replaced (another tensor in an attribute's place is refused).
     """
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale, k_tail, v_tail, block_table, *, kind="e4m3"):
@@ -211,6 +212,12 @@ class KVCache:
                           self.max_blocks, tail, _KINDS[kind])
         self._ref = ctypes.byref(self._c)
         self._sizes = {}  # workspace sizes by (T, H, parents, weights)
+        self._made = True
+
+    def __setattr__(self, name, value):
+        if "_made" in self.__dict__:
+            raise AttributeError(f"a KVCache keeps the tensors it was made of: copy into {name}, or make another")
+        super().__setattr__(name, value)
 
 
 def new_cache(B, num_pages, Hkv, D, page=64, max_blocks=None, max_new=SV_MAX_K + 1, kind="e4m3", device="cuda"):

@@ -320,6 +320,38 @@ def test_graph_replays_follow_the_lengths():
         assert torch.equal(out, eager[0]) and torch.equal(w, eager[1])
 
 
+def test_outputs_between_the_rows_that_are_read():
+    """One allocation: q's rows apart, the output in the gap between two of them; over a row it is refused."""
+    B, T, H, Hkv, D = 3, 2, 4, 2, 64
+    s = R.random_state(60, B=B, Hkv=Hkv, D=D, page=16, kind="int8", contexts=[20, 0, 300])
+    qkv = make_qkv(61, B, T, H, Hkv, D)
+    cache, positions, blocks = R.to_gpu(s)
+    _, kn, vn = views(qkv.cuda(), H, Hkv)
+    n, size = T * H * D, B * T * H * D
+    arena = torch.zeros((B * (n + size),), dtype=BF16, device="cuda")
+    q = arena.as_strided((B, T, H, D), (n + size, H * D, D, 1))
+    q.copy_(qkv[:, :, :H])
+    for row in range(B):
+        out = arena[row * (n + size) + n:][:size].view(B, T, H, D)
+        rsv.cache_attention(q, kn, vn, cache, positions, blocks, out=out)
+        check(s, *views(qkv, H, Hkv), out)
+        for at in (row * (n + size) + n - 8, (row + 1) * (n + size) - size + 8):
+            if row < B - 1 or at < row * (n + size) + n:
+                with pytest.raises(rsv.SpecVerifyError):
+                    rsv.cache_attention(q, kn, vn, cache, positions, blocks, out=arena[at:at + size].view(B, T, H, D))
+    with pytest.raises(rsv.SpecVerifyError):
+        rsv.cache_attention(q, kn, vn, cache, positions, blocks, out=arena[8:8 + size].view(B, T, H, D))
+
+
+def test_a_cache_keeps_its_tensors():
+    s = R.random_state(62, B=1, Hkv=1, D=64, page=16, kind="int8", contexts=[20])
+    cache, _, _ = R.to_gpu(s)
+    with pytest.raises(AttributeError):
+        cache.block_table = cache.block_table.clone()
+    with pytest.raises(AttributeError):
+        cache.page = 32
+
+
 def test_refusals_on_device_tensors():
     s = R.random_state(50, B=2, Hkv=2, D=64, page=16, kind="e4m3", contexts=[20, 40])
     cache, positions, blocks = R.to_gpu(s)

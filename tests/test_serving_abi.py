@@ -105,6 +105,21 @@ def test_attention_refuses(bad):
     assert attention(**bad) == B.SV_ERR_ARG
 
 
+ROW = 2 * 3 * 512               # bytes from one row of q, k_new and v_new to the next;
+QB, KB = 2048 + 512, 2048 + 256  # of a row that are read; of the outputs:
+OUT, WEIGHTS = 2 * 2 * 3 * 4 * 64, 2 * 3 * 10 * 4
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=P[10]), dict(out=P[10] + QB - 16), dict(out=P[10] + ROW + QB - 16), dict(out=P[10] + 16 - OUT),
+    dict(out=P[11]), dict(out=P[11] + KB - 16), dict(out=P[12] + ROW + KB - 16), dict(out=P[12] + 16 - OUT),
+    dict(q_row=0, out=P[10] + QB - 16), dict(weights=P[10]), dict(weights=P[12] + KB - 4),
+    dict(weights=P[11] + 4 - WEIGHTS), dict(weights=P[15]), dict(weights=P[15] + OUT - 4),
+    dict(weights=P[15] + 4 - WEIGHTS)])
+def test_attention_refuses_outputs_over_what_it_reads(bad):
+    assert attention(**bad) == B.SV_ERR_ARG
+
+
 def test_attention_limits_and_workspace():
     assert attention(T=B.SV_MAX_K + 2) == B.SV_ERR_UNSUPPORTED
     assert attention(T=B.SV_MAX_NODES + 1, parents=P[16]) == B.SV_ERR_UNSUPPORTED
@@ -149,6 +164,7 @@ def test_commit_refuses_unsupported_caches(bad):
     dict(positions_out=None), dict(blocks_out=None), dict(T=0), dict(kn=P[10] + 8), dict(kv_tok=4), dict(kv_row=-8),
     dict(positions_out=P[13]), dict(blocks_out=P[14]), dict(positions_out=P[16]), dict(positions_out=P[14]),
     dict(positions_out=P[13] + 4), dict(blocks_out=P[14] + 4), dict(nodes=P[17], stride=1),
+    dict(positions_out=P[12]), dict(blocks_out=P[12] - 4),
     dict(weights=P[18]), dict(totals=P[18]), dict(totals_out=P[18]), dict(totals=P[18], totals_out=P[18] + 40)])
 def test_commit_refuses(bad):
     assert commit(**bad) == B.SV_ERR_ARG
