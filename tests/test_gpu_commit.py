@@ -106,7 +106,7 @@ def test_pages_and_lengths(D, page, kind):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("T", [1, 2, 17, 64])
-def test_up_to_the_longest_rounds(T, tree, kind):
+def test_up_to_the_longest_steps(T, tree, kind):
     """A step may complete several blocks; every row accepts another number."""
     if T == 1 and tree:
         pytest.skip("a tree of the root alone is a chain of one token")
