@@ -515,7 +515,7 @@ typedef enum { SV_E4M3 = 0, SV_INT8 = 1 } sv_kind;
  *              side, as the matrix instructions take them
  * k_scale, v_scale [num_pages, Hkv] float32, positive (a NaN makes every
  *              output that sees the block NaN; attention takes a v_scale below
- *              2^-90 as 2^-90)
+ *              2^-126 as 2^-126)
  * k_tail, v_tail [B, tail, Hkv, D] bf16 rings: the row's token number p lies in
  *              slot p % tail.  tail is a multiple of page.
  * block_table  [B, max_blocks] int32: the page of each block; entries past a
@@ -553,10 +553,11 @@ typedef struct {
  *   weights[b][t][j] = the softmax mass of block j, summed over the H heads
  * What a query does not see does not reach it, infinities and NaN included.
  * Scores and softmax statistics are float32; q, the new tokens and the tail
- * enter as bf16 and the codes exactly; a probability (times its block's
- * v_scale) is rounded to 11 bits before its product with a code and to 16
- * before that with the tail's or a new token's value; the output is rounded
- * to bf16.
+ * enter as bf16 and the codes exactly, whatever their scales; a probability is
+ * rounded to 11 bits beside a code, or by at most 2^-21 of the largest one of
+ * its 64 cached keys (the row's keys 64 i .. 64 i + 63; 2^-16 where these are
+ * of several pages), and to 16 bits beside a tail or new token's value; what
+ * is 2^-100 of the largest may be lost; the output is rounded to bf16.
  *
  * q            element (b, t, h, d) at b * q_row + t * q_tok + h * D + d, bf16
  * k_new, v_new element (b, t, h, d) at b * kv_row + t * kv_tok + h * D + d,

@@ -49,8 +49,19 @@ constexpr int CMIN = 4;        // tiles of a run at least: one per wave
 // (16 rows of up to 16k tokens, one query each, D = 128: 76 against 83 us).
 constexpr int RESIDENT = 2;
 constexpr float GROW = 8.f;    // a maximum may lag this much (a factor of 256) before the sums are rescaled
-constexpr float UP = 6.f;      // probabilities are held 2^6 up: with GROW, f16 takes them from 2^14 down to 2^-24
-constexpr float VMIN = 0x1p-90f;  // smallest value scale told apart (see spec_verify.h)
+// Where f16 takes probabilities times value scales: a tile's largest of both
+// makes 2^(MID - HALF) to 2^(MID + HALF + 1), at most 2^15 and, as f16's
+// smallest step is 2^-24, a probability is off by at most 2^-21 of the
+// largest, where scales differ by a factor of 2^(ALIKE + 1) by 2^-16.
+constexpr float MID = 5.f, HALF = 9.f;
+// Tail and new tokens: 2^x that the sums take, so that 2^8 (GROW) times 320 of
+// them times the largest bf16 stay below 2^127.
+constexpr int NEAR_X = -18;
+constexpr float ALIKE = 4.f;   // value scales of one tile that differ by 2^5 and more need more range than f16 has
+constexpr float LOW = -110.f;  // scores further below the maximum count as this far, so that 2^x stays in float32's range
+constexpr float VMIN = 0x1p-126f;  // smallest value scale told apart (see spec_verify.h)
+constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
+constexpr int TOP = 100;       // sums are not raised above 2^TOP
 
 struct AttnArgs {
   const uint16_t* q;
@@ -327,39 +338,126 @@ __device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(b
 
 template <int D, int NQ>
 struct State {
-  f32x4 o[D / 16][NQ];  // O^T: lane (g, query) holds channels 16 dt + 4 g + r
+  f32x4 o[D / 16][NQ];  // O^T times 2^x: lane (g, query) holds channels 16 dt + 4 g + r
   float m[NQ], l[NQ];   // l: of the lane's own keys
+  int xs[(NQ + 1) / 2];  // x, two 16-bit numbers to a word: beside 64 queries every register counts
+
+  __device__ __forceinline__ int x(int n) const { return n & 1 ? xs[n / 2] >> 16 : (int)(int16_t)xs[n / 2]; }
+  __device__ __forceinline__ void set_x(int n, int v) {
+    xs[n / 2] = n & 1 ? (xs[n / 2] & 0xFFFF) | v << 16 : (xs[n / 2] & ~0xFFFF) | (v & 0xFFFF);
+  }
 };
 
-// A tile's softmax; the lane holds N scores of one query, raw, and their keys
-// share the factor c and the value scale 2^lv.  The running maximum m is that
-// of s c + lv, so the p = 2^(s c + lv - m + UP) that come out are the
-// probabilities times the value scale, and need no product with it; l takes
-// p / 2^lv.  any: the lane's keys exist.
-template <int D, int NQ, int N>
-__device__ __forceinline__ void softmax_tile(State<D, NQ>& st, int n, const float (&s)[N], float c, float lv,
-                                             float inv, bool any, float (&p)[N], float& psum) {
+// The running maximum follows mx, a tile's largest score.
+template <int D, int NQ>
+__device__ __forceinline__ float follow(State<D, NQ>& st, int n, float mx) {
+  const float m = fmaxf(st.m[n], mx);
+  const float f = m == NEG_INF ? 1.f : exp2_fast(st.m[n] - m);
+  st.m[n] = m;
+  st.l[n] *= f;
+  return f;
+}
+template <int D, int NQ>
+__device__ __forceinline__ bool lags(const State<D, NQ>& st, int n, float mx) {
+  return mx > st.m[n] + GROW;
+}
+
+// The softmax of a tile of tail and new tokens; the lane holds 8 scores of one
+// query, raw.  p: probabilities times 2^NEAR_X.
+template <int D, int NQ>
+__device__ __forceinline__ void softmax_near(State<D, NQ>& st, int n, const float (&s)[8], float c, float (&p)[8]) {
   float mx = s[0];
 #pragma unroll
-  for (int i = 1; i < N; ++i) mx = fmaxf(mx, s[i]);
-  mx = groups_max(any ? fmaf(mx, c, lv) : NEG_INF);
-  if (__any(mx > st.m[n] + GROW || (st.m[n] == NEG_INF && mx > NEG_INF))) {
-    const float m = fmaxf(st.m[n], mx);
-    const float f = m == NEG_INF ? 1.f : exp2_fast(st.m[n] - m);
-    st.m[n] = m;
-    st.l[n] *= f;
+  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
+  mx = groups_max(mx * c);
+  if (__any(lags(st, n, mx))) {
+    const float f = follow(st, n, mx);
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= f;
   }
-  const float off = any ? lv + UP - (st.m[n] == NEG_INF ? 0.f : st.m[n]) : NEG_INF;
-  const float k = any ? c : 0.f;
+  const float off = NEAR_X - fmaxf(st.m[n], -FAR);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p[i] = exp2_fast(fmaf(s[i], c, off));
+    sum += p[i];
+  }
+  st.l[n] = fmaf(sum, (float)(1 << -NEAR_X), st.l[n]);
+}
+
+// A block's value scale as 2^e f, 1 <= f < 2.
+struct ValueScale {
+  int e;
+  float log, inv;  // log2 f, 1 / f; -inf and 0 where there is no block
+};
+__device__ __forceinline__ ValueScale value_scale(float v, bool any) {
+  v = !any ? 1.f : v < VMIN ? VMIN : v;
+  const float f = 2.f * __builtin_amdgcn_frexp_mantf(v);
+  return {__builtin_amdgcn_frexp_expf(v) - 1, any ? __builtin_amdgcn_logf(f) : NEG_INF, any ? __builtin_amdgcn_rcpf(f) : 0.f};
+}
+
+// The softmax of a cached tile; the lane holds 16 scores of one query, raw,
+// whose keys share the factor c and the value scale v; top: the largest v.e
+// of the tile's.  any: the lane's keys exist.  p: probabilities times the
+// value scale times 2^x, or, where scales are unlike, times f alone; psum: the
+// sum of the probabilities.
+//
+// f16 has five bits of exponent, so x follows the tile's largest score and
+// scale (their product lies at 2^e before x), up and down, the float32 sums
+// with it, whatever the scales of the tiles before were.  x and the running
+// maximum move apart: a probability in the denominator does not depend on any
+// value scale.  They move seldom (18 binades of e are one x).  One maximum of
+// score and scale together costs less (32 trees of 61 nodes: 156 against 166
+// us; 64 chains over 8192 keys: 119 against 122) and loses every cached value
+// of a wave that is small beside its tail's or another block's.
+template <int D, int NQ>
+__device__ __forceinline__ void softmax_cached(State<D, NQ>& st, int n, const float (&s)[16], float c, const ValueScale& v,
+                                               float top, bool any, bool unlike, float (&p)[16], float& psum) {
+  float mx = s[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) mx = fmaxf(mx, s[i]);
+  mx = groups_max(any ? mx * c : NEG_INF);
+  auto off_range = [&]() { return fabsf(fmaxf(mx - st.m[n], LOW) + (top - MID + (float)st.x(n))) > HALF; };
+  // Plain bit operations: branches would part the tile's instructions.
+  if (__any(lags(st, n, mx) | off_range())) {
+    const bool fresh = __all(st.m[n] == NEG_INF);  // the sums are zero
+    float f = follow(st, n, mx);
+    const float e = fmaxf(mx - st.m[n], LOW) + top;
+    int dx = mx > NEG_INF && off_range() ? (int)rintf(MID - e) - st.x(n) : 0;
+    if (!fresh) {
+      if (__any(dx != 0)) {
+        float big = 0.f;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float y = fabsf(st.o[dt][n][r]);
+            big = fmaxf(big, y == __builtin_inff() ? 0.f : y);
+          }
+        big = groups_max(big);
+        if (big > 0.f) dx = min(dx, TOP - __builtin_amdgcn_frexp_expf(big));
+      }
+      int left = dx;
+      do {  // once, but between the ends of float32's range
+        const int step = min(max(left, -120), 120);
+        f = ldexpf(f, step);
+        left -= step;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= f;
+        f = 1.f;
+      } while (__any(left != 0));
+    }
+    st.set_x(n, st.x(n) + dx);
+  }
+  const int up = unlike ? 0 : v.e + st.x(n);
+  const float off = (float)up + v.log - fmaxf(st.m[n], -FAR);
   psum = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    p[i] = exp2_fast(fmaf(s[i], k, off));
+  for (int i = 0; i < 16; ++i) {
+    p[i] = exp2_fast(fmaf(s[i], c, off));
     psum += p[i];
   }
-  psum *= inv;
+  psum = ldexpf(psum * v.inv, -up);
   st.l[n] += psum;
 }
 
@@ -529,7 +627,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   if (b - base >= ROWS) {
     base = b;
     __syncthreads();  // idle rows are passed without one
-    if (t < ROWS && b + t < a.c.B) sh.rows[t] = row_of<MT>(a, b + t);
+    if (t < ROWS && b + t < a.c.B) sh.rows[t] = row_of<MT>(args_again(), b + t);
     __syncthreads();
   }
   Row row = sh.rows[b - base];
@@ -609,6 +707,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   for (int n = 0; n < NQ; ++n) {
     st.m[n] = NEG_INF;
     st.l[n] = 0.f;
+    st.set_x(n, NEAR_X);
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -665,7 +764,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     bf16x8 hi[NQ], lo[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float x[8], p[8], psum;
+      float x[8], p[8];
       // Seen: the tail (node < 0) and, of the new tokens, a chain's up to the
       // query's own or those of its path.  Plain bit operations: the compiler
       // made wrong code of the same condition written with branches.
@@ -677,7 +776,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         const bool see = (key < have) & ((node <= last) | (bool)((path >> (node & 63)) & 1));
         x[j] = see ? s[j >> 2][n][j & 3] : NEG_INF;
       }
-      softmax_tile<D, NQ, 8>(st, n, x, a.scale2, 0.f, 1.f, true, p, psum);
+      softmax_near(st, n, x, a.scale2, p);
       union { bf16x2 h[4]; bf16x8 v; } y, z;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -779,9 +878,15 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
         for (int n = 0; n < NQ; ++n) s[ut][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, q[n][ks], s[ut][n], 0, 0, 0);
       }
-    const float c = r.ks * a.scale2, vs = r.vs < VMIN ? VMIN : r.vs;
-    const float lv = __builtin_amdgcn_logf(vs), inv = __builtin_amdgcn_rcpf(vs);
     const bool ok = r.ok;
+    const float c = ok ? r.ks * a.scale2 : 0.f;
+    const ValueScale vs = value_scale(r.vs, ok);
+    bool unlike = false;
+    float top = (float)vs.e;
+    if (SMALL) {
+      top = groups_max(ok ? top : -150.f);
+      unlike = __any(ok & ((float)vs.e < top - ALIKE));
+    }
     if (!__all(ok)) {
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt)
@@ -798,7 +903,32 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       float x[16], p[16], psum;
 #pragma unroll
       for (int j = 0; j < 16; ++j) x[j] = s[j >> 2][n][j & 3];
-      softmax_tile<D, NQ, 16>(st, n, x, c, lv, ok ? inv : 0.f, ok, p, psum);
+      softmax_cached(st, n, x, c, vs, top, ok, unlike, p, psum);
+      if (unlike) {
+        // Blocks of small values beside some of large ones (or of zeros, whose
+        // scale is 1): bf16 pairs, which have float32's range.
+        const int up = vs.e + st.x(n);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          union { bf16x2 h[4]; bf16x8 v; } y, z;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x2 e = {ldexpf(p[8 * u + 2 * j], up), ldexpf(p[8 * u + 2 * j + 1], up)};
+            y.h[j] = __builtin_convertvector(e, bf16x2);
+            z.h[j] = __builtin_convertvector(e - __builtin_convertvector(y.h[j], f32x2), bf16x2);
+          }
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t w0 = r.v[dt][2 * u], w1 = r.v[dt][2 * u + 1];
+            asm volatile("" : "+v"(w0), "+v"(w1));  // widened here, and not kept for the next n
+            const bf16x8 v8 = widen<KIND>(w0, w1);
+            st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, z.v, st.o[dt][n], 0, 0, 0);
+            st.o[dt][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v8, y.v, st.o[dt][n], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) p[j] = 0.f;
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         union { f16x2 h[4]; f16x8 v; } y;
@@ -810,7 +940,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         float z = psum;
         if (a.sshift > 4) z = sum16(z);
         if (a.sshift > 5) z = sum32(z);
-        sums[n] = st.m[n] - UP + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
+        sums[n] = st.m[n] + __builtin_amdgcn_logf(z);  // -inf where the page does not exist
       }
     }
     told = tile;
@@ -827,9 +957,21 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 
   if (a.mass) tell();
   // ---- the four waves join ------------------------------------------------------
+  // Each wave, and each part, puts out a mean of values with the weight that
+  // the mean has, so that nothing passes float32's range on the way.
+  float whole[NQ];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const float l = groups_sum(st.l[n]);
+    whole[n] = l == 0.f ? 0.f : 1.f / l;
+    const int x = st.x(n);
+    if (__any((x < -80) | (x > 80))) {  // by two factors, each in float32's range
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= ldexpf(1.f, -x / 2);
+      whole[n] = ldexpf(whole[n], -x - -x / 2);
+    } else {
+      whole[n] = ldexpf(whole[n], -x);
+    }
     if (g == 0) {
       sh.m[w][n * 16 + col] = st.m[n];
       sh.l[w][n * 16 + col] = l;
@@ -840,7 +982,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   for (int n = 0; n < NQ; ++n)
 #pragma unroll
     for (int dt = 0; dt < D / 16; ++dt)
-      *reinterpret_cast<f32x4*>(&sh.o[w][(n * 16 + col) * (D + 4) + dt * 16 + g * 4]) = st.o[dt][n];
+      *reinterpret_cast<f32x4*>(&sh.o[w][(n * 16 + col) * (D + 4) + dt * 16 + g * 4]) = st.o[dt][n] * whole[n];
   __syncthreads();
   const AttnArgs& z = args_again();
   const int64_t step = (int64_t)z.c.Hkv * z.mtiles * MT, at0 = ((int64_t)h * z.mtiles + mt) * MT;
@@ -853,21 +995,25 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     float m = sh.m[0][rr], l = 0.f;
 #pragma unroll
     for (int k = 1; k < NWAVE; ++k) m = fmaxf(m, sh.m[k][rr]);
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    float f[NWAVE];
 #pragma unroll
     for (int k = 0; k < NWAVE; ++k) {
-      const float f = sh.m[k][rr] == NEG_INF ? 0.f : exp2_fast(sh.m[k][rr] - m);
-      l += sh.l[k][rr] * f;
-      x += *reinterpret_cast<const f32x4*>(&sh.o[k][rr * (D + 4) + d]) * f;
+      f[k] = sh.m[k][rr] == NEG_INF ? 0.f : sh.l[k][rr] * exp2_fast(sh.m[k][rr] - m);
+      l += f[k];
     }
+    // 0 times infinity, NaN, where every score is -inf; not before the last join.
+    const float whole = nparts > 1 && l == 0.f ? 0.f : 1.f / l;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NWAVE; ++k) x += *reinterpret_cast<const f32x4*>(&sh.o[k][rr * (D + 4) + d]) * (f[k] * whole);
     if (nparts > 1) {
       pub_store2(z.part_o + (slot + rr) * D + d, x[0], x[1]);
       pub_store2(z.part_o + (slot + rr) * D + d + 2, x[2], x[3]);
       if (d == 0) pub_store2(z.part_ml + (slot + rr) * 2, m, l);
     } else {
       const int qr = mt * MT + rr;
-      if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x * (1.f / l));
-      if (z.mass && d == 0) z.lse[tile * MT + rr] = m - UP + __builtin_amdgcn_logf(l);
+      if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x);
+      if (z.mass && d == 0) z.lse[tile * MT + rr] = m + __builtin_amdgcn_logf(l);
     }
   }
   if (nparts > 1) {
@@ -909,23 +1055,26 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
           float top = big[v];
 #pragma unroll
           for (int j = 0; j < J; ++j) top = fmaxf(top, e[j][v].x);  // a part read twice is no other maximum
-          const float keep = big[v] == NEG_INF ? 0.f : exp2_fast(big[v] - top);
-          x[v] *= keep;
-          sum[v] *= keep;
+          const float keep = big[v] == NEG_INF ? 0.f : sum[v] * exp2_fast(big[v] - top);
+          float f[J];
+          sum[v] = keep;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            const float f = s0 + j >= nparts || e[j][v].x == NEG_INF ? 0.f : exp2_fast(e[j][v].x - top);
-            sum[v] += e[j][v].y * f;
-            x[v] += f32x4{y[j][v][0].x, y[j][v][0].y, y[j][v][1].x, y[j][v][1].y} * f;
+            f[j] = s0 + j >= nparts || e[j][v].x == NEG_INF ? 0.f : e[j][v].y * exp2_fast(e[j][v].x - top);
+            sum[v] += f[j];
           }
+          const float whole = sum[v] == 0.f ? 0.f : 1.f / sum[v];
+          x[v] *= keep * whole;
+#pragma unroll
+          for (int j = 0; j < J; ++j) x[v] += f32x4{y[j][v][0].x, y[j][v][0].y, y[j][v][1].x, y[j][v][1].y} * (f[j] * whole);
           big[v] = top;
         }
       }
 #pragma unroll
       for (int v = 0; v < V4; ++v) {
         const int e = v * WG + t, rr = e / (D / 4), d = e % (D / 4) * 4, qr = mt * MT + rr;
-        if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x[v] * (1.f / sum[v]));
-        if (z.mass && d == 0) z.lse[tile * MT + rr] = big[v] - UP + __builtin_amdgcn_logf(sum[v]);
+        if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x[v] + 0.f * (1.f / sum[v]));
+        if (z.mass && d == 0) z.lse[tile * MT + rr] = big[v] + __builtin_amdgcn_logf(sum[v]);
       }
     }
   }
