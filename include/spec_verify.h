@@ -425,7 +425,8 @@ typedef struct {
   /* Tokens that count for the penalties: row b's are history[b *
    * history_stride + 0 .. history_lens[b]), of which the first
    * prompt_lens[b] are the prompt (prompt_lens NULL: none).  Lengths are
-   * taken as at least 0 and at most history_stride.  A token outside [0, V)
+   * taken as at least 0 and at most history_stride, or history_width (below)
+   * where that is not 0.  A token outside [0, V)
    * is ignored.  history may be NULL (no tokens but the drafted ones). */
   const int32_t* history;
   const int32_t* history_lens;
@@ -449,6 +450,9 @@ typedef struct {
   const uint32_t* mask;
   const int32_t* mask_rows;
   int num_masks;
+  /* Entries of a row's history that may be read, where rows lie further apart
+   * than they are long: in [0, history_stride]; 0 means history_stride. */
+  int64_t history_width;
 } sv_controls;
 
 /*

@@ -57,7 +57,7 @@ class SvControls(ctypes.Structure):
                 ("history_stride", ctypes.c_int64), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
                 ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
                 ("bias_lens", ctypes.c_void_p), ("bias_stride", ctypes.c_int64), ("mask", ctypes.c_void_p),
-                ("mask_rows", ctypes.c_void_p), ("num_masks", ctypes.c_int)]
+                ("mask_rows", ctypes.c_void_p), ("num_masks", ctypes.c_int), ("history_width", ctypes.c_int64)]
 
 
 class SvCache(ctypes.Structure):

@@ -212,7 +212,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
   if (t < 64 && sh.local[t] >= 0) atomicOr(&sh.touched[sh.local[t] >> 5], 1u << (sh.local[t] & 31));
   if (a.penalties && a.c.history) {
     const int32_t* h = a.c.history + b * a.c.history_stride;
-    const int n = (int)min((int64_t)max(a.c.history_lens[b], 0), a.c.history_stride);
+    const int n = (int)min((int64_t)max(a.c.history_lens[b], 0), a.c.history_width);
     const int np = a.c.prompt_lens ? max(a.c.prompt_lens[b], 0) : 0;
     auto take = [&](int tok, int j) {
       const uint32_t d = (uint32_t)tok - (uint32_t)lo;
@@ -394,7 +394,10 @@ extern "C" int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
   }
   a.penalties = a.c.repetition || a.c.presence || a.c.frequency;
   if (a.penalties) {
-    if (a.c.history && (!a.c.history_lens || a.c.history_stride < 0 || a.c.history_stride > INT32_MAX)) return SV_ERR_ARG;
+    if (a.c.history && (!a.c.history_lens || a.c.history_stride < 0 || a.c.history_stride > INT32_MAX ||
+                        a.c.history_width < 0 || a.c.history_width > a.c.history_stride))
+      return SV_ERR_ARG;
+    if (a.c.history_width == 0) a.c.history_width = a.c.history_stride;
     if (P > 1 && (!tokens || tokens_stride < (parents ? P : P - 1) || tokens_stride > INT32_MAX)) return SV_ERR_ARG;
   }
   if (a.c.bias_ids && (!a.c.bias_values || a.c.bias_stride < 0 || a.c.bias_stride > INT32_MAX - 1)) return SV_ERR_ARG;

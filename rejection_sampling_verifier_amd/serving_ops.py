@@ -140,12 +140,14 @@ def adjust_logits(logits, tokens=None, *, parents=None, history=None, history_le
         raise ValueError(f"tokens must hold at least {need} drafted tokens per row")
     _maybe("parents", parents, (B, P), i32, dev)
     if history is not None:
-        c.history_stride = _rows("history", history, B, i32, dev)
+        c.history_stride, c.history_width = _rows("history", history, B, i32, dev), history.shape[1]
         if history_lens is None:
             raise ValueError("history needs history_lens")
         _need("history_lens", history_lens, (B,), i32, dev)
         _maybe("prompt_lens", prompt_lens, (B,), i32, dev)
-        c.history, c.history_lens, c.prompt_lens = history.data_ptr(), history_lens.data_ptr(), _p(prompt_lens)
+        # an empty one is none: a width of 0 would mean the pitch
+        c.history = history.data_ptr() if history.shape[1] else None
+        c.history_lens, c.prompt_lens = history_lens.data_ptr(), _p(prompt_lens)
     if bias_ids is not None:
         _need("bias_ids", bias_ids, (B, None), i32, dev)
         _need("bias_values", bias_values, tuple(bias_ids.shape), f32, dev)
