@@ -6,7 +6,7 @@
 // -inf.  The call is bound by HBM: it reads and writes each logit once
 // (where a mask forbids all of a vector's tokens, it is not read).
 //
-// One work-group per (row, chunk of CH token ids, group of positions).  It
+// One work-group per (row, chunk of token ids, group of positions).  It
 // first counts the row's history inside its chunk: a direct-addressed table
 // of counts in LDS, built by integer atomics, so the order of the tokens
 // does not matter and there is nothing to sort or to clear in memory.  The
@@ -25,6 +25,14 @@
 // not counted in the table: a position's own are those of its path (a 64-bit
 // mask over the drafted tokens) that fall into the chunk, usually none or
 // one, so positions need no barrier between them.
+//
+// A token's bias is its last entry's: a bit per id and the bits' ranks give
+// each biased id a place in LDS, where a maximum over entry numbers settles
+// it once per work-group.  (A search of the chunk's entries by each listed id
+// at each position: 388 against 301 us with every control, 300 entries a row,
+// and 52.9 ms against 48 us with 20,000 entries side by side in 8 rows of 8
+// positions of 131,072 ids.)  Rows with more entries than places get chunks of
+// as many ids as there are places, which takes half of the lanes.
 
 #include <cstdint>
 
@@ -35,11 +43,11 @@ using namespace sv;
 
 namespace {
 
-constexpr int CH = 4096;                 // token ids per chunk
+constexpr int CH = 4096;                 // token ids per chunk at most
 constexpr int GRID_WANTED = 1024;        // work-groups that fill the chip; below, positions are split too
 constexpr uint32_t IN_PROMPT = 1u << 31; // table entry: occurs in the prompt;
 constexpr uint32_t BIASED = 1u << 30;    // has a bias; the rest counts n(x)
-constexpr int BIASES = 1024;             // bias entries of a chunk that LDS holds
+constexpr int BIASES = 2048;             // biased ids of a chunk that LDS holds; rows with more entries get chunks of so many
 
 struct AdjustArgs {
   const void* in;
@@ -50,6 +58,7 @@ struct AdjustArgs {
   int64_t tokens_stride;
   sv_controls c;
   int P, V, C, PG;  // positions, ids, chunks, position groups
+  int chunk;        // ids of a chunk
   int words;        // words of a mask row
   int penalties, inplace;
 };
@@ -95,9 +104,12 @@ struct Tables {
   uint32_t touched[CH / 32];
   int before[CH / 32 + 1];      // listed ids before each word of `touched`
   uint16_t list[CH];
-  uint16_t bias_at[BIASES];     // bias entries in the chunk: place and number
-  int bias_no[BIASES];
-  int biases;
+  uint32_t biased[CH / 32];
+  int rank[CH / 32 + 1];        // biased ids before each word of `biased`
+  union {                       // of each biased id, in order: 1 + its last entry, then
+    int entry[BIASES];
+    float bias[BIASES];         // that entry's value
+  };
   int local[64];                // drafted tokens' places in the chunk
   uint64_t path[64];            // tree: nodes on the path root .. v
   uint64_t here[CH / 256];      // drafted tokens inside each window of a wave's 64 vectors
@@ -144,7 +156,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
   const int pg = blockIdx.x % a.PG;
   const int chunk = (blockIdx.x / a.PG) % a.C;
   const int b = blockIdx.x / a.PG / a.C;
-  const int lo = chunk * CH, len = min(CH, a.V - lo);
+  const int lo = chunk * a.chunk, len = min(a.chunk, a.V - lo);
 
   constexpr uint32_t ALL = (1u << VEC) - 1;
   const int p0 = (int)((int64_t)a.P * pg / a.PG), p1 = (int)((int64_t)a.P * (pg + 1) / a.PG);
@@ -191,8 +203,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
   if (!a.inplace) fetch(now, p0);
 
   for (int i = t; i < CH / 4; i += WG) reinterpret_cast<u32x4*>(sh.count)[i] = u32x4{0, 0, 0, 0};
-  if (t < CH / 32) sh.touched[t] = 0;
-  if (t == 0) sh.biases = 0;
+  if (t < CH / 32) sh.touched[t] = sh.biased[t] = 0;
   const int drafted = a.penalties && a.tokens ? (a.parents ? a.P : a.P - 1) : 0;
   if (t < 64) {
     int at = -1;
@@ -244,30 +255,41 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
     if (d < (uint32_t)len) {
       atomicOr(&sh.count[d], BIASED);
       atomicOr(&sh.touched[d >> 5], 1u << (d & 31));
-      const int k = atomicAdd(&sh.biases, 1);  // in any order: the search below takes the last entry by its number
-      if (k < BIASES) {
-        sh.bias_at[k] = (uint16_t)d;
-        sh.bias_no[k] = e;
-      }
+      atomicOr(&sh.biased[d >> 5], 1u << (d & 31));
     }
   }
+  if (nbias > 0)
+    for (int k = t; k < BIASES; k += WG) sh.entry[k] = 0;
   __syncthreads();
 
-  // The list of touched ids.
-  if (t < 64) {
-    const uint32_t w0 = sh.touched[2 * t], w1 = sh.touched[2 * t + 1];
+  // The places of touched ids in their list, and of biased ones in theirs, by
+  // a wave each.
+  if (t < 128) {
+    const uint32_t* bits = t < 64 ? sh.touched : sh.biased;
+    int* before = t < 64 ? sh.before : sh.rank;
+    const uint32_t w0 = bits[2 * lane], w1 = bits[2 * lane + 1];
     const int n0 = __popc(w0), n = n0 + __popc(w1);
     int inc = n;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int u = __shfl_up(inc, o, 64);
-      if (t >= o) inc += u;
+      if (lane >= o) inc += u;
     }
-    sh.before[2 * t] = inc - n;
-    sh.before[2 * t + 1] = inc - n + n0;
-    if (t == 63) sh.before[128] = inc;
+    before[2 * lane] = inc - n;
+    before[2 * lane + 1] = inc - n + n0;
+    if (lane == 63) before[128] = inc;
   }
   __syncthreads();
+  auto bias_place = [&](int d) { return sh.rank[d >> 5] + __popc(sh.biased[d >> 5] & ((1u << (d & 31)) - 1)); };
+  if (nbias > 0) {
+    // A token's last entry counts, whatever order they come in here.
+    for (int e = t; e < nbias; e += WG) {
+      const uint32_t d = (uint32_t)bias_ids[e] - (uint32_t)lo;
+      if (d < (uint32_t)len) atomicMax(&sh.entry[bias_place(d)], e + 1);
+    }
+    __syncthreads();
+    for (int k = t; k < sh.rank[CH / 32]; k += WG) sh.bias[k] = bias_values[sh.entry[k] - 1];
+  }
   if (t < CH / 32) {
     int k = sh.before[t];
     for (uint32_t m = sh.touched[t]; m; m &= m - 1) sh.list[k++] = (uint16_t)(t * 32 + __ffs(m) - 1);
@@ -290,7 +312,6 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
     k1[j] = __builtin_amdgcn_readfirstlane(sh.before[win / 32 + 2 * VEC]);
     here[j] = sh.here[win / (64 * VEC)];
   }
-  const int nb = sh.biases;
   // Listed id d's logit; path: the position's drafted tokens near it.
   auto adjusted = [&](float x, int d, uint64_t path) {
     const uint32_t c = sh.count[d];
@@ -298,17 +319,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
     for (uint64_t m = path; m; m &= m - 1) n += sh.local[__builtin_ctzll(m)] == d;
     if (n | (c & IN_PROMPT)) x = x > 0.f ? x / r : x * r;
     if (n) x = (x - freq * (float)n) - pres;
-    if (c & BIASED) {
-      int last = -1;
-      if (nb <= BIASES) {
-        for (int k = 0; k < nb; ++k)
-          if (sh.bias_at[k] == d) last = max(last, sh.bias_no[k]);
-      } else {
-        for (int k = 0; k < nbias; ++k)
-          if (bias_ids[k] == lo + d) last = k;
-      }
-      x = x + bias_values[last];
-    }
+    if (c & BIASED) x = x + sh.bias[bias_place(d)];
     return x;
   };
 
@@ -413,7 +424,8 @@ extern "C" int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
   a.tokens_stride = tokens_stride;
   a.P = P;
   a.V = V;
-  a.C = (V - 1) / CH + 1;
+  a.chunk = a.c.bias_ids && a.c.bias_stride > BIASES ? BIASES : CH;
+  a.C = (V - 1) / a.chunk + 1;
   a.words = (V - 1) / 32 + 1;
   const int64_t groups = (int64_t)B * a.C;
   a.PG = (int)(groups >= GRID_WANTED ? 1 : (GRID_WANTED + groups - 1) / groups);

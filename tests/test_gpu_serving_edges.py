@@ -24,3 +24,40 @@ def test_lengths_beyond_a_view_of_a_wider_history(first, width):
     x["history_lens"] = torch.tensor([64, width + 1, 2 ** 31 - 1], dtype=torch.int32).cuda()
     x["prompt_lens"] = None
     A.check(logits, x, rsv.adjust_logits(logits, **x))
+
+
+def last_entries(ids, values, V):
+    """Each token's last entry, by numpy's own order of assignment."""
+    out = torch.zeros(V, dtype=torch.float64)
+    seen = torch.zeros(V, dtype=torch.bool)
+    for x, v in zip(ids.tolist(), values.tolist()):
+        if 0 <= x < V:
+            out[x], seen[x] = v, True
+    return out, seen
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("V, entries, spread", [(9000, 1500, 4000), (9000, 2048, 9000), (9000, 2049, 2049),
+                                                (9000, 9000, 9000), (4099, 20000, 4099), (5003, 3000, 7)])
+def test_dense_biases(V, entries, spread, dtype):
+    """Many biased ids side by side, and repeated ones: the last entry of each counts."""
+    g = torch.Generator().manual_seed(72)
+    B, P = 2, 5
+    first = (V - spread) // 2
+    ids = first + torch.randint(0, spread, (B, entries), generator=g, dtype=torch.int32)
+    if entries == V:
+        ids = torch.stack([torch.randperm(V, generator=g, dtype=torch.int32) for _ in range(B)])
+    values = torch.randn((B, entries), generator=g)
+    lens = torch.tensor([entries, entries - 700], dtype=torch.int32)
+    logits = torch.randn((B, P, V), generator=g).to(dtype)
+    got = rsv.adjust_logits(logits.cuda(), bias_ids=ids.cuda(), bias_values=values.cuda(), bias_lens=lens.cuda()).cpu()
+    inplace = logits.cuda()
+    rsv.adjust_logits(inplace, bias_ids=ids.cuda(), bias_values=values.cuda(), bias_lens=lens.cuda(), out=inplace)
+    assert torch.equal(inplace.cpu(), got)
+    for b in range(B):
+        add, seen = last_entries(ids[b, :lens[b]], values[b, :lens[b]], V)
+        ref = logits[b].double() + add
+        # one float32 sum, 2^-24 of it, and the output's half step
+        tol = (ref.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -24)) * (1 + 2.0 ** -20)
+        assert ((got[b].double() - ref).abs() <= tol)[:, seen].all()
+        assert torch.equal(got[b][:, ~seen], logits[b][:, ~seen])
