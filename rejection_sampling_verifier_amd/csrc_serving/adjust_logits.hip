@@ -29,7 +29,7 @@
 // A token's bias is its last entry's: a bit per id and the bits' ranks give
 // each biased id a place in LDS, where a maximum over entry numbers settles
 // it once per work-group.  (A search of the chunk's entries by each listed id
-// at each position: 388 against 301 us with every control, 300 entries a row,
+// at each position: 388 against 306 us with every control, 300 entries a row,
 // and 52.9 ms against 48 us with 20,000 entries side by side in 8 rows of 8
 // positions of 131,072 ids.)  Rows with more entries than places get chunks of
 // as many ids as there are places, which takes half of the lanes.
@@ -312,15 +312,20 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
     k1[j] = __builtin_amdgcn_readfirstlane(sh.before[win / 32 + 2 * VEC]);
     here[j] = sh.here[win / (64 * VEC)];
   }
-  // Listed id d's logit; path: the position's drafted tokens near it.
-  auto adjusted = [&](float x, int d, uint64_t path) {
+  // Changes listed id d's logit, where something applies to it (a NaN's bits
+  // would not pass through the conversions); path: the position's drafted
+  // tokens near it.
+  const uint32_t applies = BIASED | (a.c.repetition ? IN_PROMPT : 0);
+  auto adjust = [&](ET& logit, int d, uint64_t path) {
     const uint32_t c = sh.count[d];
     uint32_t n = c & ~(IN_PROMPT | BIASED);
     for (uint64_t m = path; m; m &= m - 1) n += sh.local[__builtin_ctzll(m)] == d;
+    if (!(n | (c & applies))) return;
+    float x = Out<ET>::widen(logit);
     if (n | (c & IN_PROMPT)) x = x > 0.f ? x / r : x * r;
     if (n) x = (x - freq * (float)n) - pres;
     if (c & BIASED) x = x + sh.bias[bias_place(d)];
-    return x;
+    logit = Out<ET>::narrow(x);
   };
 
   if (a.inplace) fetch(now, p0);
@@ -345,7 +350,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void ad
           __builtin_amdgcn_wave_barrier();
           for (int k = k0[j] + lane; k < k1[j]; k += 64) {
             const int d = sh.list[k];
-            stage[d - win] = Out<ET>::narrow(adjusted(Out<ET>::widen(stage[d - win]), d, on));
+            adjust(stage[d - win], d, on);
           }
           __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
           __builtin_amdgcn_wave_barrier();

@@ -61,3 +61,22 @@ def test_dense_biases(V, entries, spread, dtype):
         tol = (ref.abs() * (torch.finfo(dtype).eps / 2 + 2.0 ** -24)) * (1 + 2.0 ** -20)
         assert ((got[b].double() - ref).abs() <= tol)[:, seen].all()
         assert torch.equal(got[b][:, ~seen], logits[b][:, ~seen])
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("dtype, word, bits", [(BF16, torch.int16, 0x7F81), (torch.float32, torch.int32, 0x7F800001)])
+def test_listed_logits_that_nothing_applies_to_keep_their_bits(dtype, word, bits, inplace):
+    """A drafted token before its own position, and a prompt token without a repetition penalty: signalling NaN."""
+    B, P, V = 1, 4, 300
+    logits = torch.randn((B, P, V), generator=torch.Generator().manual_seed(73)).to(dtype)
+    logits.view(word)[..., [5, 9, 40]] = bits
+    want = logits.clone()
+    logits = logits.cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    got = rsv.adjust_logits(logits, i32([[7, 5, 9]]), history=i32([[40, 41]]), history_lens=i32([2]), prompt_lens=i32([2]),
+                            presence=torch.ones(1, device="cuda"), out=logits if inplace else None).cpu()
+    same = torch.ones((B, P, V), dtype=torch.bool)
+    for i, t in ((1, 7), (2, 7), (2, 5), (3, 7), (3, 5), (3, 9)):
+        same[0, i, t] = False
+        assert float(want[0, i, t]) - 1 == pytest.approx(float(got[0, i, t]), rel=2 ** -7, nan_ok=True)
+    assert torch.equal(got.view(word)[same], want.view(word)[same])
