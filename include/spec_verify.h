@@ -578,10 +578,12 @@ typedef struct {
  *              overlap the other or a row of q, k_new or v_new.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
  *              not have.
- * workspace, workspace_bytes  as spec_verify: zero-filled before its first use
- *              with a given shape (B, T, H and Hkv, parents or not, weights or
- *              not, and the cache's D, page, max_blocks), left ready for the
- *              next call of that shape, not to be used by two calls at once.
+ * workspace, workspace_bytes  as spec_verify, but only its first 4 * B * Hkv *
+ *              ceil(T * H / Hkv / 16) bytes need to be zero-filled before its
+ *              first use with a given shape (B, T, H and Hkv, parents or not,
+ *              weights or not, and the cache's D, page, max_blocks); left ready
+ *              for the next call of that shape, not to be used by two calls at
+ *              once.
  * One kernel, two with weights.
  */
 int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,

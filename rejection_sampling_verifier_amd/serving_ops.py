@@ -288,8 +288,8 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
 
     Returns out [B, T, H, D], or (out, weights).  Tensors made here hold zeros
     behind query_lens.  A call given no workspace uses one cached for its
-    shape, device and stream; under graph capture it makes and clears one that
-    belongs to the graph.
+    shape, device and stream; under graph capture it makes one that belongs to
+    the graph, and clears its counters in it.
     """
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
@@ -321,8 +321,10 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
             _need("out", out, (B, T, H, D), torch.bfloat16, dev)
         if workspace is None:
             if torch.cuda.is_current_stream_capturing():
-                # a workspace of the graph's own, cleared in it: graphs replayed at once must not share one
-                workspace = torch.zeros(need, dtype=torch.uint8, device=dev)
+                # a workspace of the graph's own: graphs replayed at once must not share one.  Its counters,
+                # all that has to be zero, are cleared in the graph.
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace[:4 * B * cache.Hkv * -(-(T * (H // cache.Hkv)) // 16)].zero_()
             else:
                 key = (B, T, H, cache.Hkv, D, cache.page, cache.max_blocks, parents is not None, weights is not None)
                 workspace = _cached_workspace("attention", key, need, dev, handle)
