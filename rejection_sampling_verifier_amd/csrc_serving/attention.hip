@@ -74,8 +74,9 @@ struct AttnArgs {
   const int32_t* parents;
   const int32_t* qlens;
   int T, H, G, mtiles;
-  int runs;                    // runs of all row tiles' lines, per head, that fill the chip
-  int even;                    // runs if no line ended with a part of one: the sum over lines is at most runs
+  int even;                    // runs of all row tiles' lines, per head, if no line ended with a part of one; with
+                               // c = ceil(tiles / even) tiles to a run, the sum over lines of ceil(line / c) is at
+                               // most even + mtiles - 1, for which the grid is made
   float scale2;                // scale * log2(e)
   uint16_t* out;
   float* weights;
@@ -1251,7 +1252,6 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   a.H = H;
   a.G = H / c.Hkv;
   a.mtiles = pl.mtiles;
-  a.runs = pl.runs;
   a.even = pl.even;
   a.scale2 = scale * LOG2E;
   a.out = static_cast<uint16_t*>(out);
