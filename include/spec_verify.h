@@ -624,13 +624,13 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
  * cache        with tail >= page - 1 + T.  No page may be in reserve for two
  *              rows.
  * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
- *              a second kernel updates them), but not overlap them or
- *              num_accepted otherwise.
+ *              a second kernel updates them).
  * weights      [B, T, max_blocks] float32 (spec_verify_attention's) or NULL.
  * totals, totals_out [B, max_blocks] float32, both or none: totals_out[b][j]
  *              is totals[b][j] plus the weights of block j from the committed
  *              tokens for the blocks that row b had, 0 for the rest.  They may
  *              be the same array.
+ * Beyond that no output may overlap an input or another output.
  */
 int spec_verify_commit(const void* k_new, const void* v_new, int64_t kv_row,
                        int64_t kv_tok, int T, const int32_t* num_accepted,
@@ -659,7 +659,8 @@ int spec_verify_commit(const void* k_new, const void* v_new, int64_t kv_row,
  * blocks       [B] int32
  * totals_out, table_out, blocks_out  as these; each may be its input itself
  *              (table_out only up to max_blocks = 16384, else
- *              SV_ERR_UNSUPPORTED), but not overlap it otherwise.
+ *              SV_ERR_UNSUPPORTED).  Beyond that no output may overlap an input
+ *              or another output.
  * evicted      [B] int32: how many blocks left.
  * budget, keep_first, keep_last >= 0; 1 <= max_blocks <= SV_MAX_BLOCKS.
  * One kernel, no workspace.

@@ -30,10 +30,30 @@ __device__ __forceinline__ RowState row_state(const sv_cache& c, const int32_t* 
   return s;
 }
 
-// Whether two arrays of n bytes share any.
-inline bool overlap(const void* a, const void* b, size_t n) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + n && y < x + n;
+// An argument's array.
+struct Array {
+  const void* p;
+  size_t bytes;
+};
+// Whether an output shares bytes with another output, or with an input other
+// than the one that it may be itself (updated in place).
+struct Output {
+  Array a;
+  const void* in;
+};
+inline bool overlap(const Array& a, const Array& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+template <size_t NO, size_t NI>
+inline bool outputs_overlap(const Output (&out)[NO], const Array (&in)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(out[i].a, out[j].a)) return true;
+    for (const Array& a : in)
+      if (!(a.p == out[i].a.p && a.p == out[i].in) && overlap(out[i].a, a)) return true;
+  }
+  return false;
 }
 
 // Checks of the cache's description that every entry point makes.

@@ -275,14 +275,14 @@ extern "C" int spec_verify_commit(const void* k_new, const void* v_new, int64_t 
   if (T > SV_MAX_K + 1) return SV_ERR_UNSUPPORTED;
   if (c.tail < c.page - 1 + T) return SV_ERR_ARG;
   const size_t nb = (size_t)c.B * 4, nt = nb * c.max_blocks;
-  if ((positions == positions_out) != (blocks == blocks_out) || overlap(positions_out, blocks_out, nb) ||
-      overlap(positions, blocks_out, nb) || overlap(blocks, positions_out, nb) ||
-      overlap(num_accepted, positions_out, nb) || overlap(num_accepted, blocks_out, nb) ||
-      (positions != positions_out && (overlap(positions, positions_out, nb) || overlap(blocks, blocks_out, nb))))
-    return SV_ERR_ARG;
-  if (totals && totals != totals_out && overlap(totals, totals_out, nt)) return SV_ERR_ARG;
+  if ((positions == positions_out) != (blocks == blocks_out)) return SV_ERR_ARG;
   if ((totals == nullptr) != (totals_out == nullptr) || (weights && !totals)) return SV_ERR_ARG;
   if (nodes && (nodes_stride < T - 1 || nodes_stride > INT_MAX)) return SV_ERR_ARG;
+  // What some work-groups still read when others write.
+  const Output out[] = {{{positions_out, nb}, positions}, {{blocks_out, nb}, blocks}, {{totals_out, nt}, totals}};
+  const Array in[] = {{positions, nb}, {blocks, nb}, {num_accepted, nb}, {totals, nt}, {c.block_table, nt},
+                      {weights, nt * T}, {nodes, 4 * ((size_t)nodes_stride * (c.B - 1) + T - 1)}};
+  if (outputs_overlap(out, in)) return SV_ERR_ARG;
   const void* aligned[] = {k_new, v_new};
   for (const void* p : aligned)
     if (reinterpret_cast<uintptr_t>(p) % 16) return SV_ERR_ARG;

@@ -20,7 +20,7 @@
 #include "cache.h"
 
 using namespace sv;
-using svr::overlap;
+using namespace svr;
 
 namespace {
 
@@ -266,13 +266,11 @@ extern "C" int spec_verify_evict(const float* totals, const int32_t* block_table
       max_blocks < 1 || budget < 0 || keep_first < 0 || keep_last < 0)
     return SV_ERR_ARG;
   if (max_blocks > SV_MAX_BLOCKS) return SV_ERR_UNSUPPORTED;
-  const size_t n = (size_t)B * max_blocks * 4;
-  if ((totals_out != totals && overlap(totals_out, totals, n)) ||
-      (table_out != block_table && overlap(table_out, block_table, n)) || overlap(totals_out, block_table, n) ||
-      overlap(table_out, totals, n) || overlap(totals_out, table_out, n) ||
-      (blocks_out != blocks && overlap(blocks_out, blocks, (size_t)B * 4)) || overlap(evicted, blocks, (size_t)B * 4) ||
-      overlap(evicted, blocks_out, (size_t)B * 4))
-    return SV_ERR_ARG;
+  const size_t n = (size_t)B * max_blocks * 4, nb = (size_t)B * 4;
+  const Output out[] = {{{totals_out, n}, totals}, {{table_out, n}, block_table}, {{blocks_out, nb}, blocks},
+                        {{evicted, nb}, nullptr}};
+  const Array in[] = {{totals, n}, {block_table, n}, {blocks, nb}};
+  if (outputs_overlap(out, in)) return SV_ERR_ARG;
   if (max_blocks > HELD_BLOCKS && table_out == block_table) return SV_ERR_UNSUPPORTED;
   const EvictArgs a{totals, block_table, blocks, totals_out, table_out, blocks_out, evicted, max_blocks, budget,
                     keep_first, keep_last};

@@ -7,10 +7,32 @@ from __future__ import annotations
 import pytest
 
 from rejection_sampling_verifier_amd import binding as B
-from tests.test_serving_abi import P, adjust
+from tests.test_serving_abi import P, adjust, commit, evict
 
 
 @pytest.mark.parametrize("width", [-1, 5])
 def test_a_history_is_no_wider_than_its_rows_are_apart(width):
     assert adjust(c_repetition=P[3], c_history=P[5], c_history_lens=P[6], c_history_stride=4,
                   c_history_width=width) == B.SV_ERR_ARG
+
+
+COUNTERS, TOTALS, WEIGHTS, NODES = 2 * 4, 2 * 10 * 4, 2 * 3 * 10 * 4, 4 * (5 + 2)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(totals_out=P[19]), dict(totals_out=P[19] + WEIGHTS - 4), dict(totals_out=P[19] + 4 - TOTALS),   # over weights
+    dict(totals_out=P[6]), dict(totals_out=P[12] + 4), dict(totals_out=P[13]), dict(totals_out=P[14] + 4 - TOTALS),
+    dict(totals_out=P[17] + NODES - 4), dict(totals_out=P[15]), dict(totals_out=P[16] - TOTALS + 4),
+    dict(positions_out=P[6] + TOTALS - 4), dict(blocks_out=P[17] + NODES - 4), dict(positions_out=P[19]),
+    dict(blocks_out=P[18] + 4)])
+def test_commit_refuses_outputs_over_what_it_reads(bad):
+    a = dict(nodes=P[17], stride=5, weights=P[19], totals=P[18], totals_out=P[20])
+    assert commit(**dict(a, **bad)) == B.SV_ERR_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(evicted=P[0]), dict(evicted=P[1] + 1600 - 4), dict(evicted=P[3] + 8), dict(evicted=P[4] - 12),
+    dict(blocks_out=P[0] + 1596), dict(blocks_out=P[1]), dict(blocks_out=P[3] - 12), dict(blocks_out=P[4]),
+    dict(totals_out=P[2] - 1596), dict(table_out=P[2])])
+def test_evict_refuses_outputs_over_what_it_reads(bad):
+    assert evict(**bad) == B.SV_ERR_ARG
