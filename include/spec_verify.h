@@ -575,7 +575,8 @@ typedef struct {
  * T in [1, SV_MAX_K + 1] ([1, SV_MAX_NODES] with parents), H a multiple of
  * Hkv (at most 256 times it), scale positive and finite.
  * out          [B, T, H, D] bf16 contiguous.  Neither it nor weights may
- *              overlap the other or a row of q, k_new or v_new.
+ *              overlap the other, the workspace, a row of q, k_new or v_new,
+ *              or another input.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
  *              not have.
  * workspace, workspace_bytes  as spec_verify, but only its first 4 * B * Hkv *

@@ -1234,7 +1234,12 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
     if (crosses(p, row, c.B, span, out, bytes) || (weights && crosses(p, row, c.B, span, weights, mass)))
       return SV_ERR_ARG;
   }
-  if (weights && crosses(weights, 0, 1, mass, out, bytes)) return SV_ERR_ARG;
+  const size_t nb = (size_t)c.B * 4, pages = (size_t)c.num_pages * c.Hkv, tail = (size_t)c.B * c.tail * c.Hkv * c.D * 2;
+  const Output written[] = {{{out, (size_t)bytes}, nullptr}, {{weights, (size_t)mass}, nullptr}, {{workspace, pl.total}, nullptr}};
+  const Array read[] = {{positions, nb}, {blocks, nb}, {query_lens, nb}, {parents, nb * T}, {c.block_table, nb * c.max_blocks},
+                        {c.k_pages, pages * c.page * c.D}, {c.v_pages, pages * c.page * c.D}, {c.k_scale, pages * 4},
+                        {c.v_scale, pages * 4}, {c.k_tail, tail}, {c.v_tail, tail}};
+  if (outputs_overlap(written, read)) return SV_ERR_ARG;
   AttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.kn = static_cast<const uint16_t*>(k_new);

@@ -7,7 +7,7 @@ from __future__ import annotations
 import pytest
 
 from rejection_sampling_verifier_amd import binding as B
-from tests.test_serving_abi import P, adjust, commit, evict
+from tests.test_serving_abi import OUT, P, WEIGHTS, adjust, attention, commit, evict
 
 
 @pytest.mark.parametrize("width", [-1, 5])
@@ -16,7 +16,7 @@ def test_a_history_is_no_wider_than_its_rows_are_apart(width):
                   c_history_width=width) == B.SV_ERR_ARG
 
 
-COUNTERS, TOTALS, WEIGHTS, NODES = 2 * 4, 2 * 10 * 4, 2 * 3 * 10 * 4, 4 * (5 + 2)
+COUNTERS, TOTALS, NODES = 2 * 4, 2 * 10 * 4, 4 * (5 + 2)
 
 
 @pytest.mark.parametrize("bad", [
@@ -36,3 +36,15 @@ def test_commit_refuses_outputs_over_what_it_reads(bad):
     dict(totals_out=P[2] - 1596), dict(table_out=P[2])])
 def test_evict_refuses_outputs_over_what_it_reads(bad):
     assert evict(**bad) == B.SV_ERR_ARG
+
+
+PAGES, TAIL = 100 * 2 * 16 * 64, 2 * 32 * 2 * 64 * 2
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=P[20]), dict(out=P[20] + 16 - OUT), dict(weights=P[20] + 64), dict(weights=P[0] + PAGES - 4),
+    dict(out=P[1]), dict(out=P[4] + TAIL - 16), dict(weights=P[5]), dict(weights=P[2] + 796), dict(out=P[3]),
+    dict(out=P[6]), dict(weights=P[13] + 4), dict(weights=P[14] + 4 - WEIGHTS), dict(out=P[16], parents=P[16]),
+    dict(weights=P[17], lens=P[17])])
+def test_attention_refuses_outputs_over_any_input(bad):
+    assert attention(**bad) == B.SV_ERR_ARG
