@@ -491,7 +491,8 @@ typedef struct {
  *              that node.
  * B >= 1, P in [1, SV_MAX_K + 1] (SV_MAX_NODES with parents), V >= 1.
  * One kernel, no workspace.  SV_ERR_ARG, SV_ERR_UNSUPPORTED (P too large, or
- * a grid beyond 2^31 work-groups) or SV_ERR_HIP.
+ * 2^24 and more rows times parts of 4096 ids: of 2048 where bias_stride
+ * passes 2048) or SV_ERR_HIP.
  */
 int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
                               int64_t stride, const int32_t* tokens,
@@ -578,7 +579,7 @@ typedef struct {
  *              overlap the other, the workspace, a row of q, k_new or v_new,
  *              or another input.
  * weights      [B, T, max_blocks] float32 or NULL; 0 for blocks that a row does
- *              not have.
+ *              not have.  Fewer than 2^32 of them.
  * workspace, workspace_bytes  as spec_verify, but only its first 4 * B * Hkv *
  *              ceil(T * H / Hkv / 16) bytes need to be zero-filled before its
  *              first use with a given shape (B, T, H and Hkv, parents or not,
@@ -623,7 +624,8 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
  * num_accepted [B] int32; nodes [B, nodes_stride] int32 or NULL, nodes_stride
  *              >= T - 1.
  * cache        with tail >= page - 1 + T.  No page may be in reserve for two
- *              rows.
+ *              rows, nor in reserve for one and among the blocks of another.
+ *              B (2 + 2 Hkv + max_blocks / 256) < 2^24.
  * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
  *              a second kernel updates them).
  * weights      [B, T, max_blocks] float32 (spec_verify_attention's) or NULL.
@@ -663,7 +665,8 @@ int spec_verify_commit(const void* k_new, const void* v_new, int64_t kv_row,
  *              SV_ERR_UNSUPPORTED).  Beyond that no output may overlap an input
  *              or another output.
  * evicted      [B] int32: how many blocks left.
- * budget, keep_first, keep_last >= 0; 1 <= max_blocks <= SV_MAX_BLOCKS.
+ * budget, keep_first, keep_last >= 0; 1 <= max_blocks <= SV_MAX_BLOCKS; B <
+ * 2^22.
  * One kernel, no workspace.
  */
 int spec_verify_evict(const float* totals, const int32_t* block_table,

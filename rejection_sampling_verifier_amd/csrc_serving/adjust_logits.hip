@@ -44,6 +44,7 @@ using namespace sv;
 namespace {
 
 constexpr int CH = 4096;                 // token ids per chunk at most
+constexpr int64_t MAX_GROUPS = UINT32_MAX / WG;  // a launch has fewer than 2^32 work-items
 constexpr int GRID_WANTED = 1024;        // work-groups that fill the chip; below, positions are split too
 constexpr uint32_t IN_PROMPT = 1u << 31; // table entry: occurs in the prompt;
 constexpr uint32_t BIASED = 1u << 30;    // has a bias; the rest counts n(x)
@@ -435,7 +436,7 @@ extern "C" int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
   const int64_t groups = (int64_t)B * a.C;
   a.PG = (int)(groups >= GRID_WANTED ? 1 : (GRID_WANTED + groups - 1) / groups);
   if (a.PG > P) a.PG = P;
-  if (groups * a.PG > INT32_MAX) return SV_ERR_UNSUPPORTED;
+  if (groups * a.PG > MAX_GROUPS) return SV_ERR_UNSUPPORTED;
   if (a.c.bias_stride <= 0) a.c.bias_ids = nullptr;
   void (*const k)(AdjustArgs) = dtype == SV_BF16 ? adjust_logits_kernel<uint16_t> : adjust_logits_kernel<float>;
   (void)hipGetLastError();

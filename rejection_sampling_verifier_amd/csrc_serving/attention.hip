@@ -1151,7 +1151,7 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
     off = align256(off + sizeof(float) * rows * mpad);
     pl.mass = off;
     off = align256(off + sizeof(float) * rows * mpad * (size_t)nsub);
-    if (((int64_t)c.B * T * c.max_blocks + WG - 1) / WG > INT_MAX) return SV_ERR_UNSUPPORTED;
+    if (((int64_t)c.B * T * c.max_blocks + WG - 1) / WG > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
   }
   pl.total = off;
   return SV_OK;

@@ -16,6 +16,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+constexpr int64_t MAX_ITEMS = UINT32_MAX;  // a launch has fewer than 2^32 work-items
+
 // The counters of one row, brought into range: full blocks kept and tokens
 // in the tail (its first token's ring slot is `start`).
 struct RowState {

@@ -311,7 +311,7 @@ extern "C" int spec_verify_commit(const void* k_new, const void* v_new, int64_t 
   a.total_groups = totals ? (c.max_blocks + WG - 1) / WG : 0;
   a.inplace = positions == positions_out;
   const int64_t grid = (int64_t)c.B * (2 + a.quant_groups + a.total_groups);
-  if (grid > INT_MAX) return SV_ERR_UNSUPPORTED;
+  if (grid > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
   (void)hipGetLastError();
   hipLaunchKernelGGL(kernel_of(c), dim3((uint32_t)grid), dim3(WG), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;

@@ -265,7 +265,7 @@ extern "C" int spec_verify_evict(const float* totals, const int32_t* block_table
   if (!totals || !block_table || !blocks || !totals_out || !table_out || !blocks_out || !evicted || B < 1 ||
       max_blocks < 1 || budget < 0 || keep_first < 0 || keep_last < 0)
     return SV_ERR_ARG;
-  if (max_blocks > SV_MAX_BLOCKS) return SV_ERR_UNSUPPORTED;
+  if (max_blocks > SV_MAX_BLOCKS || B > MAX_ITEMS / ET) return SV_ERR_UNSUPPORTED;
   const size_t n = (size_t)B * max_blocks * 4, nb = (size_t)B * 4;
   const Output out[] = {{{totals_out, n}, totals}, {{table_out, n}, block_table}, {{blocks_out, nb}, blocks},
                         {{evicted, nb}, nullptr}};

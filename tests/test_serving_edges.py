@@ -7,7 +7,7 @@ from __future__ import annotations
 import pytest
 
 from rejection_sampling_verifier_amd import binding as B
-from tests.test_serving_abi import OUT, P, WEIGHTS, adjust, attention, commit, evict
+from tests.test_serving_abi import OUT, P, WEIGHTS, adjust, attention, cache, commit, evict
 
 
 @pytest.mark.parametrize("width", [-1, 5])
@@ -48,3 +48,20 @@ PAGES, TAIL = 100 * 2 * 16 * 64, 2 * 32 * 2 * 64 * 2
     dict(weights=P[17], lens=P[17])])
 def test_attention_refuses_outputs_over_any_input(bad):
     assert attention(**bad) == B.SV_ERR_ARG
+
+
+def test_launches_of_2_to_the_32_work_items_are_refused():
+    """A launch counts its work-items in 32 bits."""
+    far = P[0] + (1 << 50)
+    one = dict(P=1, V=4096, row=4096, stride=4096, out_row=4096, out_stride=4096, out=far)
+    assert adjust(B=2 ** 24, **one) == B.SV_ERR_UNSUPPORTED
+    biased = dict(one, c_bias_ids=P[7], c_bias_values=P[8], c_bias_stride=2049)
+    assert adjust(B=2 ** 23, **biased) == B.SV_ERR_UNSUPPORTED
+    big = cache(B=65536, Hkv=128, num_pages=1, max_blocks=1)
+    for i, k in enumerate(("k_pages", "v_pages", "k_scale", "v_scale", "k_tail", "v_tail", "block_table")):
+        setattr(big, k, (1 << 50) + (i << 44))
+    assert commit(c=big, kn=1 << 52, vn=1 << 53) == B.SV_ERR_UNSUPPORTED
+    many = cache(B=65536, Hkv=1, max_blocks=65536, page=16)
+    assert attention(c=many, H=1, T=1, weights=P[16], ws=None)[0] == B.SV_ERR_UNSUPPORTED
+    assert evict(B=2 ** 22, most=1, totals=1 << 50, table=1 << 51, totals_out=1 << 52, table_out=1 << 53,
+                 blocks=1 << 54, blocks_out=1 << 55, evicted=1 << 56) == B.SV_ERR_UNSUPPORTED
