@@ -9,6 +9,7 @@ Outputs and workspaces that a call allocates belong to the stream it runs on.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -89,6 +90,11 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _count(n, most):
+    """A whole number for a C int: those past `most` count as `most`, and negative ones, which are refused, as -1."""
+    return max(-1, min(operator.index(n), most))
+
+
 def _logit_strides(name, t):
     """(row, position) strides of a [B, P, V] tensor with contiguous logits."""
     B, P, V = t.shape
@@ -123,6 +129,8 @@ def adjust_logits(logits, tokens=None, *, parents=None, history=None, history_le
     if logits.dim() != 3 or 0 in logits.shape:
         raise ValueError("logits must be [B, P, V]")
     B, P, V = logits.shape
+    if V > 2 ** 31 - 1 or B > 2 ** 31 - 1:
+        raise ValueError(f"logits are too large: {tuple(logits.shape)}")
     dt = _dtype_code(logits)
     in_row, in_pos = _logit_strides("logits", logits)
     i32, f32 = torch.int32, torch.float32
@@ -409,6 +417,7 @@ def cache_evict(block_table, totals, blocks, budget, *, keep_first=0, keep_last=
     _need("block_table", block_table, (B, most), torch.int32, dev)
     _need("totals", totals, (B, most), torch.float32, dev)
     _need("blocks", blocks, (B,), torch.int32, dev)
+    budget, keep_first, keep_last = (_count(n, most) for n in (budget, keep_first, keep_last))
     handle, scope = _scope(dev, stream)
     with scope:
         outs = []

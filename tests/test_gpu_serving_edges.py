@@ -80,3 +80,19 @@ def test_listed_logits_that_nothing_applies_to_keep_their_bits(dtype, word, bits
         same[0, i, t] = False
         assert float(want[0, i, t]) - 1 == pytest.approx(float(got[0, i, t]), rel=2 ** -7, nan_ok=True)
     assert torch.equal(got.view(word)[same], want.view(word)[same])
+
+
+def test_eviction_counts_past_32_bits_and_below_zero():
+    """A budget of 2^32 is no budget of 0."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, totals, blocks = torch.arange(12, **i32).view(2, 6), torch.rand((2, 6), device="cuda"), torch.tensor([6, 4], **i32)
+    for kw in (dict(budget=2 ** 32), dict(budget=2 ** 63), dict(budget=2, keep_first=2 ** 32), dict(budget=0, keep_last=2 ** 40)):
+        t, w, n, gone = rsv.cache_evict(table, totals, blocks, **kw)
+        assert torch.equal(t, table) and torch.equal(n, blocks) and not gone.any()
+        assert torch.equal(w[0], totals[0]) and torch.equal(w[1, :4], totals[1, :4])
+    assert rsv.cache_evict(table, totals, blocks, 3, keep_first=2 ** 31 - 1)[3].tolist() == [0, 0]
+    for kw in (dict(budget=-1), dict(budget=-2 ** 32), dict(budget=1, keep_first=-5), dict(budget=1, keep_last=-2 ** 33)):
+        with pytest.raises(rsv.SpecVerifyError):
+            rsv.cache_evict(table, totals, blocks, **kw)
+    with pytest.raises(TypeError):
+        rsv.cache_evict(table, totals, blocks, 2.5)
