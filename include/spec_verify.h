@@ -574,7 +574,8 @@ typedef struct {
  *              tokens.  What lies behind them in q, k_new and v_new is not
  *              read, and in out and weights not written; a row of 0 is idle.
  * T in [1, SV_MAX_K + 1] ([1, SV_MAX_NODES] with parents), H a multiple of
- * Hkv (at most 256 times it), scale positive and finite.
+ * Hkv (at most 256 times it), scale positive and finite.  B (max_blocks * page
+ * / 64 + 10) ceil(T * H / Hkv / 16) < 2^30.
  * out          [B, T, H, D] bf16 contiguous.  Neither it nor weights may
  *              overlap the other, the workspace, a row of q, k_new or v_new,
  *              or another input.

@@ -1128,7 +1128,8 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   pl.mtiles = (M + mt - 1) / mt;
   const int64_t tiles = (int64_t)c.B * pl.mtiles, heads = tiles * c.Hkv;
   const int64_t most = ((int64_t)c.max_blocks * c.page + 63) / 64 + (c.page - 1 + T + 31) / 32;
-  if (most * tiles > INT_MAX || heads > INT_MAX) return SV_ERR_UNSUPPORTED;
+  // The device counts a line's tiles, and that many once more, in 32 bits.
+  if (most * tiles > INT_MAX / 2 || heads > INT_MAX) return SV_ERR_UNSUPPORTED;
   // Runs that the chip holds at once (see the kernel's registers).  Each row
   // tile's line may end with a part of a run, so the length of a run is
   // chosen for that many fewer (half of them where row tiles are many).

@@ -65,3 +65,11 @@ def test_launches_of_2_to_the_32_work_items_are_refused():
     assert attention(c=many, H=1, T=1, weights=P[16], ws=None)[0] == B.SV_ERR_UNSUPPORTED
     assert evict(B=2 ** 22, most=1, totals=1 << 50, table=1 << 51, totals_out=1 << 52, table_out=1 << 53,
                  blocks=1 << 54, blocks_out=1 << 55, evicted=1 << 56) == B.SV_ERR_UNSUPPORTED
+
+
+def test_rows_of_more_tiles_than_32_bits_count_are_refused():
+    """8191 rows of 65536 blocks of 256 tokens are nearly 2^31 tiles, which a rounded-up division carries past it."""
+    for b, hkv in ((8191, 1), (4097, 1024)):
+        assert attention(c=cache(B=b, Hkv=hkv, page=256, max_blocks=65536, tail=512), H=hkv, T=1,
+                         ws=None)[0] == B.SV_ERR_UNSUPPORTED
+    assert attention(c=cache(B=2000, Hkv=1, page=256, max_blocks=65536, tail=512), H=1, T=1, ws=None)[0] == B.SV_OK
