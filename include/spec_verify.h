@@ -490,9 +490,9 @@ typedef struct {
  *              path of a node whose parent is not an earlier node starts at
  *              that node.
  * B >= 1, P in [1, SV_MAX_K + 1] (SV_MAX_NODES with parents), V >= 1.
- * One kernel, no workspace.  SV_ERR_ARG, SV_ERR_UNSUPPORTED (P too large, or
- * 2^24 and more rows times parts of 4096 ids: of 2048 where bias_stride
- * passes 2048) or SV_ERR_HIP.
+ * One kernel, no workspace.  SV_ERR_ARG, SV_ERR_UNSUPPORTED (P too large; a
+ * history_width or bias_stride beyond 2^30 - 1024; 2^24 and more rows times
+ * parts of 4096 ids, of 2048 where bias_stride passes 2048) or SV_ERR_HIP.
  */
 int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
                               int64_t stride, const int32_t* tokens,

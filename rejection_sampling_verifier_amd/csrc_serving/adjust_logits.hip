@@ -48,6 +48,7 @@ constexpr int64_t MAX_GROUPS = UINT32_MAX / WG;  // a launch has fewer than 2^32
 constexpr int GRID_WANTED = 1024;        // work-groups that fill the chip; below, positions are split too
 constexpr uint32_t IN_PROMPT = 1u << 31; // table entry: occurs in the prompt;
 constexpr uint32_t BIASED = 1u << 30;    // has a bias; the rest counts n(x)
+constexpr int64_t MAX_ENTRIES = (1 << 30) - 1024;  // of a row's history or biases: a count stays below BIASED, an index in 32 bits
 constexpr int BIASES = 2048;             // biased ids of a chunk that LDS holds; rows with more entries get chunks of so many
 
 struct AdjustArgs {
@@ -415,9 +416,11 @@ extern "C" int spec_verify_adjust_logits(const void* logits, int64_t row_stride,
                         a.c.history_width < 0 || a.c.history_width > a.c.history_stride))
       return SV_ERR_ARG;
     if (a.c.history_width == 0) a.c.history_width = a.c.history_stride;
+    if (a.c.history && a.c.history_width > MAX_ENTRIES) return SV_ERR_UNSUPPORTED;
     if (P > 1 && (!tokens || tokens_stride < (parents ? P : P - 1) || tokens_stride > INT32_MAX)) return SV_ERR_ARG;
   }
   if (a.c.bias_ids && (!a.c.bias_values || a.c.bias_stride < 0 || a.c.bias_stride > INT32_MAX - 1)) return SV_ERR_ARG;
+  if (a.c.bias_ids && a.c.bias_stride > MAX_ENTRIES) return SV_ERR_UNSUPPORTED;
   if (a.c.mask && (a.c.num_masks < 0 || (!a.c.mask_rows && a.c.num_masks < (int64_t)B * P))) return SV_ERR_ARG;
   a.in = logits;
   a.out = out;

@@ -73,3 +73,12 @@ def test_rows_of_more_tiles_than_32_bits_count_are_refused():
         assert attention(c=cache(B=b, Hkv=hkv, page=256, max_blocks=65536, tail=512), H=hkv, T=1,
                          ws=None)[0] == B.SV_ERR_UNSUPPORTED
     assert attention(c=cache(B=2000, Hkv=1, page=256, max_blocks=65536, tail=512), H=1, T=1, ws=None)[0] == B.SV_OK
+
+
+def test_rows_of_2_to_the_30_entries_are_refused():
+    """A count shares its word with two flags, and indices run past a row's end by a work-group's stride."""
+    n = 2 ** 30
+    hist = dict(c_repetition=P[3], c_history=P[5], c_history_lens=P[6])
+    assert adjust(c_history_stride=n, **hist) == B.SV_ERR_UNSUPPORTED
+    assert adjust(c_history_stride=2 * n - 1, c_history_width=n, **hist) == B.SV_ERR_UNSUPPORTED
+    assert adjust(c_bias_ids=P[7], c_bias_values=P[8], c_bias_stride=2 * n - 2) == B.SV_ERR_UNSUPPORTED
