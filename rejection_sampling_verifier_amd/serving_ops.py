@@ -229,6 +229,9 @@ class KVCache:
             raise AttributeError(f"a KVCache keeps the tensors it was made of: copy into {name}, or make another")
         super().__setattr__(name, value)
 
+    def __delattr__(self, name):
+        raise AttributeError(f"a KVCache keeps the tensors it was made of: {name} cannot be deleted")
+
 
 def new_cache(B, num_pages, Hkv, D, page=64, max_blocks=None, max_new=SV_MAX_K + 1, kind="e4m3", device="cuda"):
     """An empty cache: no pages are assigned (block_table is -1), and the tails

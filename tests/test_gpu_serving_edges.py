@@ -96,3 +96,10 @@ def test_eviction_counts_past_32_bits_and_below_zero():
             rsv.cache_evict(table, totals, blocks, **kw)
     with pytest.raises(TypeError):
         rsv.cache_evict(table, totals, blocks, 2.5)
+
+
+def test_a_cache_does_not_lose_its_tensors():
+    cache = rsv.new_cache(1, 2, 1, 64, page=16)
+    for name in ("block_table", "k_pages", "_c"):
+        with pytest.raises(AttributeError):
+            delattr(cache, name)
