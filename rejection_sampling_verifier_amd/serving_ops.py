@@ -237,6 +237,8 @@ def new_cache(B, num_pages, Hkv, D, page=64, max_blocks=None, max_new=SV_MAX_K +
     """An empty cache: no pages are assigned (block_table is -1), and the tails
     hold what a commit of up to max_new tokens needs."""
     dev = torch.device(device)
+    if min(B, num_pages, Hkv, D, page, max_new) < 1 or (max_blocks is not None and max_blocks < 1):
+        raise ValueError("a cache's sizes must be at least 1")
     tail = -(-(page - 1 + max_new) // page) * page
     z = lambda shape, dtype: torch.zeros(shape, dtype=dtype, device=dev)  # noqa: E731
     table = torch.full((B, max_blocks if max_blocks is not None else max(1, num_pages // B)), -1, dtype=torch.int32,

@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import pytest
 
+import rejection_sampling_verifier_amd as rsv
 from rejection_sampling_verifier_amd import binding as B
 from tests.test_serving_abi import OUT, P, WEIGHTS, adjust, attention, cache, commit, evict
 
@@ -82,3 +83,10 @@ def test_rows_of_2_to_the_30_entries_are_refused():
     assert adjust(c_history_stride=n, **hist) == B.SV_ERR_UNSUPPORTED
     assert adjust(c_history_stride=2 * n - 1, c_history_width=n, **hist) == B.SV_ERR_UNSUPPORTED
     assert adjust(c_bias_ids=P[7], c_bias_values=P[8], c_bias_stride=2 * n - 2) == B.SV_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("bad", [dict(B=0), dict(num_pages=0), dict(Hkv=0), dict(D=0), dict(page=0), dict(max_new=0),
+                                 dict(max_blocks=0), dict(B=-1)])
+def test_new_cache_refuses_empty_sizes(bad):
+    with pytest.raises(ValueError):
+        rsv.new_cache(**dict(dict(B=1, num_pages=4, Hkv=1, D=64, page=16), **bad))
