@@ -767,8 +767,11 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     for (int n = 0; n < NQ; ++n) {
       float x[8], p[8];
       // Seen: the tail (node < 0) and, of the new tokens, a chain's up to the
-      // query's own or those of its path.  Plain bit operations: the compiler
-      // made wrong code of the same condition written with branches.
+      // query's own or those of its path.  Plain bit operations: written as
+      // key < have && (node < 0 || (parents ? path bit : node <= tok)), the
+      // compiler (clang 22 of ROCm 7.2.0) puts the path's bit into the score's
+      // register, sets the result to -inf for every new token and leaves the
+      // block that should give the seen ones their score empty.
       const int last = a.parents ? -1 : tok[n];
       const uint64_t path = a.parents ? sh.path[tok[n]] : 0;
 #pragma unroll
