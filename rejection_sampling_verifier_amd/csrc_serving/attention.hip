@@ -62,6 +62,7 @@ constexpr float LOW = -110.f;  // scores further below the maximum count as this
 constexpr float VMIN = 0x1p-126f;  // smallest value scale told apart (see spec_verify.h)
 constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
 constexpr int TOP = 100;       // sums are not raised above 2^TOP
+constexpr int LOST = -40;
 
 struct AttnArgs {
   const uint16_t* q;
@@ -450,7 +451,9 @@ __device__ __forceinline__ void softmax_cached(State<D, NQ>& st, int n, const fl
     }
     st.set_x(n, st.x(n) + dx);
   }
-  const int up = unlike ? 0 : v.e + st.x(n);
+  // Beside sums that may not be raised further, f16 takes a tile for zeros (of
+  // 2^LOST 2^GROW it knows no step); its probabilities still count.
+  const int up = unlike ? 0 : max(v.e + st.x(n), LOST);
   const float off = (float)up + v.log - fmaxf(st.m[n], -FAR);
   psum = 0.f;
 #pragma unroll

@@ -133,6 +133,16 @@ def test_a_strong_new_token_before_small_values(strong, D, page, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D, page", [(64, 64), (128, 16)])
+@pytest.mark.parametrize("gain, near", [(2.0 ** -100, 2.0 ** 120), (2.0 ** -60, 2.0 ** 100), (2.0 ** -110, 1.0),
+                                        (2.0 ** 100, 2.0 ** -100), (2.0 ** -20, 2.0 ** 20)])
+def test_ends_of_the_range_in_one_wave(gain, near, D, page, kind):
+    """Rows as long as above: what a wave's sums cannot hold beside each other still counts in the denominator."""
+    s, qkv = state(10, [16384 + 40, 9000], 8, 8, D, page, kind, 1, gain=gain, near=near)
+    check(s, qkv, 8)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("page", [16, 32, 64])
 @pytest.mark.parametrize("span", [8, 40, 110])
 def test_unlike_scales_in_one_wave(span, page, kind):
