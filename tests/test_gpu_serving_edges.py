@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import rejection_sampling_verifier_amd as rsv
+from tests import cache_ref as R
 from tests import test_gpu_adjust_logits as A
+from tests import test_gpu_attention as AT
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +105,101 @@ def test_a_cache_does_not_lose_its_tensors():
     for name in ("block_table", "k_pages", "_c"):
         with pytest.raises(AttributeError):
             delattr(cache, name)
+
+
+def test_more_rows_than_threads_with_several_row_tiles():
+    """300 rows, several to a thread, each of up to three tiles of queries, some idle."""
+    AT.case(74, [(29 * b) % 90 for b in range(300)], 33, 4, 2, 128, 32, "int8", tree=True,
+            query_lens=[(11 * b) % 35 - 1 for b in range(300)])
+
+
+@pytest.mark.parametrize("H, T", [(520, 3), (1040, 40)])
+def test_more_heads_than_work_groups(H, T):
+    """One run holds a whole line: the chip is filled by the heads alone."""
+    AT.case(75, [100, 0, 33], T, H, 520, 64, 16, "e4m3")
+
+
+def test_two_streams_at_once():
+    """Calls without a workspace on two streams have one each."""
+    B, T, H, Hkv, D = 4, 5, 8, 2, 128
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for i in range(2):
+        s = R.random_state(76 + i, B=B, Hkv=Hkv, D=D, page=64, kind="e4m3", contexts=[6000, 40, 3000, 900 * i],
+                           max_blocks=100)
+        cache, positions, blocks = R.to_gpu(s)
+        q, kn, vn = AT.views(AT.make_qkv(78 + i, B, T, H, Hkv, D).cuda(), H, Hkv)
+        want = rsv.cache_attention(q, kn, vn, cache, positions, blocks, weights=True)
+        jobs.append((q, kn, vn, cache, positions, blocks, want))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (stream, job) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(stream):
+                got[i].append(rsv.cache_attention(*job[:6], weights=True))
+    torch.cuda.synchronize()
+    for i, job in enumerate(jobs):
+        for out, w in got[i]:
+            assert torch.equal(out, job[6][0]) and torch.equal(w, job[6][1])
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_a_whole_step_captured_and_replayed(kind):
+    """Attention, controls, verification, commit and eviction in one graph that advances its state in place; each
+    replay against the eager calls on a copy of the state."""
+    B, T, H, Hkv, D, page, V, most = 3, 5, 4, 2, 64, 16, 700, 12
+    g = torch.Generator().manual_seed(79)
+
+    def state():
+        cache = rsv.new_cache(B, B * most, Hkv, D, page=page, max_blocks=most, max_new=T, kind=kind)
+        cache.block_table.copy_(torch.arange(B * most, dtype=torch.int32).view(B, most))
+        z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+        return dict(cache=cache, positions=z(B), blocks=z(B), totals=torch.zeros((B, most), device="cuda"))
+
+    inputs = dict(qkv=torch.zeros((B, T, H + 2 * Hkv, D), dtype=BF16, device="cuda"),
+                  draft=torch.zeros((B, T - 1, V), dtype=BF16, device="cuda"),
+                  tokens=torch.zeros((B, T - 1), dtype=torch.int32, device="cuda"),
+                  uniforms=torch.zeros((B, T), device="cuda"))
+    head = (torch.randn((H * D, V), generator=g) * 0.02).cuda()
+    presence, temperature = torch.full((B,), 0.3, device="cuda"), torch.full((B,), 1.0, device="cuda")
+
+    def step(s, x):
+        q, kn, vn = x["qkv"][:, :, :H], x["qkv"][:, :, H:H + Hkv], x["qkv"][:, :, H + Hkv:]
+        out, w = rsv.cache_attention(q, kn, vn, s["cache"], s["positions"], s["blocks"], weights=True)
+        target = (out.reshape(B, T, H * D).float() @ head).to(BF16)
+        rsv.adjust_logits(target, x["tokens"], presence=presence, out=target)
+        res, num = rsv.verify(target, x["draft"], x["tokens"], x["uniforms"], temperature)
+        rsv.cache_commit(s["cache"], kn, vn, num, s["positions"], s["blocks"], weights=w, totals=s["totals"],
+                         positions_out=s["positions"], blocks_out=s["blocks"], totals_out=s["totals"])
+        table = s["cache"].block_table
+        gone = rsv.cache_evict(table, s["totals"], s["blocks"], 3, keep_first=1, keep_last=1, table_out=table,
+                               totals_out=s["totals"], blocks_out=s["blocks"])[3]
+        return out, w, target, num, gone
+
+    mine, other = state(), state()
+    step(mine, inputs)                                  # the kernels and workspaces are loaded
+    mine = state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step(mine, inputs)
+    mine["positions"].zero_()
+    advanced = evicted = 0
+    for i in range(60):
+        inputs["qkv"].copy_(torch.randn(inputs["qkv"].shape, generator=g))
+        inputs["draft"].copy_(0.3 * torch.randn(inputs["draft"].shape, generator=g))
+        inputs["tokens"].copy_(torch.randint(0, V, inputs["tokens"].shape, generator=g))
+        inputs["uniforms"].copy_(torch.rand(inputs["uniforms"].shape, generator=g))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(other, inputs)
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), i
+        for k in ("positions", "blocks", "totals"):
+            assert torch.equal(mine[k], other[k]), (i, k)
+        for k in ("block_table", "k_pages", "v_pages", "k_scale", "v_scale", "k_tail", "v_tail"):
+            assert torch.equal(getattr(mine["cache"], k), getattr(other["cache"], k)), (i, k)
+        advanced += int(want[3].sum()) + B
+        evicted += int(want[4].sum())
+    assert int(mine["positions"].sum()) == advanced and evicted > 0
