@@ -410,6 +410,9 @@ const char* spec_verify_status_string(int status);
  * yang di-commit"), and eviction of the blocks that drew the least attention
  * (spec_verify_evict).
  *
+ * A prompt enters the same way, as chains of up to SV_MAX_K + 1 tokens that
+ * are all accepted.
+ *
  * The rules at the top of this file hold: device pointers owned by the
  * caller, no allocation, no synchronisation, kernels only on `stream`, whose
  * device must be the current one; device data is not validated, but every
@@ -633,7 +636,10 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
  * totals, totals_out [B, max_blocks] float32, both or none: totals_out[b][j]
  *              is totals[b][j] plus the weights of block j from the committed
  *              tokens for the blocks that row b had, 0 for the rest.  They may
- *              be the same array.
+ *              be the same array.  So a total counts what a block drew since it
+ *              was complete, not what its tokens drew in the tail: a new block
+ *              starts from 0, and spec_verify_evict's keep_last keeps it until
+ *              it has drawn some.
  * Beyond that no output may overlap an input or another output.
  */
 int spec_verify_commit(const void* k_new, const void* v_new, int64_t kv_row,

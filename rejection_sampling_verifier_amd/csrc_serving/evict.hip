@@ -13,7 +13,11 @@
 // once, a block's rank is a count over its wave's ballot and one prefix sum
 // over the waves' counts, and nothing needs to be kept aside when the table is
 // rewritten in place.  Longer rows are streamed (256 rows of up to 8191
-// blocks: 31 us streamed, 18 us from registers).
+// blocks: 31 us streamed, 18 us from registers).  Each kernel up to the size
+// that it holds, against the next larger one at that size (one row, us):
+// 256 blocks 6.0 and 6.7, 1024 8.0 and 7.8, 4096 9.7 and 10.7, 8192 13.2 and
+// 14.7, 12288 17.3 and 18.9; of 256 rows 6.5 and 7.1, 8.6 and 8.6, 11.4 and
+// 12.3, 17.4 and 18.5, 22.3 and 23.2.
 
 #include <climits>
 
