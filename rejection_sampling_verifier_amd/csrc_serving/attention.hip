@@ -48,13 +48,13 @@ constexpr int CMIN = 4;        // tiles of a run at least: one per wave
 // Two, each with a whole tile on its way, beat three of half the registers
 // (16 rows of up to 16k tokens, one query each, D = 128: 76 against 83 us).
 constexpr int RESIDENT = 2;
-constexpr float GROW = 8.f;    // a maximum may lag this much (a factor of 256) before the sums are rescaled
+constexpr float GROW = 4.f;    // a maximum may lag this much (a factor of 16) before the sums are rescaled
 // Where f16 takes probabilities times value scales: a tile's largest of both
 // makes 2^(MID - HALF) to 2^(MID + HALF + 1), at most 2^15 and, as f16's
 // smallest step is 2^-24, a probability is off by at most 2^-21 of the
 // largest, where scales differ by a factor of 2^(ALIKE + 1) by 2^-16.
-constexpr float MID = 5.f, HALF = 9.f;
-// Tail and new tokens: 2^x that the sums take, so that 2^8 (GROW) times 320 of
+constexpr float MID = 5.f, HALF = 9.f, STEP = 3.f;
+// Tail and new tokens: 2^x that the sums take, so that 2^GROW times 320 of
 // them times the largest bf16 stay below 2^127.
 constexpr int NEAR_X = -18;
 constexpr float ALIKE = 4.f;   // value scales of one tile that differ by 2^5 and more need more range than f16 has
@@ -408,9 +408,10 @@ __device__ __forceinline__ ValueScale value_scale(float v, bool any) {
 // scale (their product lies at 2^e before x), up and down, the float32 sums
 // with it, whatever the scales of the tiles before were.  x and the running
 // maximum move apart: a probability in the denominator does not depend on any
-// value scale.  They move seldom (18 binades of e are one x).  One maximum of
-// score and scale together costs less (32 trees of 61 nodes: 156 against 166
-// us; 64 chains over 8192 keys: 119 against 122) and loses every cached value
+// value scale.  18 binades of e are one x, so it moves seldom: 32 trees of 61
+// nodes take 166 us with scores of a standard deviation of 1, 172 with 4 and
+// 182 with 16; 64 chains over 8192 keys 122, 124 and 125.  One maximum of score
+// and scale together takes 156 and 119 us at any, and loses every cached value
 // of a wave that is small beside its tail's or another block's.
 template <int D, int NQ>
 __device__ __forceinline__ void softmax_cached(State<D, NQ>& st, int n, const float (&s)[16], float c, const ValueScale& v,
@@ -423,31 +424,43 @@ __device__ __forceinline__ void softmax_cached(State<D, NQ>& st, int n, const fl
   // Plain bit operations: branches would part the tile's instructions.
   if (__any(lags(st, n, mx) | off_range())) {
     const bool fresh = __all(st.m[n] == NEG_INF);  // the sums are zero
-    float f = follow(st, n, mx);
+    const float f = follow(st, n, mx);
     const float e = fmaxf(mx - st.m[n], LOW) + top;
-    int dx = mx > NEG_INF && off_range() ? (int)rintf(MID - e) - st.x(n) : 0;
+    // No further than needed, so that high and low tiles in turn find one x;
+    // the first tile with room for a maximum that lags.
+    const float y = e + (float)st.x(n);
+    const float to = y > MID ? MID + HALF - STEP : st.x(n) == NEAR_X ? MID + HALF - GROW : MID - HALF + STEP;
+    int dx = mx > NEG_INF && off_range() ? (int)rintf(to - e) - st.x(n) : 0;
     if (!fresh) {
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= f;
       if (__any(dx != 0)) {
         float big = 0.f;
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float y = fabsf(st.o[dt][n][r]);
-            big = fmaxf(big, y == __builtin_inff() ? 0.f : y);
-          }
+          for (int r = 0; r < 4; ++r) big = fmaxf(big, fabsf(st.o[dt][n][r]));
+        if (__any(big == __builtin_inff())) {  // an infinite tail or new value: the others go by themselves
+          big = 0.f;
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float y = fabsf(st.o[dt][n][r]);
+              big = fmaxf(big, y == __builtin_inff() ? 0.f : y);
+            }
+        }
         big = groups_max(big);
         if (big > 0.f) dx = min(dx, TOP - __builtin_amdgcn_frexp_expf(big));
-      }
-      int left = dx;
-      do {  // once, but between the ends of float32's range
-        const int step = min(max(left, -120), 120);
-        f = ldexpf(f, step);
-        left -= step;
+        int left = dx;
+        do {  // once, but between the ends of float32's range
+          const int step = min(max(left, -120), 120);
+          left -= step;
+          const float k = ldexpf(1.f, step);
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= f;
-        f = 1.f;
-      } while (__any(left != 0));
+          for (int dt = 0; dt < D / 16; ++dt) st.o[dt][n] *= k;
+        } while (__any(left != 0));
+      }
     }
     st.set_x(n, st.x(n) + dx);
   }
