@@ -8,6 +8,7 @@ import pytest
 
 import rejection_sampling_verifier_amd as rsv
 from rejection_sampling_verifier_amd import binding as B
+from tests.test_serving_resources import kernels  # noqa: F401
 from tests.test_serving_abi import OUT, P, WEIGHTS, adjust, attention, cache, commit, evict
 
 
@@ -90,3 +91,10 @@ def test_rows_of_2_to_the_30_entries_are_refused():
 def test_new_cache_refuses_empty_sizes(bad):
     with pytest.raises(ValueError):
         rsv.new_cache(**dict(dict(B=1, num_pages=4, Hkv=1, D=64, page=16), **bad))
+
+
+def test_four_adjusting_work_groups_to_a_cu(kernels):  # noqa: F811
+    mine = [v for k, v in kernels.items() if "adjust_logits_kernel" in k]
+    assert len(mine) == 2
+    for v in mine:
+        assert int(v["Occupancy [waves/SIMD]"]) >= 4 and 4 * int(v["LDS Size [bytes/block]"]) <= 160 * 1024, v
