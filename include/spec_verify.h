@@ -410,8 +410,10 @@ const char* spec_verify_status_string(int status);
  * yang di-commit"), and eviction of the blocks that drew the least attention
  * (spec_verify_evict).
  *
- * A prompt enters the same way, as chains of up to SV_MAX_K + 1 tokens that
- * are all accepted.
+ * A prompt enters in one call (spec_verify_append), or as chains of up to
+ * SV_MAX_K + 1 tokens that are all accepted.  Keys are rotated by their
+ * positions before they meet the cache (spec_verify_rotate,
+ * spec_verify_append).
  *
  * The rules at the top of this file hold: device pointers owned by the
  * caller, no allocation, no synchronisation, kernels only on `stream`, whose
@@ -681,6 +683,98 @@ int spec_verify_evict(const float* totals, const int32_t* block_table,
                       int keep_first, int keep_last, float* totals_out,
                       int32_t* table_out, int32_t* blocks_out,
                       int32_t* evicted, hipStream_t stream);
+
+/*
+ * sv_rotary - the rotation of queries and keys by their positions.  The
+ * first `dims` channels of a head are dims / 2 pairs: channels i and i + dims
+ * / 2, or 2 i and 2 i + 1 where interleaved is 1.  Pair i (a, b) of a token at
+ * position p becomes
+ *   (a cos x - b sin x, b cos x + a sin x),  x = p freqs[i]
+ * with x, its cosine and its sine in 64 bits, the last two rounded to float32,
+ * the products and sums in float32 and the result rounded to bf16.  The other
+ * channels stay as they are.
+ *
+ * freqs        [dims / 2] float32 device.  dims a multiple of 16, at most D.
+ * ids          [num_axes, B, T] int32 device, or NULL.  Positions of their
+ *              own for each token, one number for each axis (time, height and
+ *              width of a picture's or video's tokens); pair i goes by axis
+ *              axes[i] (taken into [0, num_axes)).  NULL: the position that
+ *              each call describes.
+ * axes         [dims / 2] int32 device, or NULL (axis 0).  Needs ids.
+ * num_axes     1 .. 16; read only with ids.
+ */
+typedef struct {
+  const float* freqs;
+  const int32_t* ids;
+  const int32_t* axes;
+  int num_axes, dims, interleaved;
+} sv_rotary;
+
+/*
+ * spec_verify_rotate - the queries and keys of a step rotated by their
+ * positions, as spec_verify_attention takes them.
+ *
+ * Token t of row b is at position positions[b] + t, of a tree (parents given)
+ * at positions[b] + the number of steps on its path from the root (0 where the
+ * path starts at the node itself), or where rotary->ids says.
+ *
+ * q            element (b, t, h, d) at b * q_row + t * q_tok + h * D + d, bf16;
+ *              k likewise, with Hkv heads.  Views of one projection's output
+ *              will do; 16-byte aligned, strides multiples of 8.
+ * q_out, k_out likewise.  Each may be its input itself, with the same strides;
+ *              beyond that neither may overlap the other or an input (the
+ *              views of one tensor may lie between each other).
+ * positions    [B] int32, the tokens before the step (a cache's); may be NULL
+ *              with ids.
+ * parents      [B, T] int32 or NULL, as in spec_verify_attention.
+ * query_lens   [B] int32 or NULL: row b has only that many (0 .. T) tokens;
+ *              what lies behind them is not read and not written.
+ * B, T, H, Hkv >= 1, T at most SV_MAX_NODES with parents; D a multiple of 16,
+ * at most 512.  One kernel, no workspace.
+ */
+int spec_verify_rotate(const void* q, int64_t q_row, int64_t q_tok,
+                       const void* k, int64_t k_row, int64_t k_tok,
+                       const sv_rotary* rotary, const int32_t* positions,
+                       const int32_t* parents, const int32_t* query_lens,
+                       int B, int T, int H, int Hkv, int D, void* q_out,
+                       int64_t qo_row, int64_t qo_tok, void* k_out,
+                       int64_t ko_row, int64_t ko_tok, hipStream_t stream);
+
+/*
+ * spec_verify_append - a prompt's keys and values enter the cache, the keys
+ * rotated on the way: what spec_verify_rotate and then spec_verify_commit of
+ * chains that are all accepted would leave, bit for bit, for any number of
+ * tokens.
+ *
+ * Row b appends its first lens[b] tokens (lens NULL: all T), token t at
+ * position positions[b] + t or where rotary->ids says.  A row is left as it
+ * was, its counters repeated, where lens[b] is outside [0, T], a counter is
+ * out of range or a completed block has no page.
+ *
+ * k, v         element (b, t, h, d) at b * kv_row + t * kv_tok + h * D + d,
+ *              bf16, as spec_verify_attention's k_new and v_new.  Tokens behind
+ *              lens[b] are not read.
+ * rotary       NULL: the keys are rotated already (or need not be).
+ * cache        with any tail.  The tokens after the last full block overwrite
+ *              the tail's old ones where the ring is shorter than page - 1 +
+ *              lens[b]; such an append cannot be undone by keeping the counters
+ *              from before it.  Pages in reserve as spec_verify_commit has it.
+ * k_out        the keys as they enter the cache, at b * ko_row + t * ko_tok +
+ *              h * D + d, or NULL; may be k itself with the same strides.
+ *              Rows that are left as they were, and what lies behind lens[b],
+ *              are not written.
+ * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
+ *              a second kernel updates them).  Beyond that no output may
+ *              overlap an input or another output.
+ * T in [1, 2^24]; B (page - 1 + T) / page Hkv < 2^24.
+ */
+int spec_verify_append(const void* k, const void* v, int64_t kv_row,
+                       int64_t kv_tok, int T, const int32_t* lens,
+                       const sv_rotary* rotary, const sv_cache* cache,
+                       const int32_t* positions, const int32_t* blocks,
+                       int32_t* positions_out, int32_t* blocks_out,
+                       void* k_out, int64_t ko_row, int64_t ko_tok,
+                       hipStream_t stream);
 
 #ifdef __cplusplus
 }

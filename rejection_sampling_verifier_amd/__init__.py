@@ -40,9 +40,11 @@ from .serving_ops import (  # noqa: F401
     KVCache,
     adjust_logits,
     attention_workspace_bytes,
+    cache_append,
     cache_attention,
     cache_commit,
     cache_evict,
     new_attention_workspace,
     new_cache,
+    rotate_tokens,
 )

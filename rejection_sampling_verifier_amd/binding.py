@@ -67,6 +67,12 @@ class SvCache(ctypes.Structure):
                [(n, ctypes.c_int) for n in ("B", "num_pages", "Hkv", "D", "page", "max_blocks", "tail", "kind")]
 
 
+class SvRotary(ctypes.Structure):
+    """sv_rotary of spec_verify.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("freqs", "ids", "axes")] + \
+               [(n, ctypes.c_int) for n in ("num_axes", "dims", "interleaved")]
+
+
 _lib = None
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)
 _COMMON = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
@@ -116,6 +122,12 @@ def load_library(path: str | None = None):
     lib.spec_verify_commit.restype = _i32
     lib.spec_verify_evict.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
     lib.spec_verify_evict.restype = _i32
+    lib.spec_verify_rotate.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, ctypes.POINTER(SvRotary), _vp, _vp, _vp, _i32,
+                                       _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp]
+    lib.spec_verify_rotate.restype = _i32
+    lib.spec_verify_append.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, ctypes.POINTER(SvRotary), ctypes.POINTER(SvCache),
+                                       _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp]
+    lib.spec_verify_append.restype = _i32
     lib.spec_verify_launches.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.spec_verify_launches.restype = _i32
     lib.spec_verify_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]

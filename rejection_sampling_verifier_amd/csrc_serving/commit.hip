@@ -19,7 +19,7 @@
 
 #include <climits>
 
-#include "cache.h"
+#include "quantise.h"
 
 using namespace sv;
 using namespace svr;
@@ -82,33 +82,6 @@ __device__ __forceinline__ void row_path(const CommitArgs& a, int b, Commit& r, 
   __syncthreads();
   if (*bad) r.n = r.filled = 0;
 }
-
-__device__ __forceinline__ float bf16_at(const u32x4& v, int k) { return Tr<uint16_t>::at(v, k); }
-
-// The scale of a block whose largest magnitude has these bf16 bits.
-template <int KIND>
-__device__ __forceinline__ float scale_of(uint32_t top) {
-  if (top >= 0x7F80u) return __uint_as_float(0x7FC00000u);
-  if (top == 0) return 1.f;
-  const float a = __uint_as_float(top << 16);
-  if (KIND == SV_INT8) return fmaxf(a / 127.f, 0x1p-126f);
-  // a = 1.m 2^e and 448 = 1.75 2^8
-  const int e = (int)(top >> 7) - 127 - ((top & 0x7Fu) <= 0x60u ? 8 : 7);
-  return ldexpf(1.f, max(e, -126));
-}
-
-template <int KIND>
-__device__ __forceinline__ uint32_t code8(float x, float scale, float inv) {
-  if (KIND == SV_E4M3) return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x * inv, 0.f, 0, false) & 0xFFu;
-  float r = rintf(x / scale);
-  const float d = fmaf(-r, scale, x), h = 0.5f * scale;  // both exact
-  const bool odd = ((int)r & 1) != 0;
-  if (d > h || (d == h && odd)) r += 1.f;
-  else if (d < -h || (d == -h && odd)) r -= 1.f;
-  return (uint32_t)(int)r & 0xFFu;
-}
-
-constexpr int TPAD = 16;  // bytes between the channels of the transposing buffer
 
 template <int KIND, int D, int PAGE>
 __global__ __launch_bounds__(WG) void cache_commit_kernel(CommitArgs a) {

@@ -13,7 +13,7 @@ import operator
 
 import torch
 
-from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, _cached_workspace, _check, _dtype_code,
+from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvRotary, _cached_workspace, _check, _dtype_code,
                       _OnStream, _stream_handle, load_library)
 
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
@@ -436,4 +436,116 @@ def cache_evict(block_table, totals, blocks, budget, *, keep_first=0, keep_last=
         _check(load_library().spec_verify_evict(
             totals.data_ptr(), block_table.data_ptr(), blocks.data_ptr(), B, most, budget, keep_first, keep_last,
             outs[1].data_ptr(), outs[0].data_ptr(), outs[2].data_ptr(), outs[3].data_ptr(), handle))
+    return tuple(outs)
+
+
+def _rotary(freqs, interleaved, axes, ids, B, T, D, dev):
+    """sv_rotary, checked against tokens [B, T] of D channels."""
+    _need("freqs", freqs, (None,), torch.float32, dev)
+    dims = 2 * freqs.shape[0]
+    if dims < 1 or dims > D:
+        raise ValueError(f"freqs must hold 1 to {D // 2} frequencies")
+    if ids is not None:
+        _need("ids", ids, (None, B, T), torch.int32, dev)
+        if ids.shape[0] < 1:
+            raise ValueError("ids must have at least one axis")
+    elif axes is not None:
+        raise ValueError("axes needs ids")
+    _maybe("axes", axes, (dims // 2,), torch.int32, dev)
+    return SvRotary(freqs.data_ptr(), _p(ids), _p(axes), 0 if ids is None else ids.shape[0], dims, int(bool(interleaved)))
+
+
+def _bf16_tokens(name, t):
+    """Sizes of a [B, T, heads, D] bf16 tensor on a GPU."""
+    _gpu(t, name)
+    if t.dim() != 4 or 0 in t.shape:
+        raise ValueError(f"{name} must be [B, T, heads, D]")
+    return tuple(t.shape)
+
+
+def rotate_tokens(q, k, freqs, positions=None, *, interleaved=False, axes=None, ids=None, parents=None,
+                  query_lens=None, q_out=None, k_out=None, stream=None):
+    """spec_verify_rotate: a step's queries and keys rotated by their positions
+    (see sv_rotary in the header).
+
+    q [B, T, H, D], k [B, T, Hkv, D] bf16, views with D-sized heads side by
+    side; freqs [dims / 2] fp32; positions [B] int32 (a cache's), needed
+    without ids; ids [axes, B, T] int32 with axes [dims / 2] int32: positions
+    of several axes; parents [B, T] int32 for trees; query_lens [B] int32.
+
+    Returns (q_out, k_out): new contiguous tensors (zeros behind query_lens),
+    or the given ones, which may be q and k themselves.
+    """
+    B, T, H, D = shape = _bf16_tokens("q", q)
+    dev = q.device
+    if _bf16_tokens("k", k)[:2] != (B, T) or k.shape[3] != D:
+        raise ValueError("k must be [B, T, Hkv, D] with q's B, T and D")
+    kv = tuple(k.shape)
+    strides = [_token_strides("q", q, shape, dev), _token_strides("k", k, kv, dev)]
+    rot = _rotary(freqs, interleaved, axes, ids, B, T, D, dev)
+    if positions is None and ids is None:
+        raise ValueError("positions are needed without ids")
+    _maybe("positions", positions, (B,), torch.int32, dev)
+    _maybe("parents", parents, (B, T), torch.int32, dev)
+    _maybe("query_lens", query_lens, (B,), torch.int32, dev)
+    handle, scope = _scope(dev, stream)
+    with scope:
+        make = torch.empty if query_lens is None else torch.zeros
+        outs = []
+        for name, t, s in (("q_out", q_out, shape), ("k_out", k_out, kv)):
+            if t is None:
+                t = make(s, dtype=torch.bfloat16, device=dev)
+            strides.append(_token_strides(name, t, s, dev))
+            outs.append(t)
+        _check(load_library().spec_verify_rotate(
+            q.data_ptr(), *strides[0], k.data_ptr(), *strides[1], ctypes.byref(rot), _p(positions), _p(parents),
+            _p(query_lens), B, T, H, kv[2], D, outs[0].data_ptr(), *strides[2], outs[1].data_ptr(), *strides[3],
+            handle))
+    return tuple(outs)
+
+
+def cache_append(cache, k, v, positions, blocks, *, lens=None, freqs=None, interleaved=False, axes=None, ids=None,
+                 k_out=None, positions_out=None, blocks_out=None, stream=None):
+    """spec_verify_append: a prompt's keys and values enter the cache, the keys
+    rotated on the way (see the header).
+
+    k, v [B, T, Hkv, D] bf16 as cache_attention's k_new and v_new, T of any
+    length; lens [B] int32: each row's tokens; freqs, interleaved, axes, ids as
+    rotate_tokens' (no freqs: the keys are taken as they are); k_out [B, T,
+    Hkv, D]: gets the rotated keys (k itself will do).
+
+    Writes the cache's pages, scales and tails, and returns (positions,
+    blocks): new tensors, or the given outs, which may be the inputs.
+    """
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    dev, B, i32 = cache.device, cache.B, torch.int32
+    if not isinstance(k, torch.Tensor) or k.dim() != 4 or 0 in k.shape:
+        raise ValueError("k must be [B, T, Hkv, D]")
+    T = k.shape[1]
+    shape = (B, T, cache.Hkv, cache.D)
+    kv = _token_strides("k", k, shape, dev)
+    if _token_strides("v", v, shape, dev) != kv:
+        raise ValueError("k and v must have the same strides")
+    out = (0, 0) if k_out is None else _token_strides("k_out", k_out, shape, dev)
+    _need("positions", positions, (B,), i32, dev)
+    _need("blocks", blocks, (B,), i32, dev)
+    _maybe("lens", lens, (B,), i32, dev)
+    rot = None
+    if freqs is not None:
+        rot = ctypes.byref(_rotary(freqs, interleaved, axes, ids, B, T, cache.D, dev))
+    elif axes is not None or ids is not None:
+        raise ValueError("axes and ids need freqs")
+    handle, scope = _scope(dev, stream)
+    with scope:
+        outs = []
+        for name, t in (("positions_out", positions_out), ("blocks_out", blocks_out)):
+            if t is None:
+                t = torch.empty_like(positions)
+            else:
+                _need(name, t, (B,), i32, dev)
+            outs.append(t)
+        _check(load_library().spec_verify_append(
+            k.data_ptr(), v.data_ptr(), *kv, T, _p(lens), rot, cache._ref, positions.data_ptr(), blocks.data_ptr(),
+            outs[0].data_ptr(), outs[1].data_ptr(), _p(k_out), *out, handle))
     return tuple(outs)
