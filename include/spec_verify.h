@@ -776,6 +776,68 @@ int spec_verify_append(const void* k, const void* v, int64_t kv_row,
                        void* k_out, int64_t ko_row, int64_t ko_tok,
                        hipStream_t stream);
 
+/*
+ * spec_verify_sample - tokens drawn from logits: drafts (several siblings of a
+ * node at once), or the next tokens of rows without drafts.
+ *
+ * Position i of row b goes by the row's rules.  With its tokens in the order
+ * of their logits (larger first, of equal ones the lower id first), w(x) =
+ * exp((l(x) - max l) / temperature[b]) and the mass of a set the sum of its
+ * w:
+ *   top_k   the first top_k[b] tokens stay (0 or less, V or more: all)
+ *   top_p   of those, each before which less than top_p[b] of their mass lies;
+ *           the first one always (1 or more, NaN: all)
+ *   min_p   of those, each with w >= min_p[b], taken as at most 1 (0 or less,
+ *           NaN: all)
+ * Draw j is the smallest kept id x for which the mass of the kept ids up to x
+ * exceeds uniforms[b][i][j] times the mass of all kept: spec_verify's draw,
+ * and with top_k alone spec_verify's truncated draft.  Weights are formed in
+ * float64; where rules cut a row masses are whole multiples of 2^-43, so a
+ * result does not depend on any order of summation.
+ * Rows with T <= 0 (or NaN) take the largest logit's lowest id.  A NaN logit
+ * counts as -inf and -inf is never drawn; where there is nothing else the
+ * token is -1 and its logprob -inf.
+ *
+ * logits       element (b, i, x) at b * row_stride + i * stride + x, of the
+ *              stated dtype and aligned to it; strides in elements, stride >=
+ *              V.
+ * uniforms     [B, P, n] float32 in [0, 1) (taken into it).
+ * temperature  [B] float32; top_k [B] int32, top_p, min_p [B] float32, or
+ *              NULL.
+ * tokens       [B, P, n] int32.
+ * logprobs     [B, P, n] float32 or NULL: ln of each token's part of the kept
+ *              mass, 0 for greedy rows.
+ * workspace, workspace_bytes  as spec_verify, but it need not be zero-filled.
+ * B, P >= 1; V in [1, 2^20]; n in [1, SV_MAX_NODES].  Two kernels.
+ */
+int spec_verify_sample(const void* logits, int64_t row_stride, int64_t stride,
+                       const float* uniforms, const float* temperature,
+                       const int32_t* top_k, const float* top_p,
+                       const float* min_p, int B, int P, int V, int n,
+                       int dtype, int32_t* tokens, float* logprobs,
+                       void* workspace, size_t* workspace_bytes,
+                       hipStream_t stream);
+
+/*
+ * spec_verify_truncate - the logits of tokens that spec_verify_sample's rules
+ * leave out become -inf, the others keep their bits: spec_verify on target (or
+ * draft) logits cut so verifies against the distribution that
+ * spec_verify_sample draws from.  Greedy rows, and rows that no rule cuts, are
+ * not changed.
+ *
+ * out          element (b, i, x) at b * out_row_stride + i * out_stride + x.  It
+ *              may be the logits themselves with the same strides; otherwise it
+ *              must not overlap them.
+ * Other arguments as spec_verify_sample.  Three kernels.
+ */
+int spec_verify_truncate(const void* logits, int64_t row_stride,
+                         int64_t stride, const float* temperature,
+                         const int32_t* top_k, const float* top_p,
+                         const float* min_p, int B, int P, int V, int dtype,
+                         void* out, int64_t out_row_stride, int64_t out_stride,
+                         void* workspace, size_t* workspace_bytes,
+                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,4 +47,8 @@ from .serving_ops import (  # noqa: F401
     new_attention_workspace,
     new_cache,
     rotate_tokens,
+    sample_tokens,
+    sample_workspace_bytes,
+    truncate_logits,
+    truncate_workspace_bytes,
 )

@@ -128,6 +128,12 @@ def load_library(path: str | None = None):
     lib.spec_verify_append.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, ctypes.POINTER(SvRotary), ctypes.POINTER(SvCache),
                                        _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp]
     lib.spec_verify_append.restype = _i32
+    lib.spec_verify_sample.argtypes = [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                       _vp, _sz, _vp]
+    lib.spec_verify_sample.restype = _i32
+    lib.spec_verify_truncate.argtypes = [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _i64,
+                                         _vp, _sz, _vp]
+    lib.spec_verify_truncate.restype = _i32
     lib.spec_verify_launches.argtypes = [_i32, _i32, _i32, _i32, _i32]
     lib.spec_verify_launches.restype = _i32
     lib.spec_verify_plan.argtypes = [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]

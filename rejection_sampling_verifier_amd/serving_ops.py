@@ -13,7 +13,7 @@ import operator
 
 import torch
 
-from .binding import (SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvRotary, _cached_workspace, _check, _dtype_code,
+from .binding import (SV_BF16, SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvRotary, _cached_workspace, _check, _dtype_code,
                       _OnStream, _stream_handle, load_library)
 
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
@@ -549,3 +549,127 @@ def cache_append(cache, k, v, positions, blocks, *, lens=None, freqs=None, inter
             k.data_ptr(), v.data_ptr(), *kv, T, _p(lens), rot, cache._ref, positions.data_ptr(), blocks.data_ptr(),
             outs[0].data_ptr(), outs[1].data_ptr(), _p(k_out), *out, handle))
     return tuple(outs)
+
+
+def _rules(logits, temperature, top_k, top_p, min_p):
+    """Checks of a step's logits and its rows' rules; (B, P, V, dtype code, strides)."""
+    dev = _gpu(logits, "logits")
+    if logits.dim() != 3 or 0 in logits.shape:
+        raise ValueError("logits must be [B, P, V]")
+    B, P, V = logits.shape
+    if max(B, P, V) > 2 ** 31 - 1:
+        raise ValueError(f"logits are too large: {tuple(logits.shape)}")
+    dt = _dtype_code(logits)
+    _need("temperature", temperature, (B,), torch.float32, dev)
+    _maybe("top_k", top_k, (B,), torch.int32, dev)
+    _maybe("top_p", top_p, (B,), torch.float32, dev)
+    _maybe("min_p", min_p, (B,), torch.float32, dev)
+    return B, P, V, dt, _logit_strides("logits", logits)
+
+
+_rule_sizes = {}  # workspace sizes by (kind, B, P, V, dtype, rules)
+
+
+def _rule_workspace(kind, B, P, V, dt, cut, dev, handle, workspace):
+    """The given workspace or one of the call's own, and its size; it need not be zero."""
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        return workspace, ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    key = (B, P, V, dt, cut)
+    n = _rule_sizes.get((kind,) + key)
+    if n is None:
+        if len(_rule_sizes) >= 1024:
+            _rule_sizes.clear()
+        n = _rule_sizes[(kind,) + key] = _rule_bytes(kind, *key)
+    if torch.cuda.is_current_stream_capturing():
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)  # the graph's own
+    else:
+        workspace = _cached_workspace(kind, key, n, dev, handle)
+    return workspace, ctypes.c_size_t(n)
+
+
+def _rule_bytes(kind, B, P, V, dt, cut):
+    size, some = ctypes.c_size_t(0), ctypes.c_void_p(256 if cut else None)
+    lib = load_library()
+    if kind == "sample":
+        _check(lib.spec_verify_sample(None, 0, 0, None, None, some, None, None, B, P, V, 1, dt, None, None, None,
+                                      ctypes.byref(size), None))
+    else:
+        _check(lib.spec_verify_truncate(None, 0, 0, None, some, None, None, B, P, V, dt, None, 0, 0, None,
+                                        ctypes.byref(size), None))
+    return size.value
+
+
+def sample_workspace_bytes(B, P, V, dtype=SV_BF16, *, cut=True):
+    """Bytes of workspace that sample_tokens needs; cut: any of top_k, top_p and min_p is given."""
+    return _rule_bytes("sample", B, P, V, dtype, cut)
+
+
+def truncate_workspace_bytes(B, P, V, dtype=SV_BF16, *, cut=True):
+    """Bytes of workspace that truncate_logits needs; cut: any of top_k, top_p and min_p is given."""
+    return _rule_bytes("truncate", B, P, V, dtype, cut)
+
+
+def sample_tokens(logits, uniforms, temperature, *, top_k=None, top_p=None, min_p=None, logprobs=None, tokens=None,
+                  workspace=None, stream=None):
+    """spec_verify_sample: tokens drawn from what top-k, top-p and min-p leave
+    of the logits (see the header for the rules).
+
+    logits [B, P, V] bf16 or fp32 with contiguous rows (a slice of a padded
+    vocabulary will do); uniforms [B, P, n] fp32: n draws per position;
+    temperature [B] fp32 (0: the largest logit); top_k [B] int32, top_p and
+    min_p [B] fp32.  logprobs: True or a [B, P, n] fp32 tensor to get each
+    token's log-probability among those left.
+
+    Returns tokens [B, P, n] int32, or (tokens, logprobs).
+    """
+    B, P, V, dt, (row, pos) = _rules(logits, temperature, top_k, top_p, min_p)
+    dev = logits.device
+    _need("uniforms", uniforms, (B, P, None), torch.float32, dev)
+    n = uniforms.shape[2]
+    shape = (B, P, n)
+    handle, scope = _scope(dev, stream)
+    with scope:
+        if tokens is None:
+            tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+        else:
+            _need("tokens", tokens, shape, torch.int32, dev)
+        if logprobs is True:
+            logprobs = torch.empty(shape, dtype=torch.float32, device=dev)
+        elif logprobs is False:
+            logprobs = None
+        else:
+            _maybe("logprobs", logprobs, shape, torch.float32, dev)
+        cut = top_k is not None or top_p is not None or min_p is not None
+        workspace, size = _rule_workspace("sample", B, P, V, dt, cut, dev, handle, workspace)
+        _check(load_library().spec_verify_sample(
+            logits.data_ptr(), row, pos, uniforms.data_ptr(), temperature.data_ptr(), _p(top_k), _p(top_p), _p(min_p),
+            B, P, V, n, dt, tokens.data_ptr(), _p(logprobs), workspace.data_ptr(), ctypes.byref(size), handle))
+    return tokens if logprobs is None else (tokens, logprobs)
+
+
+def truncate_logits(logits, temperature, *, top_k=None, top_p=None, min_p=None, out=None, workspace=None, stream=None):
+    """spec_verify_truncate: the logits that top-k, top-p and min-p leave out
+    become -inf (see spec_verify_sample in the header for the rules).
+
+    logits, temperature, top_k, top_p, min_p as sample_tokens'.  Returns
+    ``out`` (a new contiguous [B, P, V] tensor if None; ``out=logits`` works in
+    place).
+    """
+    B, P, V, dt, (row, pos) = _rules(logits, temperature, top_k, top_p, min_p)
+    dev = logits.device
+    handle, scope = _scope(dev, stream)
+    with scope:
+        if out is None:
+            out = torch.empty((B, P, V), dtype=logits.dtype, device=dev)
+        elif (not isinstance(out, torch.Tensor) or tuple(out.shape) != (B, P, V) or out.dtype != logits.dtype
+              or out.device != dev):
+            raise ValueError(f"out must be a {logits.dtype} tensor of shape {(B, P, V)} on {dev}")
+        out_row, out_pos = _logit_strides("out", out)
+        cut = top_k is not None or top_p is not None or min_p is not None
+        workspace, size = _rule_workspace("truncate", B, P, V, dt, cut, dev, handle, workspace)
+        _check(load_library().spec_verify_truncate(
+            logits.data_ptr(), row, pos, temperature.data_ptr(), _p(top_k), _p(top_p), _p(min_p), B, P, V, dt,
+            out.data_ptr(), out_row, out_pos, workspace.data_ptr(), ctypes.byref(size), handle))
+    return out
