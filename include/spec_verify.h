@@ -604,6 +604,50 @@ int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok,
                           hipStream_t stream);
 
 /*
+ * sv_prefix - pages that several rows share: what their prompts have in
+ * common.  Rows starts[i] .. starts[i + 1] - 1 begin with prefix i, the first
+ * blocks[i] pages of table[i]; other rows have none.  A row's own blocks, tail
+ * and new tokens follow it: positions[b] counts the prefix's tokens too,
+ * blocks[b] and block_table[b] only the row's own blocks (the prefix's are, to
+ * its counters, blocks that were evicted), so spec_verify_commit, _append and
+ * _evict go on as they do without one.  The prompt's tokens past the last full
+ * block belong in each row's tail.  No row may have a prefix's page in reserve.
+ *
+ * table        [count, max_blocks] int32 pages of the cache; an entry outside
+ *              [0, num_pages) is not seen.
+ * blocks       [count] int32.
+ * starts       [count + 1] int32, ascending (a prefix may have no rows).
+ * count in [1, 65536], max_blocks in [1, SV_MAX_BLOCKS].
+ */
+typedef struct {
+  const int32_t* table;
+  const int32_t* blocks;
+  const int32_t* starts;
+  int count, max_blocks;
+} sv_prefix;
+
+/*
+ * spec_verify_attention_prefix - spec_verify_attention of rows that share
+ * prefixes: each query sees its row's prefix too, and softmax and weights are
+ * over both.  A prefix's keys are read once for all its rows.  A probability
+ * beside a prefix's value is rounded to 8 bits.
+ *
+ * weights[b][t][j] are those of the row's own blocks.
+ * prefix       NULL: spec_verify_attention.
+ * Other arguments as spec_verify_attention, but the workspace's size also
+ * depends on prefix->count and max_blocks, and a workspace is of one shape of
+ * these too.  (B T H / Hkv / 128 + count) Hkv < 2^23.
+ * Three kernels, four with weights.
+ */
+int spec_verify_attention_prefix(
+    const void* q, int64_t q_row, int64_t q_tok, const void* k_new,
+    const void* v_new, int64_t kv_row, int64_t kv_tok, const sv_cache* cache,
+    const sv_prefix* prefix, const int32_t* positions, const int32_t* blocks,
+    const int32_t* parents, const int32_t* query_lens, int T, int H,
+    float scale, void* out, float* weights, void* workspace,
+    size_t* workspace_bytes, hipStream_t stream);
+
+/*
  * spec_verify_commit - the accepted path's keys and values enter the cache.
  *
  * Row b commits its root and its accepted drafts: n = num_accepted[b] + 1 of

@@ -67,6 +67,12 @@ class SvCache(ctypes.Structure):
                [(n, ctypes.c_int) for n in ("B", "num_pages", "Hkv", "D", "page", "max_blocks", "tail", "kind")]
 
 
+class SvPrefix(ctypes.Structure):
+    """sv_prefix of spec_verify.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "blocks", "starts")] + \
+               [(n, ctypes.c_int) for n in ("count", "max_blocks")]
+
+
 class SvRotary(ctypes.Structure):
     """sv_rotary of spec_verify.h."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("freqs", "ids", "axes")] + \
@@ -117,6 +123,9 @@ def load_library(path: str | None = None):
     lib.spec_verify_attention.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _i64, ctypes.POINTER(SvCache), _vp, _vp,
                                           _vp, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]
     lib.spec_verify_attention.restype = _i32
+    lib.spec_verify_attention_prefix.argtypes = (lib.spec_verify_attention.argtypes[:8] + [ctypes.POINTER(SvPrefix)]
+                                                 + lib.spec_verify_attention.argtypes[8:])
+    lib.spec_verify_attention_prefix.restype = _i32
     lib.spec_verify_commit.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, ctypes.POINTER(SvCache), _vp, _vp, _vp,
                                        _vp, _vp, _vp, _vp, _vp]
     lib.spec_verify_commit.restype = _i32

@@ -32,7 +32,8 @@
 #include <climits>
 #include <type_traits>
 
-#include "cache.h"
+#include "matrix.h"
+#include "prefix.h"
 
 using namespace sv;
 using namespace svr;
@@ -59,7 +60,6 @@ constexpr float MID = 5.f, HALF = 9.f, STEP = 3.f;
 constexpr int NEAR_X = -18;
 constexpr float ALIKE = 4.f;   // value scales of one tile that differ by 2^5 and more need more range than f16 has
 constexpr float LOW = -110.f;  // scores further below the maximum count as this far, so that 2^x stays in float32's range
-constexpr float VMIN = 0x1p-126f;  // smallest value scale told apart (see spec_verify.h)
 constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
 constexpr int TOP = 100;       // sums are not raised above 2^TOP
 constexpr int LOST = -40;
@@ -84,7 +84,8 @@ struct AttnArgs {
   unsigned* arrived; // [B][Hkv][mtiles] parts that are there; zero between calls
   float* part_o;     // [parts][Hkv][mtiles][MT][D] sums of a part of a row, against its maximum
   float* part_ml;    // [parts][Hkv][mtiles][MT][2] {m, l}
-  float* lse;      // [B][Hkv][mtiles * MT] log2 of the softmax denominator
+  float* lse;      // [B][Hkv][mtiles * MT] log2 of the softmax denominator, or NULL
+  float* own;      // [B][T][H][D] the output in float32, in place of out, where a shared prefix is joined later; or NULL
   float* mass;     // [B][Hkv][sub-blocks][mtiles * MT] log2 of a sub-block's sum
   int pshift;      // log2 page
   int sshift;      // log2 of a sub-block's keys: min(page, 64)
@@ -271,72 +272,6 @@ __device__ __forceinline__ float2 pub_load2(const float* p) {
   return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
 }
 
-// ---- lanes 16 and 32 apart --------------------------------------------------
-__device__ __forceinline__ void swap16(float x, float& u, float& v) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  u = __uint_as_float(r[0]);
-  v = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ void swap32(float x, float& u, float& v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  u = __uint_as_float(r[0]);
-  v = __uint_as_float(r[1]);
-}
-__device__ __forceinline__ float sum16(float x) { float u, v; swap16(x, u, v); return u + v; }
-__device__ __forceinline__ float sum32(float x) { float u, v; swap32(x, u, v); return u + v; }
-__device__ __forceinline__ float groups_sum(float x) { return sum32(sum16(x)); }
-__device__ __forceinline__ float groups_max(float x) {
-  float u, v;
-  swap16(x, u, v);
-  x = fmaxf(u, v);
-  swap32(x, u, v);
-  return fmaxf(u, v);
-}
-
-// ---- codes to 16 bits -----------------------------------------------------------
-// Eight codes (two words) as a matrix operand: bf16 beside the queries, f16
-// beside the probabilities.  Both kinds are exact in either.
-template <int KIND>
-__device__ __forceinline__ bf16x8 widen(uint32_t w0, uint32_t w1) {
-  union { bf16x2 p[4]; uint32_t u[4]; bf16x8 v; } r;
-  if (KIND == SV_E4M3) {
-    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, false);
-    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.f, true);
-    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, false);
-    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.f, true);
-  } else {
-    // An int8 is exact in bf16: the upper half of its float32.
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = k < 2 ? w0 : w1;
-      const int s = (k & 1) * 16;
-      const float x = (float)(int8_t)(w >> s), y = (float)(int8_t)(w >> (s + 8));
-      r.u[k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-    }
-  }
-  return r.v;
-}
-template <int KIND>
-__device__ __forceinline__ f16x8 widen_f16(uint32_t w0, uint32_t w1) {
-  union { f16x2 p[4]; f16x8 v; } r;
-  if (KIND == SV_E4M3) {
-    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false);
-    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true);
-    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false);
-    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true);
-  } else {
-    // 0x6400 + u is the f16 1024 + u: with u = code + 128, minus 1152.
-    const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = (k < 2 ? w0 : w1) ^ 0x80808080u;
-      const uint32_t m = __builtin_amdgcn_perm(0x64646464u, w, (k & 1) ? 0x04030402u : 0x04010400u);
-      r.p[k] = __builtin_bit_cast(f16x2, m) - off;
-    }
-  }
-  return r.v;
-}
-__device__ __forceinline__ bf16x8 as_bf16(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 template <int D, int NQ>
 struct State {
@@ -385,17 +320,6 @@ __device__ __forceinline__ void softmax_near(State<D, NQ>& st, int n, const floa
     sum += p[i];
   }
   st.l[n] = fmaf(sum, (float)(1 << -NEAR_X), st.l[n]);
-}
-
-// A block's value scale as 2^e f, 1 <= f < 2.
-struct ValueScale {
-  int e;
-  float log, inv;  // log2 f, 1 / f; -inf and 0 where there is no block
-};
-__device__ __forceinline__ ValueScale value_scale(float v, bool any) {
-  v = !any ? 1.f : v < VMIN ? VMIN : v;
-  const float f = 2.f * __builtin_amdgcn_frexp_mantf(v);
-  return {__builtin_amdgcn_frexp_expf(v) - 1, any ? __builtin_amdgcn_logf(f) : NEG_INF, any ? __builtin_amdgcn_rcpf(f) : 0.f};
 }
 
 // The softmax of a cached tile; the lane holds 16 scores of one query, raw,
@@ -616,10 +540,15 @@ __device__ __forceinline__ const AttnArgs& args_again() {
 
 template <int D>
 __device__ __forceinline__ void store_out(const AttnArgs& a, int b, int h, int qr, int d, f32x4 x) {
+  const int64_t at = (((int64_t)b * a.T + qr / a.G) * a.H + h * a.G + qr % a.G) * D + d;
+  if (a.own) {
+    *reinterpret_cast<f32x4*>(a.own + at) = x;
+    return;
+  }
   union { bf16x2 p[2]; uint2 u; } y;
   y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
   y.p[1] = __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2);
-  *reinterpret_cast<uint2*>(a.out + (((int64_t)b * a.T + qr / a.G) * a.H + h * a.G + qr % a.G) * D + d) = y.u;
+  *reinterpret_cast<uint2*>(a.out + at) = y.u;
 }
 
 template <int KIND, int D, int NQ, bool SMALL>
@@ -1033,7 +962,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     } else {
       const int qr = mt * MT + rr;
       if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x);
-      if (z.mass && d == 0) z.lse[tile * MT + rr] = m + __builtin_amdgcn_logf(l);
+      if (z.lse && d == 0) z.lse[tile * MT + rr] = m + __builtin_amdgcn_logf(l);
     }
   }
   if (nparts > 1) {
@@ -1094,7 +1023,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       for (int v = 0; v < V4; ++v) {
         const int e = v * WG + t, rr = e / (D / 4), d = e % (D / 4) * 4, qr = mt * MT + rr;
         if (qr < nq * z.G) store_out<D>(z, b, h, qr, d, x[v] + 0.f * (1.f / sum[v]));
-        if (z.mass && d == 0) z.lse[tile * MT + rr] = big[v] + __builtin_amdgcn_logf(sum[v]);
+        if (z.lse && d == 0) z.lse[tile * MT + rr] = big[v] + __builtin_amdgcn_logf(sum[v]);
       }
     }
   }
@@ -1132,12 +1061,13 @@ __global__ __launch_bounds__(WG) void attention_weights_kernel(AttnArgs a, int m
 
 struct Plan {
   int nq, mtiles, grid, runs, even, nsub;
-  size_t o, ml, lse, mass, total;
+  size_t o, ml, lse, mass, prefix, total;
+  PrefixPlan shared;
 };
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
+int make_plan(const sv_cache& c, int T, int H, bool weights, const sv_prefix* prefix, Plan& pl) {
   const int M = T * (H / c.Hkv);
   // 64 rows beside D = 128 would leave one wave per SIMD (61-node trees over
   // up to 4k tokens: 261 against 181 us); beside D = 64 they halve the reads
@@ -1165,10 +1095,18 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
   off = align256(off + sizeof(float) * (size_t)parts * mt * c.D);
   pl.ml = off;
   off = align256(off + sizeof(float2) * (size_t)parts * mt);
-  if (weights) {
-    const size_t rows = (size_t)c.B * c.Hkv, mpad = (size_t)pl.mtiles * mt;
+  const size_t rows = (size_t)c.B * c.Hkv, mpad = (size_t)pl.mtiles * mt;
+  if (weights || prefix) {
     pl.lse = off;
     off = align256(off + sizeof(float) * rows * mpad);
+  }
+  if (prefix) {
+    const int rc = prefix_plan(c, *prefix, T, H, pl.shared);
+    if (rc != SV_OK) return rc;
+    pl.prefix = off;
+    off += pl.shared.total;
+  }
+  if (weights) {
     pl.mass = off;
     off = align256(off + sizeof(float) * rows * mpad * (size_t)nsub);
     if (((int64_t)c.B * T * c.max_blocks + WG - 1) / WG > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
@@ -1178,11 +1116,15 @@ int make_plan(const sv_cache& c, int T, int H, bool weights, Plan& pl) {
 }
 
 template <int KIND, int D, int NQ>
-int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
+int launch(const AttnArgs& a, const Plan& pl, const PrefixArgs* prefix, hipStream_t st) {
   void (*const k)(AttnArgs) =
       a.c.page < 64 ? cache_attention_kernel<KIND, D, NQ, true> : cache_attention_kernel<KIND, D, NQ, false>;
   hipLaunchKernelGGL(k, dim3(pl.grid), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
+  if (prefix) {
+    const int rc = prefix_join(*prefix, st);
+    if (rc != SV_OK) return rc;
+  }
   if (a.weights) {
     const int64_t n = (int64_t)a.c.B * a.T * a.c.max_blocks;
     void (*const wk)(AttnArgs, int) = a.G % 4 == 0   ? attention_weights_kernel<4>
@@ -1195,14 +1137,14 @@ int launch(const AttnArgs& a, const Plan& pl, hipStream_t st) {
   return SV_OK;
 }
 template <int KIND, int D>
-int launch_rows(const AttnArgs& a, const Plan& pl, hipStream_t st) {
+int launch_rows(const AttnArgs& a, const Plan& pl, const PrefixArgs* prefix, hipStream_t st) {
   if constexpr (D == 64)
-    if (pl.nq == 4) return launch<KIND, D, 4>(a, pl, st);
-  return pl.nq == 1 ? launch<KIND, D, 1>(a, pl, st) : launch<KIND, D, 2>(a, pl, st);
+    if (pl.nq == 4) return launch<KIND, D, 4>(a, pl, prefix, st);
+  return pl.nq == 1 ? launch<KIND, D, 1>(a, pl, prefix, st) : launch<KIND, D, 2>(a, pl, prefix, st);
 }
 template <int KIND>
-int launch_dim(const AttnArgs& a, const Plan& pl, hipStream_t st) {
-  return a.c.D == 64 ? launch_rows<KIND, 64>(a, pl, st) : launch_rows<KIND, 128>(a, pl, st);
+int launch_dim(const AttnArgs& a, const Plan& pl, const PrefixArgs* prefix, hipStream_t st) {
+  return a.c.D == 64 ? launch_rows<KIND, 64>(a, pl, prefix, st) : launch_rows<KIND, 128>(a, pl, prefix, st);
 }
 
 }  // namespace
@@ -1216,19 +1158,22 @@ static bool crosses(const void* base, int64_t stride, int rows, int64_t span, co
   return first < rows && first * stride < d + n;
 }
 
-extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok, const void* k_new, const void* v_new,
-                                     int64_t kv_row, int64_t kv_tok, const sv_cache* cache, const int32_t* positions,
-                                     const int32_t* blocks, const int32_t* parents, const int32_t* query_lens, int T,
-                                     int H, float scale, void* out, float* weights, void* workspace,
-                                     size_t* workspace_bytes, hipStream_t stream) {
+static int attention(const void* q, int64_t q_row, int64_t q_tok, const void* k_new, const void* v_new, int64_t kv_row,
+                     int64_t kv_tok, const sv_cache* cache, const sv_prefix* prefix, const int32_t* positions,
+                     const int32_t* blocks, const int32_t* parents, const int32_t* query_lens, int T, int H, float scale,
+                     void* out, float* weights, void* workspace, size_t* workspace_bytes, hipStream_t stream) {
   if (!workspace_bytes) return SV_ERR_ARG;
   const int bad = check_cache(cache);
   if (bad != SV_OK) return bad;
   const sv_cache& c = *cache;
+  if (prefix) {
+    const int rc = check_prefix(prefix);
+    if (rc != SV_OK) return rc;
+  }
   if (T < 1 || H < 1 || H % c.Hkv) return SV_ERR_ARG;
   if (T > (parents ? SV_MAX_NODES : SV_MAX_K + 1) || H / c.Hkv > MAX_GROUP) return SV_ERR_UNSUPPORTED;
   Plan pl;
-  const int rc = make_plan(c, T, H, weights != nullptr, pl);
+  const int rc = make_plan(c, T, H, weights != nullptr, prefix, pl);
   if (rc != SV_OK) return rc;
   if (!workspace) {
     *workspace_bytes = pl.total;
@@ -1258,7 +1203,10 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   const Output written[] = {{{out, (size_t)bytes}, nullptr}, {{weights, (size_t)mass}, nullptr}, {{workspace, pl.total}, nullptr}};
   const Array read[] = {{positions, nb}, {blocks, nb}, {query_lens, nb}, {parents, nb * T}, {c.block_table, nb * c.max_blocks},
                         {c.k_pages, pages * c.page * c.D}, {c.v_pages, pages * c.page * c.D}, {c.k_scale, pages * 4},
-                        {c.v_scale, pages * 4}, {c.k_tail, tail}, {c.v_tail, tail}};
+                        {c.v_scale, pages * 4}, {c.k_tail, tail}, {c.v_tail, tail},
+                        {prefix ? prefix->table : nullptr, prefix ? (size_t)prefix->count * prefix->max_blocks * 4 : 0},
+                        {prefix ? prefix->blocks : nullptr, prefix ? (size_t)prefix->count * 4 : 0},
+                        {prefix ? prefix->starts : nullptr, prefix ? (size_t)(prefix->count + 1) * 4 : 0}};
   if (outputs_overlap(written, read)) return SV_ERR_ARG;
   AttnArgs a;
   a.q = static_cast<const uint16_t*>(q);
@@ -1285,11 +1233,56 @@ extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok
   a.arrived = reinterpret_cast<unsigned*>(ws);
   a.part_o = reinterpret_cast<float*>(ws + pl.o);
   a.part_ml = reinterpret_cast<float*>(ws + pl.ml);
-  a.lse = weights ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
+  a.lse = weights || prefix ? reinterpret_cast<float*>(ws + pl.lse) : nullptr;
   a.mass = weights ? reinterpret_cast<float*>(ws + pl.mass) : nullptr;
+  a.own = prefix ? reinterpret_cast<float*>(ws + pl.prefix + pl.shared.own) : nullptr;
   for (a.pshift = 4; 1 << a.pshift < c.page; ++a.pshift) {}
   a.sshift = std::min(a.pshift, 6);
   a.nsub = pl.nsub;
   (void)hipGetLastError();
-  return c.kind == SV_E4M3 ? launch_dim<SV_E4M3>(a, pl, stream) : launch_dim<SV_INT8>(a, pl, stream);
+  PrefixArgs p = {};
+  if (prefix) {
+    p.q = a.q;
+    p.q_row = q_row;
+    p.q_tok = q_tok;
+    p.c = c;
+    p.p = *prefix;
+    p.qlens = query_lens;
+    p.T = T;
+    p.H = H;
+    p.G = a.G;
+    p.pshift = a.pshift;
+    p.qtiles = pl.shared.qtiles;
+    p.splits = pl.shared.splits;
+    p.scale2 = a.scale2;
+    p.part_o = reinterpret_cast<float*>(ws + pl.prefix + pl.shared.o);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.prefix + pl.shared.ml);
+    p.own = a.own;
+    p.lse = a.lse;
+    p.mpad = pl.mtiles * 16 * pl.nq;
+    p.out = a.out;
+    const int first = prefix_launch(p, stream);
+    if (first != SV_OK) return first;
+  }
+  const PrefixArgs* const join = prefix ? &p : nullptr;
+  return c.kind == SV_E4M3 ? launch_dim<SV_E4M3>(a, pl, join, stream) : launch_dim<SV_INT8>(a, pl, join, stream);
+}
+
+extern "C" int spec_verify_attention(const void* q, int64_t q_row, int64_t q_tok, const void* k_new, const void* v_new,
+                                     int64_t kv_row, int64_t kv_tok, const sv_cache* cache, const int32_t* positions,
+                                     const int32_t* blocks, const int32_t* parents, const int32_t* query_lens, int T,
+                                     int H, float scale, void* out, float* weights, void* workspace,
+                                     size_t* workspace_bytes, hipStream_t stream) {
+  return attention(q, q_row, q_tok, k_new, v_new, kv_row, kv_tok, cache, nullptr, positions, blocks, parents, query_lens,
+                   T, H, scale, out, weights, workspace, workspace_bytes, stream);
+}
+
+extern "C" int spec_verify_attention_prefix(const void* q, int64_t q_row, int64_t q_tok, const void* k_new,
+                                            const void* v_new, int64_t kv_row, int64_t kv_tok, const sv_cache* cache,
+                                            const sv_prefix* prefix, const int32_t* positions, const int32_t* blocks,
+                                            const int32_t* parents, const int32_t* query_lens, int T, int H, float scale,
+                                            void* out, float* weights, void* workspace, size_t* workspace_bytes,
+                                            hipStream_t stream) {
+  return attention(q, q_row, q_tok, k_new, v_new, kv_row, kv_tok, cache, prefix, positions, blocks, parents, query_lens,
+                   T, H, scale, out, weights, workspace, workspace_bytes, stream);
 }

@@ -1,0 +1,396 @@
+// Attention over a prefix that several rows share, computed for all of them at
+// once (the prefix of spec_verify_attention_prefix), and its join with what
+// each row has of its own, for gfx950.
+//
+// Mathematics: S = scale Q K^T, online softmax, O = sum exp2(S - m) V, as in
+// attention.hip, but one product holds the queries of all rows that begin with
+// the prefix: n rows with T tokens and H / Hkv heads each are M = n T H / Hkv
+// rows of it per kv head, and each key is read and widened once for MT of
+// them, not once per row.  Parts join as means with the weights that they
+// have.
+//
+// A work-group takes MT = 128 queries, 32 to a wave, and one of S parts of the
+// prefix's keys, in tiles of 64.  The tile's codes come to registers while the
+// tile before is worked on, are widened to bf16 once for the work-group and
+// kept in LDS twice, so that one barrier a tile will do.  The products are
+// transposed, S^T = K Q^T and O^T = V^T P^T, with the keys dealt so that lane
+// group g = lane / 32 of a product has the scores of keys 16 g .. 16 g + 15 of
+// 32, which is the operand that O^T needs: probabilities stay in their lanes.
+// A block's value scale 2^e f goes into the values (2^e, exactly) and into the
+// probabilities (f, below 2), which are rounded to bf16.
+
+#include <algorithm>
+#include <climits>
+
+#include "matrix.h"
+#include "prefix.h"
+
+using namespace sv;
+using namespace svr;
+
+namespace {
+
+constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
+constexpr float GROW = 4.f;      // a maximum may lag this much (a factor of 16) before the sums are rescaled
+constexpr int KEYS = 64;         // of a tile
+constexpr int MT = 32 * NWAVE;   // queries of one
+constexpr int RESIDENT = 2;      // work-groups of a CU, by registers and LDS
+
+// A group's prefix and its rows, brought into range.
+struct Group {
+  int first, rows, blocks, tiles, per, parts;  // per: tiles of a part
+};
+__device__ __forceinline__ Group group_of(const PrefixArgs& a, int g) {
+  Group r;
+  r.first = min(max(a.p.starts[g], 0), a.c.B);
+  r.rows = max(min(max(a.p.starts[g + 1], 0), a.c.B) - r.first, 0);
+  r.blocks = min(max(a.p.blocks[g], 0), a.p.max_blocks);
+  r.tiles = (int)(((int64_t)r.blocks * a.c.page + KEYS - 1) / KEYS);
+  r.per = (r.tiles + a.splits - 1) / a.splits;
+  r.parts = r.per ? (r.tiles + r.per - 1) / r.per : 0;
+  return r;
+}
+
+template <int KIND>
+__device__ __forceinline__ u32x4 widen_by(uint32_t w0, uint32_t w1, float scale) {
+  union { bf16x2 p[4]; u32x4 v; } r;
+  if (KIND == SV_E4M3) {
+    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
+    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
+    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
+    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w = k < 2 ? w0 : w1;
+      const int s = (k & 1) * 16;
+      const float x = (float)(int8_t)(w >> s) * scale, y = (float)(int8_t)(w >> (s + 8)) * scale;
+      r.v[k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+    }
+  }
+  return r.v;
+}
+
+// A tile's place in LDS: pieces of 8 values (16 bytes), piece p of a row at p ^
+// twist, so that the rows that LDS serves together differ in their banks.
+template <int D>
+struct Tile {
+  u32x4 k[KEYS * (D / 8)];   // [key][channel]
+  u32x4 v[D * (KEYS / 8)];   // [channel][key]
+  __device__ __forceinline__ static int at_k(int key, int p) { return key * (D / 8) + (p ^ (key & (D / 8 - 1))); }
+  __device__ __forceinline__ static int at_v(int d, int p) { return d * (KEYS / 8) + (p ^ (d & (KEYS / 8 - 1))); }
+};
+
+template <int KIND, int D>
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RESIDENT))) void prefix_attention_kernel(PrefixArgs a) {
+  constexpr int NP = KEYS * D / 16 / WG;  // 16-byte pieces of K's codes, and of V's, per thread
+  __shared__ Tile<D> sh[2];
+  const int t = threadIdx.x, lane = t & 63, g = lane >> 5, col = lane & 31, w = t >> 6;
+
+  // Which unit: part and head of a prefix first, tiles of queries, which read
+  // the same keys, next to each other on one XCD.
+  const int each = gridDim.x / 8, unit = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+  int qt = unit % a.qtiles;
+  const int h = unit / a.qtiles % a.c.Hkv, part = unit / a.qtiles / a.c.Hkv;
+  if (part >= a.splits) return;
+  // The prefix that the tile of queries belongs to: 64 of them looked up at a time.
+  const int each_row = a.T * a.G;
+  int which = 0;
+  Group grp = {};
+  for (;; which += 64) {
+    if (which >= a.p.count) return;
+    if (which + lane < a.p.count) grp = group_of(a, which + lane);
+    else grp.rows = 0;
+    const int n = (grp.rows * each_row + MT - 1) / MT;  // below 2^23
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(inc, o, 64);
+      if (lane >= o) inc += u;
+    }
+    const uint64_t past = __ballot(qt < inc);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      qt -= __builtin_amdgcn_readlane(inc - n, at);
+      which += at;
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(Group) / 4); ++k)
+        reinterpret_cast<int*>(&grp)[k] = __builtin_amdgcn_readlane(reinterpret_cast<int*>(&grp)[k], at);
+      break;
+    }
+    qt -= __builtin_amdgcn_readlane(inc, 63);
+  }
+  const int tile0 = part * grp.per, tile1 = min(tile0 + grp.per, grp.tiles);
+  if (tile0 >= tile1) return;
+
+  // The lane's query.
+  const int r = qt * MT + w * 32 + col, in = r / each_row, rest = r % each_row, tok = rest / a.G;
+  const int b = grp.first + min(in, grp.rows - 1);
+  const bool live = in < grp.rows && tok < (a.qlens ? min(max(a.qlens[b], 0), a.T) : a.T);
+  const int head = h * a.G + rest % a.G;
+  const bool queries = __any(live);  // a wave without only brings keys
+  bf16x8 q[D / 16];
+  {
+    const uint16_t* from = a.q + b * a.q_row + tok * a.q_tok + (int64_t)head * D + g * 8;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      u32x4 x = {0, 0, 0, 0};
+      if (live) x = *reinterpret_cast<const u32x4*>(from + s * 16);
+      q[s] = __builtin_bit_cast(bf16x8, x);
+    }
+  }
+
+  const int32_t* table = a.p.table + (int64_t)which * a.p.max_blocks;
+  const int keys = grp.blocks * a.c.page;  // at most 2^24
+  auto page_at = [&](int key) { return key < keys ? table[key >> a.pshift] : -1; };
+  auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.c.num_pages; };
+  // The tile on its way: codes, the value scales of the pieces, and of the lane's keys.
+  u32x4 kc[NP], vc[NP];
+  float vw;                  // the value scale of the thread's value pieces
+  float ks[2], vs[2];        // of the lane's keys in each half,
+  bool ok[2];                // where they exist
+  int pk[NP], pv, pl[2];     // pages of the tile after it
+  const int vp = t & 3;      // the keys of the thread's value pieces: 16 vp ..
+  auto find = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) pk[i] = page_at(tile * KEYS + (i * WG + t) / (D / 16));
+    pv = page_at(tile * KEYS + vp * 16);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pl[i] = page_at(tile * KEYS + i * 32 + g * 16);
+  };
+  auto bring = [&](int tile) {
+    const int mask = a.c.page - 1;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int s = i * WG + t, key = tile * KEYS + s / (D / 16), p = s % (D / 16);
+      kc[i] = u32x4{0, 0, 0, 0};
+      if (there(pk[i]))
+        kc[i] = *reinterpret_cast<const u32x4*>(a.c.k_pages + (((int64_t)pk[i] * a.c.Hkv + h) * a.c.page + (key & mask)) * D + p * 16);
+    }
+    vw = 1.f;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int d = (i * WG + t) / 4;
+      vc[i] = u32x4{0, 0, 0, 0};
+      if (there(pv))
+        vc[i] = *reinterpret_cast<const u32x4*>(a.c.v_pages + (((int64_t)pv * a.c.Hkv + h) * D + d) * a.c.page + ((tile * KEYS + vp * 16) & mask));
+    }
+    if (there(pv)) vw = a.c.v_scale[(int64_t)pv * a.c.Hkv + h];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ok[i] = there(pl[i]);
+      ks[i] = ok[i] ? a.c.k_scale[(int64_t)pl[i] * a.c.Hkv + h] : 0.f;
+      vs[i] = ok[i] ? a.c.v_scale[(int64_t)pl[i] * a.c.Hkv + h] : 1.f;
+    }
+  };
+  auto store = [&](Tile<D>& to) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int s = i * WG + t, key = s / (D / 16), p = s % (D / 16) * 2;
+      to.k[Tile<D>::at_k(key, p)] = widen_by<KIND>(kc[i][0], kc[i][1], 1.f);
+      to.k[Tile<D>::at_k(key, p + 1)] = widen_by<KIND>(kc[i][2], kc[i][3], 1.f);
+    }
+    const float by = ldexpf(1.f, value_scale(vw, true).e);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int d = (i * WG + t) / 4;
+      to.v[Tile<D>::at_v(d, vp * 2)] = widen_by<KIND>(vc[i][0], vc[i][1], by);
+      to.v[Tile<D>::at_v(d, vp * 2 + 1)] = widen_by<KIND>(vc[i][2], vc[i][3], by);
+    }
+  };
+
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+  float m = NEG_INF, l = 0.f;  // l: of the lane's own keys
+
+  find(tile0);
+  bring(tile0);
+  find(min(tile0 + 1, tile1 - 1));
+  for (int tile = tile0; tile < tile1; ++tile) {
+    Tile<D>& now = sh[(tile - tile0) & 1];
+    store(now);
+    float c[2];
+    ValueScale sc[2];
+    bool here[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      here[i] = ok[i];
+      c[i] = ok[i] ? ks[i] * a.scale2 : 0.f;
+      sc[i] = value_scale(vs[i], ok[i]);
+    }
+    __syncthreads();
+    if (tile + 1 < tile1) {
+      bring(tile + 1);
+      find(min(tile + 2, tile1 - 1));
+    }
+    if (!queries) continue;
+    f32x16 s[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[i][j] = 0.f;
+      const int key = i * 32 + 16 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, now.k[Tile<D>::at_k(key, ks * 2 + g)]), q[ks],
+                                                       s[i], 0, 0, 0);
+    }
+    float mx = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float top = s[i][0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) top = fmaxf(top, s[i][j]);
+      mx = fmaxf(mx, here[i] ? top * c[i] : NEG_INF);
+    }
+    {
+      float u, v;
+      swap32(mx, u, v);
+      mx = fmaxf(u, v);
+    }
+    if (__any(mx > m + GROW)) {
+      const float to = fmaxf(m, mx), f = to == NEG_INF ? 1.f : exp2_fast(m - to);
+      m = to;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
+    }
+    bf16x8 p[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float off = sc[i].log - fmaxf(m, -FAR);  // -inf where there is no block
+      float x[16], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = exp2_fast(fmaf(s[i][j], c[i], off));
+        sum += x[j];
+      }
+      l = fmaf(sum, sc[i].inv, l);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        union { bf16x2 h[4]; bf16x8 v; } y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.h[j] = __builtin_convertvector(f32x2{x[8 * u + 2 * j], x[8 * u + 2 * j + 1]}, bf16x2);
+        p[i][u] = y.v;
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, now.v[Tile<D>::at_v(dt * 32 + col, i * 4 + g * 2 + u)]), p[i][u], o[dt], 0, 0, 0);
+  }
+  l = sum32(l);
+  if (!live) return;
+  const float whole = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = (((int64_t)part * a.c.B + b) * a.T + tok) * a.H + head;
+  if (g == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 x = {o[dt][4 * i], o[dt][4 * i + 1], o[dt][4 * i + 2], o[dt][4 * i + 3]};
+      *reinterpret_cast<f32x4*>(a.part_o + at * D + dt * 32 + i * 8 + g * 4) = x * whole;
+    }
+}
+
+// out = the mean of what a row has of its own and of its prefix's parts, each
+// with its weight; D / 4 threads for a token's head.
+template <int D>
+__global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
+  const int64_t e = ((int64_t)blockIdx.x * WG + threadIdx.x) / (D / 4);
+  const int d = threadIdx.x % (D / 4) * 4;
+  const int64_t all = (int64_t)a.c.B * a.T * a.H;
+  if (e >= all) return;
+  const int head = (int)(e % a.H), tok = (int)(e / a.H % a.T), b = (int)(e / a.H / a.T);
+  if (a.qlens && tok >= a.qlens[b]) return;
+  // The last group that starts at or before the row.
+  int lo = 0, hi = a.p.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.p.starts[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  const Group g = group_of(a, lo);
+  const int parts = b >= g.first && b < g.first + g.rows ? g.parts : 0;
+  const int64_t at = ((int64_t)b * a.c.Hkv + head / a.G) * a.mpad + tok * a.G + head % a.G;
+  const float own = a.lse[at];
+  f32x4 x = *reinterpret_cast<const f32x4*>(a.own + e * D + d);
+  float top = own;
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[(s * all + e) * 2]);
+  float sum = 0.f;
+  if (own == NEG_INF) {
+    if (top > NEG_INF) x = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else {
+    sum = exp2_fast(own - top);
+    x *= sum;
+  }
+  for (int s = 0; s < parts; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * all + e) * 2);
+    if (ml.x == NEG_INF && !(ml.y != ml.y)) continue;
+    const float f = ml.y * exp2_fast(ml.x - top);
+    sum += f;
+    x += *reinterpret_cast<const f32x4*>(a.part_o + (s * all + e) * D + d) * f;
+  }
+  if (parts) x *= 1.f / sum;
+  union { bf16x2 p[2]; uint2 u; } y;
+  y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
+  y.p[1] = __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2);
+  *reinterpret_cast<uint2*>(a.out + e * D + d) = y.u;
+  if (d == 0 && parts) a.lse[at] = top + __builtin_amdgcn_logf(sum);
+}
+
+}  // namespace
+
+namespace svr {
+
+int check_prefix(const sv_prefix* p) {
+  if (!p || !p->table || !p->blocks || !p->starts || p->count < 1 || p->max_blocks < 1) return SV_ERR_ARG;
+  if (p->count > 65536 || p->max_blocks > SV_MAX_BLOCKS) return SV_ERR_UNSUPPORTED;
+  const void* words[] = {p->table, p->blocks, p->starts};
+  for (const void* w : words)
+    if (reinterpret_cast<uintptr_t>(w) % 4) return SV_ERR_ARG;
+  return SV_OK;
+}
+
+int prefix_plan(const sv_cache& c, const sv_prefix& p, int T, int H, PrefixPlan& pl) {
+  const int64_t m = (int64_t)c.B * T * (H / c.Hkv);  // queries of a kv head, of all groups
+  const int64_t full = (m + MT - 1) / MT;
+  const int64_t qtiles = m / MT + std::min(p.count, c.B);  // each group's last tile may be a part of one
+  // As many parts of the keys as fill the chip once, but none under two tiles.
+  const int64_t tiles = ((int64_t)p.max_blocks * c.page + KEYS - 1) / KEYS;
+  pl.splits = (int)std::max<int64_t>(1, std::min(256 * RESIDENT / (full * c.Hkv), (tiles + 1) / 2));
+  const int64_t grid = qtiles * c.Hkv * pl.splits;
+  if (grid > (1 << 23)) return SV_ERR_UNSUPPORTED;
+  pl.qtiles = (int)qtiles;
+  const size_t rows = (size_t)c.B * T * H, al = 255;
+  pl.o = 0;
+  pl.ml = (rows * pl.splits * c.D * sizeof(float) + al) / 256 * 256;
+  pl.own = pl.ml + (rows * pl.splits * 2 * sizeof(float) + al) / 256 * 256;
+  pl.total = pl.own + (rows * c.D * sizeof(float) + al) / 256 * 256;
+  return SV_OK;
+}
+
+int prefix_launch(const PrefixArgs& a, hipStream_t st) {
+  void (*const k)(PrefixArgs) =
+      a.c.kind == SV_E4M3 ? (a.c.D == 64 ? prefix_attention_kernel<SV_E4M3, 64> : prefix_attention_kernel<SV_E4M3, 128>)
+                          : (a.c.D == 64 ? prefix_attention_kernel<SV_INT8, 64> : prefix_attention_kernel<SV_INT8, 128>);
+  const int64_t grid = ((int64_t)a.qtiles * a.c.Hkv * a.splits + 7) / 8 * 8;
+  hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(WG), 0, st, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+int prefix_join(const PrefixArgs& a, hipStream_t st) {
+  const int64_t n = (int64_t)a.c.B * a.T * a.H * (a.c.D / 4);
+  hipLaunchKernelGGL(a.c.D == 64 ? prefix_join_kernel<64> : prefix_join_kernel<128>, dim3((uint32_t)((n + WG - 1) / WG)),
+                     dim3(WG), 0, st, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+}
+
+}  // namespace svr

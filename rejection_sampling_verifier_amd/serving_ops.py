@@ -13,8 +13,8 @@ import operator
 
 import torch
 
-from .binding import (SV_BF16, SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvRotary, _cached_workspace, _check, _dtype_code,
-                      _OnStream, _stream_handle, load_library)
+from .binding import (SV_BF16, SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvPrefix, SvRotary, _cached_workspace,
+                      _check, _dtype_code, _OnStream, _stream_handle, load_library)
 
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
 
@@ -221,7 +221,7 @@ class KVCache:
                           k_tail.data_ptr(), v_tail.data_ptr(), block_table.data_ptr(), B, pages, Hkv, D, page,
                           self.max_blocks, tail, _KINDS[kind])
         self._ref = ctypes.byref(self._c)
-        self._sizes = {}  # workspace sizes by (T, H, parents, weights)
+        self._sizes = {}  # workspace sizes by (T, H, parents, weights, prefix)
         self._made = True
 
     def __setattr__(self, name, value):
@@ -265,39 +265,65 @@ def _token_strides(name, t, shape, dev):
     return row, tok
 
 
-def _attention_bytes(cache, T, H, tree, weights):
-    key = (T, H, tree, weights)
+def _attention_bytes(cache, T, H, tree, weights, prefix=None):
+    """prefix: None or (count, max_blocks)."""
+    key = (T, H, tree, weights, prefix)
     n = cache._sizes.get(key)
     if n is None:
         size = ctypes.c_size_t(0)
         some = ctypes.c_void_p(256)  # tells the query which arguments the call will have
-        _check(load_library().spec_verify_attention(None, 0, 0, None, None, 0, 0, cache._ref, None, None,
-                                                    some if tree else None, None, T, H, 1.0, None,
-                                                    some if weights else None, None, ctypes.byref(size), None))
+        shared = None if prefix is None else ctypes.byref(SvPrefix(256, 256, 256, *prefix))
+        _check(load_library().spec_verify_attention_prefix(
+            None, 0, 0, None, None, 0, 0, cache._ref, shared, None, None, some if tree else None, None, T, H, 1.0, None,
+            some if weights else None, None, ctypes.byref(size), None))
+        if len(cache._sizes) >= 1024:
+            cache._sizes.clear()
         n = cache._sizes[key] = size.value
     return n
 
 
-def attention_workspace_bytes(cache, T, H, *, tree=False, weights=False):
-    """Bytes of workspace that cache_attention needs for T new tokens and H heads."""
-    return _attention_bytes(cache, T, H, tree, weights)
+def attention_workspace_bytes(cache, T, H, *, tree=False, weights=False, prefix=None):
+    """Bytes of workspace that cache_attention needs for T new tokens and H
+    heads; prefix: the shape of prefix_table, if any."""
+    return _attention_bytes(cache, T, H, tree, weights, None if prefix is None else tuple(prefix))
 
 
-def new_attention_workspace(cache, T, H, *, tree=False, weights=False):
+def new_attention_workspace(cache, T, H, *, tree=False, weights=False, prefix=None):
     """A zero-filled workspace for cache_attention at this shape."""
-    return torch.zeros(_attention_bytes(cache, T, H, tree, weights), dtype=torch.uint8, device=cache.device)
+    return torch.zeros(attention_workspace_bytes(cache, T, H, tree=tree, weights=weights, prefix=prefix),
+                       dtype=torch.uint8, device=cache.device)
+
+
+def _prefix(table, blocks, starts, dev):
+    """sv_prefix of the arguments, or None."""
+    if table is None:
+        if blocks is not None or starts is not None:
+            raise ValueError("prefix_blocks and prefix_starts need prefix_table")
+        return None
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or 0 in table.shape:
+        raise ValueError("prefix_table must be [count, max_blocks]")
+    n, most = table.shape
+    _need("prefix_table", table, (n, most), torch.int32, dev)
+    _need("prefix_blocks", blocks, (n,), torch.int32, dev)
+    _need("prefix_starts", starts, (n + 1,), torch.int32, dev)
+    return SvPrefix(table.data_ptr(), blocks.data_ptr(), starts.data_ptr(), n, most)
 
 
 def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, query_lens=None, scale=None,
-                    weights=None, out=None, workspace=None, stream=None):
+                    prefix_table=None, prefix_blocks=None, prefix_starts=None, weights=None, out=None, workspace=None,
+                    stream=None):
     """spec_verify_attention: attention of a step's new tokens over the cache
-    and over each other (see the header).
+    and over each other; with a prefix, spec_verify_attention_prefix: over the
+    pages that rows share too (see the header).
 
     q [B, T, H, D], k_new and v_new [B, T, Hkv, D] bf16, views with D-sized
     heads side by side (slices of a fused projection will do); positions and
     blocks [B] int32; parents [B, T] int32 for trees; query_lens [B] int32;
     scale None: D ** -0.5.  weights: True or a [B, T, max_blocks] fp32 tensor to
-    get every block's attention mass.
+    get every block's attention mass.  prefix_table [n, any], prefix_blocks [n]
+    and prefix_starts [n + 1] int32: rows prefix_starts[i] to prefix_starts[i +
+    1] - 1 see the first prefix_blocks[i] pages of prefix_table[i] before their
+    own, each read once for all of them.
 
     Returns out [B, T, H, D], or (out, weights).  Tensors made here hold zeros
     behind query_lens.  A call given no workspace uses one cached for its
@@ -318,8 +344,10 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
     _need("blocks", blocks, (B,), torch.int32, dev)
     _maybe("parents", parents, (B, T), torch.int32, dev)
     _maybe("query_lens", query_lens, (B,), torch.int32, dev)
+    prefix = _prefix(prefix_table, prefix_blocks, prefix_starts, dev)
+    shared = None if prefix is None else (prefix.count, prefix.max_blocks)
     handle, scope = _scope(dev, stream)
-    need = _attention_bytes(cache, T, H, parents is not None, weights is not None and weights is not False)
+    need = _attention_bytes(cache, T, H, parents is not None, weights is not None and weights is not False, shared)
     with scope:
         make = torch.empty if query_lens is None else torch.zeros
         if weights is True:
@@ -339,16 +367,17 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
                 workspace[:4 * B * cache.Hkv * -(-(T * (H // cache.Hkv)) // 16)].zero_()
             else:
-                key = (B, T, H, cache.Hkv, D, cache.page, cache.max_blocks, parents is not None, weights is not None)
+                key = (B, T, H, cache.Hkv, D, cache.page, cache.max_blocks, parents is not None, weights is not None,
+                       shared)
                 workspace = _cached_workspace("attention", key, need, dev, handle)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
-        _check(load_library().spec_verify_attention(
+        _check(load_library().spec_verify_attention_prefix(
             q.data_ptr(), q_row, q_tok, k_new.data_ptr(), v_new.data_ptr(), kv[0], kv[1], cache._ref,
-            positions.data_ptr(), blocks.data_ptr(), _p(parents), _p(query_lens), T, H,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), _p(weights), workspace.data_ptr(), ctypes.byref(n),
-            handle))
+            None if prefix is None else ctypes.byref(prefix), positions.data_ptr(), blocks.data_ptr(), _p(parents),
+            _p(query_lens), T, H, D ** -0.5 if scale is None else scale, out.data_ptr(), _p(weights),
+            workspace.data_ptr(), ctypes.byref(n), handle))
     return out if weights is None else (out, weights)
 
 
