@@ -301,15 +301,18 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 }
 
 // out = the mean of what a row has of its own and of its prefix's parts, each
-// with its weight; D / 4 threads for a token's head.
-template <int D>
+// with its weight.  D / 4 threads take every PG-th part of a token's head, four
+// parts' loads at once, and the PG groups join in their order (8 rows of one
+// token, 64 parts: 51 us with one thread to a channel's parts).
+template <int D, int PG>
 __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
-  const int64_t e = ((int64_t)blockIdx.x * WG + threadIdx.x) / (D / 4);
-  const int d = threadIdx.x % (D / 4) * 4;
-  const int64_t all = (int64_t)a.c.B * a.T * a.H;
-  if (e >= all) return;
-  const int head = (int)(e % a.H), tok = (int)(e / a.H % a.T), b = (int)(e / a.H / a.T);
-  if (a.qlens && tok >= a.qlens[b]) return;
+  constexpr int L = D / 4, ROWS = WG / (L * PG), AHEAD = 4;
+  __shared__ f32x4 sx[PG > 1 ? WG : 1];
+  __shared__ float2 sml[PG > 1 ? WG / L : 1];
+  const int lane = threadIdx.x % L, pg = threadIdx.x / L % PG, d = lane * 4;
+  const int64_t all = (int64_t)a.c.B * a.T * a.H, e = (int64_t)blockIdx.x * ROWS + threadIdx.x / (L * PG);
+  const int head = (int)(e % a.H), tok = (int)(e / a.H % a.T), b = (int)min(e / a.H / a.T, (int64_t)a.c.B - 1);
+  const bool live = e < all && !(a.qlens && tok >= a.qlens[b]);
   // The last group that starts at or before the row.
   int lo = 0, hi = a.p.count;
   while (hi - lo > 1) {
@@ -318,32 +321,78 @@ __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
     else hi = mid;
   }
   const Group g = group_of(a, lo);
-  const int parts = b >= g.first && b < g.first + g.rows ? g.parts : 0;
+  const int parts = live && b >= g.first && b < g.first + g.rows ? g.parts : 0;
   const int64_t at = ((int64_t)b * a.c.Hkv + head / a.G) * a.mpad + tok * a.G + head % a.G;
-  const float own = a.lse[at];
-  f32x4 x = *reinterpret_cast<const f32x4*>(a.own + e * D + d);
-  float top = own;
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[(s * all + e) * 2]);
-  float sum = 0.f;
-  if (own == NEG_INF) {
-    if (top > NEG_INF) x = f32x4{0.f, 0.f, 0.f, 0.f};
-  } else {
-    sum = exp2_fast(own - top);
-    x *= sum;
+  // Own part in group 0.  A part of nothing (its every score -inf) counts for nothing.
+  float top = NEG_INF, sum = 0.f;
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+  if (pg == 0 && live) {
+    top = a.lse[at];
+    x = *reinterpret_cast<const f32x4*>(a.own + e * D + d);
+    sum = top == NEG_INF ? 0.f : 1.f;
   }
-  for (int s = 0; s < parts; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * all + e) * 2);
-    if (ml.x == NEG_INF && !(ml.y != ml.y)) continue;
-    const float f = ml.y * exp2_fast(ml.x - top);
-    sum += f;
-    x += *reinterpret_cast<const f32x4*>(a.part_o + (s * all + e) * D + d) * f;
+  const bool none = pg == 0 && top == NEG_INF;  // x is NaN there, and stays so if no part has anything
+  const f32x4 kept = x;
+  if (none) x = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = pg; s0 < parts; s0 += PG * AHEAD) {
+    float2 ml[AHEAD];
+    f32x4 y[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t s = min(s0 + k * PG, parts - 1) * all + e;
+      ml[k] = *reinterpret_cast<const float2*>(a.part_ml + s * 2);
+      y[k] = *reinterpret_cast<const f32x4*>(a.part_o + s * D + d);
+    }
+    float to = top;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) to = fmaxf(to, ml[k].x);  // a part read twice is no other maximum
+    const float f = top == NEG_INF ? 0.f : exp2_fast(top - to);
+    sum *= f;
+    x *= f;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (s0 + k * PG >= parts || (ml[k].x == NEG_INF && ml[k].y == ml[k].y)) continue;
+      const float w = ml[k].y * exp2_fast(ml[k].x - to);
+      sum += w;
+      x += y[k] * w;
+    }
+    top = to;
   }
+  if constexpr (PG > 1) {
+    sx[threadIdx.x] = x;
+    if (lane == 0) sml[threadIdx.x / L] = make_float2(top, sum);
+    __syncthreads();
+    if (pg) return;
+    const int first = threadIdx.x / L;
+#pragma unroll
+    for (int k = 1; k < PG; ++k) top = fmaxf(top, sml[first + k].x);
+    sum = 0.f;
+    x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < PG; ++k) {
+      const float2 ml = sml[first + k];
+      if (ml.x == NEG_INF && ml.y == 0.f) continue;
+      const float f = exp2_fast(ml.x - top);
+      sum = fmaf(ml.y, f, sum);
+      x += sx[threadIdx.x + k * L] * f;
+    }
+  }
+  if (!live) return;
   if (parts) x *= 1.f / sum;
+  if (none && !(sum > 0.f)) x = kept;
   union { bf16x2 p[2]; uint2 u; } y;
   y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
   y.p[1] = __builtin_convertvector(f32x2{x[2], x[3]}, bf16x2);
   *reinterpret_cast<uint2*>(a.out + e * D + d) = y.u;
   if (d == 0 && parts) a.lse[at] = top + __builtin_amdgcn_logf(sum);
+}
+
+template <int D, int PG>
+int join(const PrefixArgs& a, hipStream_t st) {
+  constexpr int ROWS = WG / (D / 4 * PG);
+  const int64_t rows = (int64_t)a.c.B * a.T * a.H;
+  hipLaunchKernelGGL((prefix_join_kernel<D, PG>), dim3((uint32_t)((rows + ROWS - 1) / ROWS)), dim3(WG), 0, st, a);
+  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
 }  // namespace
@@ -387,10 +436,8 @@ int prefix_launch(const PrefixArgs& a, hipStream_t st) {
 }
 
 int prefix_join(const PrefixArgs& a, hipStream_t st) {
-  const int64_t n = (int64_t)a.c.B * a.T * a.H * (a.c.D / 4);
-  hipLaunchKernelGGL(a.c.D == 64 ? prefix_join_kernel<64> : prefix_join_kernel<128>, dim3((uint32_t)((n + WG - 1) / WG)),
-                     dim3(WG), 0, st, a);
-  return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
+  const bool few = a.splits <= 8;
+  return a.c.D == 64 ? (few ? join<64, 1>(a, st) : join<64, 8>(a, st)) : (few ? join<128, 1>(a, st) : join<128, 8>(a, st));
 }
 
 }  // namespace svr

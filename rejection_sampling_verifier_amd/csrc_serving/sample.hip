@@ -16,10 +16,14 @@
 // rules cut the row it also puts out the chunk's candidates, those that a bound
 // from the chunk alone does not exclude: a chunk's top k are found among the k
 // largest of its lanes' maxima, its nucleus above (1 - p) / V of its sum, min-p
-// below its maximum.  sample_row_kernel, a work-group per row, finds the
-// row's bound among the candidates and draws.  A chunk with more candidates
-// than its list holds is read again there.
+// below its maximum.  sample_row_kernel finds the row's bound among the
+// candidates and draws.  Candidates that fit LDS are a work-group's.  A row
+// with more, up to all its tokens, is shared by several where rows are few:
+// each counts its chunks (again from the logits, where a chunk's list is too
+// short), and the last to arrive adds the counts up and goes on with what
+// lies in the bin of the bound.
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -33,9 +37,10 @@ namespace {
 constexpr int MAX_VOCAB = 1 << 20;   // so that sums of weights of up to 2^43 stay below 2^63
 constexpr int MAX_DRAWS = SV_MAX_NODES;
 constexpr int MAX_CHUNKS = 512;
-constexpr int RW = 1024;             // threads of the kernel over rows
-constexpr int BINS = 2 * RW;
-constexpr int HELD = 6144;           // candidates of a row that LDS holds
+constexpr int BINS = 2048;
+constexpr int EACH = BINS / WG;      // of a thread
+constexpr int HELD = 2048;           // candidates of a row that LDS holds
+constexpr int MANY = 16384;          // listed candidates of a row that several work-groups share
 constexpr double ONE = 0x1p43;       // a weight of 1 as a whole number
 
 struct Chunk {
@@ -61,7 +66,12 @@ struct SampleArgs {
   double* subs;       // [rows][C][4 NV] sums of a wave's vectors, rows without a cut; of spec_verify_sample
   uint64_t* lists;    // [rows][C][cap] order << 32 | id
   uint2* bounds;      // [rows] of spec_verify_truncate
+  unsigned* arrived;  // [rows] work-groups that have put out their counts
+  uint64_t* masses;   // [rows][BINS] of all of them
+  uint32_t* counts;   // [rows][1 + share][BINS] of all of them, and of each
   int B, P, V, n, C, cap;
+  int share;          // work-groups of a row
+  int fill;           // sample_stats_kernel writes -inf to out, sample_row_kernel what is kept
 };
 
 // A row's rules.
@@ -90,31 +100,36 @@ __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int b) {
   return r;
 }
 
-// 2^y for y <= 0, to about 2^-50: y's whole part goes into the exponent, the
-// rest, at most 1/2, into the series of exp(r ln 2), whose 13th power is below
-// 2^-50.  fp64 multiply-adds run at the rate of fp32 ones here.
-__device__ __forceinline__ double exp2_64(double y) {
-  const double n = rint(y), r = (y - n) * 0.69314718055994530942;
-  double s = 1.0 / 479001600.0;
-  s = fma(s, r, 1.0 / 39916800.0);
-  s = fma(s, r, 1.0 / 3628800.0);
-  s = fma(s, r, 1.0 / 362880.0);
-  s = fma(s, r, 1.0 / 40320.0);
-  s = fma(s, r, 1.0 / 5040.0);
-  s = fma(s, r, 1.0 / 720.0);
-  s = fma(s, r, 1.0 / 120.0);
-  s = fma(s, r, 1.0 / 24.0);
-  s = fma(s, r, 1.0 / 6.0);
-  s = fma(s, r, 0.5);
-  s = fma(s, r, 1.0);
-  s = fma(s, r, 1.0);
-  return ldexp(s, (int)fmax(n, -1100.0));
-}
+// 2^y for -1000 <= y <= 0, to about 2^-42: y's whole part goes into the
+// exponent, the rest r, at most 1/2, into the series of 2^r, whose 11th term is
+// 2^-42.  It is rounded off by adding 1.5 * 2^52, which leaves it in the sum's
+// low bits.  fp64 additions and multiply-adds run at the rate of fp32 ones here,
+// conversions and ldexp at a quarter of it.
+// The series' factors are held in scalar registers: as literals each would take
+// two instructions to every multiply-add.
+struct Series {
+  double k[10];  // ln(2)^k / k!, k = 1 ... 10
+  __device__ __forceinline__ Series()
+      : k{6.9314718055994531e-1, 2.4022650695910072e-1, 5.5504108664821580e-2, 9.6181291076284772e-3,
+          1.3333558146428443e-3, 1.5403530393381609e-4, 1.5252733804059841e-5, 1.3215486790144310e-6,
+          1.0178086009239700e-7, 7.0549116208011233e-9} {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) asm volatile("" : "+s"(k[i]));
+  }
+  __device__ __forceinline__ double exp2(double y) const {
+    const double t = y + 0x1.8p52, r = y - (t - 0x1.8p52);
+    double s = fma(k[9], r, k[8]);
+#pragma unroll
+    for (int i = 7; i >= 0; --i) s = fma(s, r, k[i]);
+    s = fma(s, r, 1.0);
+    return __hiloint2double(__double2hiint(s) + (__double2loint(t) << 20), __double2loint(s));
+  }
+};
 // The weight of a logit against a maximum, c = log2(e) / T.  1 at the maximum,
 // whatever it is, 0 for -inf.
 __device__ __forceinline__ double weight(float l, float top, double c) {
   if (l == top) return 1.0;
-  return l == NEG_INF ? 0.0 : exp2_64(fmax(((double)l - (double)top) * c, -2000.0));
+  return l == NEG_INF ? 0.0 : Series().exp2(fmax(((double)l - (double)top) * c, -1000.0));
 }
 // ln of a token's part of the sum `total` of the weights.
 __device__ __forceinline__ float log_part(float l, float top, float T, double total) {
@@ -175,16 +190,75 @@ __device__ __forceinline__ float logit_at(const u32x4& v, int k) {
   return fmaxf(Tr<ET>::at(v, k), NEG_INF);
 }
 
+// Logits by their bits: whole numbers in the order of the logits, -0 just below
+// 0, +NaN above everything, -NaN below.  Two bf16 at once, in 16 bits each.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+template <typename ET>
+struct Bits {
+  static constexpr uint32_t INF = sizeof(ET) == 2 ? 0xFF80u : 0xFF800000u;   // of +inf; above it is NaN
+  static constexpr uint32_t LEAST = sizeof(ET) == 2 ? 0x0080u : 0x00800000u;  // of the lowest finite logit
+  __device__ __forceinline__ static uint32_t word(uint32_t w) {
+    if (sizeof(ET) == 4) return w ^ ((uint32_t)((int32_t)w >> 31) | 0x80000000u);
+    const i16x2 s = __builtin_bit_cast(i16x2, w) >> 15;
+    return w ^ (__builtin_bit_cast(uint32_t, s) | 0x80008000u);
+  }
+  __device__ __forceinline__ static uint32_t most(uint32_t x, uint32_t y) {
+    if (sizeof(ET) == 4) return x > y ? x : y;
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, x), __builtin_bit_cast(u16x2, y)));
+  }
+  // The largest of a vector.
+  __device__ __forceinline__ static uint32_t top(const u32x4& v) {
+    const uint32_t m = most(most(word(v[0]), word(v[1])), most(word(v[2]), word(v[3])));
+    return sizeof(ET) == 4 ? m : (m >> 16 > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);
+  }
+  __device__ __forceinline__ static uint32_t of(ET e) {
+    if constexpr (sizeof(ET) == 2) return word((uint32_t)e) & 0xFFFFu;
+    else return word(__float_as_uint(e));
+  }
+  __device__ __forceinline__ static float logit(uint32_t k) { return logit_of<ET>(k); }
+  // The least of the logits at or above a float, none of which is -inf.
+  __device__ __forceinline__ static uint32_t at_least(float l) {
+    uint32_t k = order_of<ET>(l);
+    if (l == 0.f) --k;                                   // -0 counts as 0
+    if (sizeof(ET) == 2 && (__float_as_uint(l) & 0xFFFFu)) {  // between two bf16: the next one up
+      if (!(__float_as_uint(l) >> 31)) ++k;
+    }
+    return k > LEAST ? k : LEAST;
+  }
+};
+
 __device__ __forceinline__ double shfl_xor64(double x, int m) { return __shfl_xor(x, m, 64); }
+
+template <typename T>
+__device__ __forceinline__ T wave_upto(T v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const T u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+template <typename ET>
+__device__ __forceinline__ ET minus_inf() {
+  if constexpr (sizeof(ET) == 2) return 0xFF80u;
+  else return NEG_INF;
+}
 
 // ---- per chunk ----------------------------------------------------------------
 
+constexpr int QUEUE = 512;  // vectors of a chunk that are looked through for candidates
+
 template <typename ET, int NV>
-__global__ __launch_bounds__(WG) void sample_stats_kernel(SampleArgs a) {
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void sample_stats_kernel(SampleArgs a) {
   constexpr int VEC = Tr<ET>::VEC;
-  __shared__ float shf[NWAVE];
+  __shared__ uint32_t shk[NWAVE];
   __shared__ int shi[NWAVE];
   __shared__ double shd[NWAVE];
+  __shared__ u32x4 queue[QUEUE];
+  __shared__ int ids[QUEUE];
+  __shared__ int queued, found;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   const int row = blockIdx.x / a.C, chunk = blockIdx.x % a.C;
   const int b = row / a.P;
@@ -194,23 +268,70 @@ __global__ __launch_bounds__(WG) void sample_stats_kernel(SampleArgs a) {
   u32x4 v[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) v[j] = x.load(q0 + j * WG);
-  float mine = NEG_INF;
+  if (a.arrived) {  // what the row's work-groups will add to
+    for (int i = chunk * WG + t; i < BINS; i += a.C * WG) {
+      a.masses[(int64_t)row * BINS + i] = 0;
+      a.counts[(int64_t)row * (a.share + 1) * BINS + i] = 0;
+    }
+    if (chunk == 0 && t == 0) a.arrived[row] = 0;
+  }
+  if (t == 0) queued = found = 0;
+  uint32_t top_of[NV], mine = 0;
+  for (bool again = true; again;) {
+    mine = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      top_of[j] = Bits<ET>::top(v[j]);
+      mine = mine > top_of[j] ? mine : top_of[j];
+    }
+    again = mine > Bits<ET>::INF;
+    if (again) {  // NaN: as -inf
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) mine = fmaxf(mine, logit_at<ET>(v[j], k));
-  const float top = block_max(mine, shf);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (sizeof(ET) == 4) {
+            if (Bits<ET>::word(v[j][k]) > Bits<ET>::INF) v[j][k] = Tr<ET>::NEG_INF_WORD;
+          } else {
+            if ((Bits<ET>::word(v[j][k]) & 0xFFFFu) > Bits<ET>::INF) v[j][k] = (v[j][k] & 0xFFFF0000u) | 0xFF80u;
+            if (Bits<ET>::word(v[j][k]) >> 16 > Bits<ET>::INF) v[j][k] = (v[j][k] & 0xFFFFu) | 0xFF800000u;
+          }
+        }
+    }
+  }
+  uint32_t key = mine;
+#pragma unroll
+  for (int s = 32; s; s >>= 1) key = max(key, (uint32_t)__shfl_xor((int)key, s, 64));
+  if (lane == 0) shk[w] = key;
+  __syncthreads();
+  for (int k = 0; k < NWAVE; ++k) key = max(key, shk[k]);
+  const float top = key < Bits<ET>::LEAST ? NEG_INF : Bits<ET>::logit(key);
   Chunk o = {0.0, top, NEG_INF, INT_MAX, 0};
   Chunk* const put = a.chunks + (int64_t)row * a.C + chunk;
+  const bool cut = !r.greedy && r.cut();
+  if (a.fill) {
+    // The output's vectors: what is kept of a row that rules cut comes later.
+    ET* const y = static_cast<ET*>(a.out) + b * a.out_row + (int64_t)(row % a.P) * a.out_pos;
+    const uint32_t none = Tr<ET>::NEG_INF_WORD;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int id = x.first(q0 + j * WG);
+      if (id >= 0 && id + VEC <= a.V) {
+        *reinterpret_cast<u32x4*>(y + id) = cut ? u32x4{none, none, none, none} : v[j];
+      } else {
+        for (int k = max(0, -id); k < VEC && id + k < a.V; ++k) y[id + k] = cut ? minus_inf<ET>() : x.p[id + k];
+      }
+    }
+  }
   if (r.greedy || top == NEG_INF) {
     if (top > NEG_INF) {
       int first = INT_MAX;
-      if (mine == top) {
+      if (Bits<ET>::logit(mine) == top) {
 #pragma unroll
         for (int j = NV - 1; j >= 0; --j)
 #pragma unroll
           for (int k = VEC - 1; k >= 0; --k)
-            if (logit_at<ET>(v[j], k) == top) first = x.first(q0 + j * WG) + k;
+            if (Tr<ET>::at(v[j], k) == top) first = x.first(q0 + j * WG) + k;
       }
 #pragma unroll
       for (int s = 32; s; s >>= 1) first = min(first, __shfl_xor(first, s, 64));
@@ -221,22 +342,27 @@ __global__ __launch_bounds__(WG) void sample_stats_kernel(SampleArgs a) {
     if (t == 0) *put = o;
     return;
   }
-  const bool cut = r.cut();
   const double c = rate(r.T);
   if (r.whole()) {
-    double s[NV], all = 0.0;
+    double all = 0.0;
+    const Series series;
+    const double from = top;
+    double* const subs = cut || !a.subs ? nullptr : a.subs + ((int64_t)row * a.C + chunk) * (NWAVE * NV);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      s[j] = 0.0;
+      double z = 0.0;
+      if (top == INFINITY) {  // beside it the others weigh nothing
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) s[j] += weight(logit_at<ET>(v[j], k), top, c);
-      all += s[j];
-    }
-    if (!cut && a.subs) {
-      double* subs = a.subs + ((int64_t)row * a.C + chunk) * (NWAVE * NV);
+        for (int k = 0; k < VEC; ++k) z += logit_at<ET>(v[j], k) == top ? 1.0 : 0.0;
+      } else {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        double z = s[j];
+        for (int k = 0; k < VEC; ++k) {
+          if (k % 4 == 0) __builtin_amdgcn_sched_barrier(0);  // four at a time: more would not fit the registers
+          z += series.exp2(fmax(((double)logit_at<ET>(v[j], k) - from) * c, -1000.0));
+        }
+      }
+      all += z;
+      if (subs) {
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) z += shfl_xor64(z, m);
         if (lane == 0) subs[j * NWAVE + w] = z;
@@ -251,45 +377,71 @@ __global__ __launch_bounds__(WG) void sample_stats_kernel(SampleArgs a) {
   if (cut) {
     float low = NEG_INF;  // no token under it is kept
     if (r.k) {
-      // Each wave looks for a logit that a quarter of k of its lanes' maxima
-      // reach; the lowest of the four is reached by k.
-      const int q = (r.k + NWAVE - 1) / NWAVE;
-      uint32_t key = 0;
-      if (q <= 64) {
-        const uint32_t own = order_of<ET>(mine);
-        for (uint32_t bit = sizeof(ET) == 2 ? 1u << 15 : 1u << 31; bit; bit >>= 1)
-          if (__popcll(__ballot(own >= (key | bit))) >= q) key |= bit;
-      }
-      if (lane == 0) shf[w] = key <= order_of<ET>(NEG_INF) ? NEG_INF : logit_of<ET>(key);
+      // W waves look for a logit that a W-th of k of their lanes' maxima reach;
+      // the lowest of theirs is reached by k.  W is 4, fewer where waves have
+      // fewer lanes with logits (a row's last chunk, a masked vocabulary).
+      const int lanes = __popcll(__ballot(mine >= Bits<ET>::LEAST));
+      if (lane == 0) shi[w] = lanes;
       __syncthreads();
-      low = fminf(fminf(shf[0], shf[1]), fminf(shf[2], shf[3]));
+      int q = INT_MAX;
+      for (int W = NWAVE; W > 0 && q == INT_MAX; --W) {
+        const int each = (r.k + W - 1) / W;
+        if ((shi[0] >= each) + (shi[1] >= each) + (shi[2] >= each) + (shi[3] >= each) >= W) q = each;
+      }
+      uint32_t reached = q == INT_MAX ? 0 : UINT32_MAX;
+      if (shi[w] >= q) {
+        reached = 0;
+        for (uint32_t bit = sizeof(ET) == 2 ? 1u << 15 : 1u << 31; bit; bit >>= 1)
+          if (__popcll(__ballot(mine >= (reached | bit))) >= q) reached |= bit;
+      }
+      if (lane == 0) shk[w] = reached;
+      __syncthreads();
+      reached = min(min(shk[0], shk[1]), min(shk[2], shk[3]));
+      if (reached >= Bits<ET>::LEAST) low = Bits<ET>::logit(reached);
       o.low = low;
     } else if (r.by_p) {
       low = under(top, r.T, (1.0 - (double)r.p) * o.sum / a.V);
     }
     if (r.m_first()) low = fmaxf(low, under(top, r.T, (double)r.m));
+    // Vectors that hold a candidate stand in line in LDS, where each element is looked at by one lane.
+    const uint32_t least = Bits<ET>::at_least(low);
     int n = 0;
 #pragma unroll
+    for (int j = 0; j < NV; ++j) n += top_of[j] >= least;
+    const int upto = wave_upto(n), waves = __builtin_amdgcn_readlane(upto, 63);
+    int at = 0;
+    if (lane == 0 && waves) at = atomicAdd(&queued, waves);
+    at = __builtin_amdgcn_readfirstlane(at) + upto - n;
+#pragma unroll
     for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) {
-        const float l = logit_at<ET>(v[j], k);
-        n += (l >= low) & (l > NEG_INF);
-      }
-    int total;
-    __syncthreads();
-    int at = block_count_scan(n, shi, total);
-    o.listed = total <= a.cap ? total : -1;
-    if (o.listed > 0 && n) {
-      uint64_t* list = a.lists + ((int64_t)row * a.C + chunk) * a.cap;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          const float l = logit_at<ET>(v[j], k);
-          if ((l >= low) & (l > NEG_INF))
-            list[at++] = (uint64_t)order_of<ET>(l) << 32 | (uint32_t)(x.first(q0 + j * WG) + k);
+      if (top_of[j] >= least) {
+        if (at < QUEUE) {
+          queue[at] = v[j];
+          ids[at] = x.first(q0 + j * WG);
         }
+        ++at;
+      }
+    __syncthreads();
+    const int vectors = queued;
+    if (vectors <= QUEUE) {
+      uint64_t* const list = a.lists + ((int64_t)row * a.C + chunk) * a.cap;
+      for (int e0 = 0; e0 < vectors * VEC; e0 += WG) {
+        const int e = e0 + t;
+        uint32_t k = 0;
+        if (e < vectors * VEC) k = Bits<ET>::of(reinterpret_cast<const ET*>(queue)[e]);
+        const bool hit = k >= least;
+        const uint64_t hits = __ballot(hit);
+        if (!hits) continue;
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&found, (int)__popcll(hits));
+        to = __builtin_amdgcn_readfirstlane(to) + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
+        if (hit && to < a.cap)
+          list[to] = (uint64_t)order_of<ET>(Bits<ET>::logit(k)) << 32 | (uint32_t)(ids[e / VEC] + e % VEC);
+      }
+      __syncthreads();
+      o.listed = found <= a.cap ? found : -1;
+    } else {
+      o.listed = -1;
     }
   }
   if (t == 0) *put = o;
@@ -304,35 +456,31 @@ struct RowLds {
   double upto[MAX_CHUNKS];
   float top[MAX_CHUNKS];
   int listed[MAX_CHUNKS];
-  uint64_t sums[RW / 64];
-  uint32_t counts[RW / 64];
-  uint64_t before;      // what the search found
-  uint32_t before_count, bin;
-  int found, n;
-  float low, max;
+  uint64_t sums[NWAVE];
+  uint64_t before;      // what a search found
+  uint32_t bin;
+  int found, n, last;
 };
 
 // Over the work-group's threads, in their order: what lies before this one.
-__device__ __forceinline__ uint64_t scan64(uint64_t v, uint64_t* sums, uint64_t& total) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint64_t inc = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t u = __shfl_up((unsigned long long)inc, o, 64);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 63) sums[w] = inc;
+__device__ __forceinline__ uint64_t before_me(uint64_t v, uint64_t* sums, uint64_t& total) {
+  const int w = threadIdx.x >> 6;
+  const uint64_t inc = wave_upto((unsigned long long)v);
+  if ((threadIdx.x & 63) == 63) sums[w] = inc;
   __syncthreads();
   uint64_t base = 0;
   total = 0;
 #pragma unroll
-  for (int k = 0; k < RW / 64; ++k) {
+  for (int k = 0; k < NWAVE; ++k) {
     if (k < w) base += sums[k];
     total += sums[k];
   }
   __syncthreads();
   return base + inc - v;
 }
+
+template <typename T>
+__device__ __forceinline__ T max_of(T x, T y) { return x > y ? x : y; }
 
 template <typename ET, int NV>
 struct RowWork {
@@ -341,44 +489,71 @@ struct RowWork {
   RowLds& sh;
   const RowOf<ET>& x;
   int row;
-  float max;
+  float top;       // the row's maximum
   double c;
   float low;       // no candidate under it
-  bool in_lds;
+  bool lists;      // the candidates are in the chunks' lists, or else among all logits
+  bool in_lds;     // the candidates are sh.held
+  bool shared;     // the first counts are several work-groups'
   uint32_t kt;     // kept: order above kt, or kt itself with ids below idlim
   int idlim;
 
   __device__ __forceinline__ bool kept(uint32_t o, int id) const { return o > kt || (o == kt && id < idlim); }
-  __device__ __forceinline__ double w(uint32_t o) const { return weight(logit_of<ET>(o), max, c); }
+  __device__ __forceinline__ double w(uint32_t o) const { return weight(logit_of<ET>(o), top, c); }
 
   // f(order, id) for the row's candidates in chunks [c0, c1).
   template <typename F>
   __device__ __forceinline__ void visit_chunks(int c0, int c1, F f) const {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int ch = c0 + wave; ch < c1; ch += RW / 64) {
-      const uint64_t* list = a.lists + ((int64_t)row * a.C + ch) * a.cap;
-      for (int i = lane; i < sh.listed[ch]; i += 64) {
-        const uint64_t e = list[i];
-        if (logit_of<ET>((uint32_t)(e >> 32)) >= low) f((uint32_t)(e >> 32), (int)(uint32_t)e);
+    if (lists) {
+      // A wave takes every fourth chunk, the lists of eight of them side by side.
+      constexpr int SIDE = 8;
+      const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      const uint32_t least = order_of<ET>(low);
+      const uint64_t* const list = a.lists + (int64_t)row * a.C * a.cap;
+      for (int ch = c0 + wave; ch < c1; ch += NWAVE * SIDE) {
+        int n[SIDE], most = 0;
+#pragma unroll
+        for (int j = 0; j < SIDE; ++j) {
+          n[j] = ch + j * NWAVE < c1 ? __builtin_amdgcn_readfirstlane(sh.listed[ch + j * NWAVE]) : 0;
+          most = max_of(most, n[j]);
+        }
+        for (int i = lane; i - lane < most; i += 64) {
+          uint64_t e[SIDE];
+#pragma unroll
+          for (int j = 0; j < SIDE; ++j) {
+            e[j] = 0;  // of no logit
+            if (i < n[j]) e[j] = list[(int64_t)(ch + j * NWAVE) * a.cap + i];
+          }
+#pragma unroll
+          for (int j = 0; j < SIDE; ++j)
+            if (i < n[j] && (uint32_t)(e[j] >> 32) >= least) f((uint32_t)(e[j] >> 32), (int)(uint32_t)e[j]);
+        }
       }
+      return;
     }
-    for (int ch = c0; ch < c1; ++ch) {
-      if (sh.listed[ch] >= 0) continue;
-      for (int q = threadIdx.x; q < WG * NV; q += RW) {
-        const u32x4 v = x.load(ch * WG * NV + q);
+    constexpr int AHEAD = 8;
+    const uint32_t least = Bits<ET>::at_least(low);
+#pragma unroll 1
+    for (int q = c0 * NV * WG + (int)threadIdx.x; q < c1 * NV * WG; q += AHEAD * WG) {
+      u32x4 v[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) v[j] = x.load(q + j * WG);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (Bits<ET>::top(v[j]) < least || q + j * WG >= c1 * NV * WG) continue;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          const float l = logit_at<ET>(v, k);
-          if ((l >= low) & (l > NEG_INF)) f(order_of<ET>(l), x.first(ch * WG * NV + q) + k);
+          const float l = Tr<ET>::at(v[j], k);
+          if ((l >= low) & (l > NEG_INF)) f(order_of<ET>(l), x.first(q + j * WG) + k);
         }
       }
     }
   }
-  // f(order, id) for the row's candidates with ids in [i0, i1).
+  // f(order, id) for the row's candidates, those with ids in [i0, i1) at least.
   template <typename F>
   __device__ __forceinline__ void visit(int i0, int i1, F f) const {
     if (in_lds) {
-      for (int i = threadIdx.x; i < sh.n; i += RW) {
+      for (int i = threadIdx.x; i < sh.n; i += WG) {
         const uint64_t e = sh.held[i];
         f((uint32_t)(e >> 32), (int)(uint32_t)e);
       }
@@ -387,8 +562,29 @@ struct RowWork {
     const int per = WG * NV * VEC;
     visit_chunks((i0 + x.lead) / per, min(a.C, (i1 - 1 + x.lead) / per + 1), f);
   }
+  // The candidates that `keep` takes, n of them at most, come to LDS if it has room.
+  template <typename F>
+  __device__ __forceinline__ void hold(uint64_t n, int c0, int c1, F keep) {
+    if (in_lds || n > HELD) return;
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    visit_chunks(c0, c1, [&](uint32_t o, int id) {
+      if (!keep(o, id)) return;
+      // One addition for the lanes that are here together: each by itself would wait for the others'.
+      const uint64_t here = __ballot(1);
+      const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(here >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)here, 0));
+      int at = 0;
+      if (before == 0) at = atomicAdd(&sh.n, (int)__popcll(here));
+      at = __builtin_amdgcn_readfirstlane(at) + before;
+      if (at < HELD) sh.held[at] = (uint64_t)o << 32 | (uint32_t)id;
+    });
+    __syncthreads();
+    in_lds = sh.n <= HELD;
+  }
   __device__ __forceinline__ void clear() {
-    for (int i = threadIdx.x; i < BINS; i += RW) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < BINS; i += WG) {
       sh.mass[i] = 0;
       sh.count[i] = 0;
     }
@@ -396,120 +592,236 @@ struct RowWork {
   }
   // Of the bins, from the last down or from the first up, the one in which the
   // running sum (of counts or masses) reaches `need`: sh.found, sh.bin and what
-  // lies before it.  The total of the masses comes back.
+  // lies before it.  The total comes back.
   template <bool DOWN, bool MASS>
   __device__ __forceinline__ uint64_t search(uint64_t need) {
     const int t = threadIdx.x;
     __syncthreads();
     if (t == 0) sh.found = 0;
-    const int i0 = DOWN ? BINS - 1 - 2 * t : 2 * t, i1 = DOWN ? i0 - 1 : i0 + 1;
-    const uint64_t v0 = MASS ? sh.mass[i0] : sh.count[i0], v1 = MASS ? sh.mass[i1] : sh.count[i1];
+    uint64_t v[EACH], own = 0;
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const int i = DOWN ? BINS - 1 - (t * EACH + k) : t * EACH + k;
+      v[k] = MASS ? sh.mass[i] : sh.count[i];
+      own += v[k];
+    }
     uint64_t total;
-    const uint64_t before = scan64(v0 + v1, sh.sums, total);
-    if (before < need && need <= before + v0 + v1) {
-      const bool second = need > before + v0;
-      sh.found = 1;
-      sh.bin = second ? i1 : i0;
-      sh.before = second ? before + v0 : before;
+    uint64_t before = before_me(own, sh.sums, total);
+    if (before < need && need <= before + own) {
+#pragma unroll
+      for (int k = 0; k < EACH; ++k) {
+        if (before < need && need <= before + v[k]) {
+          sh.found = 1;
+          sh.bin = DOWN ? BINS - 1 - (t * EACH + k) : t * EACH + k;
+          sh.before = before;
+        }
+        before += v[k];
+      }
     }
     __syncthreads();
     return total;
   }
+  // The orders that a cut looks at first, and how many of them make a bin.
+  __device__ __forceinline__ void range(uint32_t& lo, uint32_t& hi, int& shift) const {
+    lo = max_of(kt, order_of<ET>(low));
+    hi = order_of<ET>(top);
+    shift = 0;
+    while ((hi - lo) >> shift >= BINS) ++shift;
+  }
+  // A bin of one order has a mass of so many times its weight.
+  template <bool MASS>
+  __device__ __forceinline__ void add(uint32_t o, uint32_t lo, int shift) {
+    const uint32_t bin = (o - lo) >> shift;
+    atomicAdd(&sh.count[bin], 1u);
+    if (MASS && shift) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)whole_of(w(o)));
+  }
+  template <bool MASS>
+  __device__ __forceinline__ void fill(uint32_t lo, int shift) {
+    __syncthreads();
+    if (!MASS || shift) return;
+    for (int i = threadIdx.x; i < BINS; i += WG)
+      if (sh.count[i]) sh.mass[i] = sh.count[i] * whole_of(w(lo + i));
+  }
+  // The first counts of a cut, of chunks [c0, c1).
+  template <bool MASS>
+  __device__ __forceinline__ void count(int c0, int c1) {
+    uint32_t lo, hi;
+    int shift;
+    range(lo, hi, shift);
+    clear();
+    if (in_lds) visit(0, a.V, [&](uint32_t o, int id) { if (o >= lo && kept(o, id)) add<MASS>(o, lo, shift); });
+    else visit_chunks(c0, c1, [&](uint32_t o, int id) { if (o >= lo && kept(o, id)) add<MASS>(o, lo, shift); });
+    if (!shared) fill<MASS>(lo, shift);
+    else __syncthreads();
+  }
+  __device__ __forceinline__ int part_begin(int part) const { return (int)((int64_t)a.C * part / a.share); }
+  // The counts of a row's work-groups, each put out and added up; the last of them to arrive has the sums.
+  template <bool MASS>
+  __device__ __forceinline__ bool share_counts(int part) {
+    const int t = threadIdx.x;
+    uint32_t lo, hi;
+    int shift;
+    range(lo, hi, shift);
+    uint32_t* const all = a.counts + (int64_t)row * (a.share + 1) * BINS;
+    uint64_t* const mass = a.masses + (int64_t)row * BINS;
+    for (int i = t; i < BINS; i += WG) {
+      const uint32_t n = sh.count[i];
+      __hip_atomic_store(all + (int64_t)(part + 1) * BINS + i, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (!n) continue;
+      __hip_atomic_fetch_add(all + i, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (MASS && shift) __hip_atomic_fetch_add(mass + i, sh.mass[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    wait_vmem();
+    __syncthreads();
+    if (t == 0)
+      sh.last = __hip_atomic_fetch_add(a.arrived + row, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                (unsigned)a.share - 1;
+    __syncthreads();
+    if (!sh.last) return false;
+    uint32_t n[EACH];
+    uint64_t m[EACH];
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      n[k] = __hip_atomic_load(all + k * WG + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      m[k] = MASS && shift ? __hip_atomic_load(mass + k * WG + t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      sh.count[k * WG + t] = n[k];
+      sh.mass[k * WG + t] = m[k];
+    }
+    fill<MASS>(lo, shift);
+    return true;
+  }
+  // Of the work-groups whose counts of this bin, one after the other, reach n:
+  // its chunks, and what is left of n.  By every wave for itself.
+  __device__ __forceinline__ void part_of(uint32_t bin, uint64_t& n, int& c0, int& c1) const {
+    const int lane = threadIdx.x & 63;
+    const uint32_t* const own = a.counts + ((int64_t)row * (a.share + 1) + 1) * BINS + bin;
+    for (int p0 = 0; p0 < a.share; p0 += 64) {
+      uint32_t v = 0;
+      if (p0 + lane < a.share) v = __hip_atomic_load(own + (int64_t)(p0 + lane) * BINS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const uint32_t upto = wave_upto(v);
+      const uint64_t past = __ballot(upto >= n);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        n -= __builtin_amdgcn_readlane(upto - v, at);
+        c0 = part_begin(p0 + at);
+        c1 = part_begin(p0 + at + 1);
+        return;
+      }
+      n -= __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
 
   // Cuts the kept set down to its first tokens in the order of logits: as many
-  // as `need` (counts), or until their mass reaches it.
+  // as `need` (counts), or until their mass reaches it.  The first counts are
+  // in the bins.
   template <bool MASS>
   __device__ __forceinline__ void cut(uint64_t need) {
-    uint32_t lo = kt, hi = order_of<ET>(max);
-    {
-      const uint32_t l = order_of<ET>(low);
-      if (l > lo) lo = l;
-    }
+    const bool all = in_lds;
+    cut_down<MASS>(need);
+    in_lds = all;  // what it held meanwhile were the candidates around the bound
+  }
+  template <bool MASS>
+  __device__ __forceinline__ void cut_down(uint64_t need) {
+    uint32_t lo, hi;
+    int shift;
+    range(lo, hi, shift);
     uint64_t left = need;
-    uint32_t ties = 0;
-    for (;;) {
-      int shift = 0;
-      while ((hi - lo) >> shift >= BINS) ++shift;
-      clear();
-      visit(0, a.V, [&](uint32_t o, int id) {
-        if (o < lo || o > hi || !kept(o, id)) return;
-        const uint32_t bin = (o - lo) >> shift;
-        atomicAdd(&sh.count[bin], 1u);
-        if (MASS) atomicAdd((unsigned long long*)&sh.mass[bin], (unsigned long long)whole_of(w(o)));
-      });
+    for (bool first = true;; first = false) {
       search<true, MASS>(left);
       if (!sh.found) return;  // all of them do not reach it
       left -= sh.before;
-      lo += sh.bin << shift;
+      const uint32_t bin = sh.bin, ties = sh.count[bin];
+      lo += bin << shift;
       if (shift == 0) {
-        ties = sh.count[sh.bin];
-        break;
+        // Of the tokens with this logit as many as it takes, the lowest ids first.
+        uint64_t n = left;
+        if (MASS) {
+          const uint64_t one = whole_of(w(lo));
+          n = one ? (left + one - 1) / one : ties;
+        }
+        if (lo != kt) idlim = INT_MAX;
+        kt = lo;
+        if (n >= ties) return;
+        const int limit = idlim;
+        int c0 = 0, c1 = a.C;
+        if (shared && first) part_of(bin, n, c0, c1);
+        hold(c0 || c1 < a.C ? 0 : ties, c0, c1, [&](uint32_t o, int id) { return o == lo && id < limit; });
+        const int per = WG * NV * VEC;
+        int i0 = max(0, c0 * per - x.lead), i1 = min(a.V, c1 * per - x.lead);
+        const int last = i1;
+        while ((i1 - i0 - 1) >> shift >= BINS) ++shift;
+        for (int pass = 0; pass < 2; ++pass) {
+          clear();
+          visit(i0, i1, [&](uint32_t o, int id) {
+            if (o == lo && id < limit && id >= i0 && id < i1) atomicAdd(&sh.count[(id - i0) >> shift], 1u);
+          });
+          search<false, false>(n);
+          n -= sh.before;
+          i0 += sh.bin << shift;
+          i1 = min(last, i0 + (1 << shift));
+          shift = 0;
+        }
+        idlim = i0 + 1;
+        return;
       }
       hi = min(hi, lo + ((1u << shift) - 1));
-    }
-    // Of the tokens with this logit as many as it takes, the lowest ids first.
-    uint64_t n = left;
-    if (MASS) {
-      const uint64_t one = whole_of(w(lo));
-      n = one ? (left + one - 1) / one : ties;
-    }
-    const int limit = lo == kt ? idlim : INT_MAX;
-    kt = lo;
-    idlim = limit;
-    if (n >= ties) return;
-    int shift = 0;
-    while ((a.V - 1) >> shift >= BINS) ++shift;
-    int i0 = 0, i1 = a.V;
-    for (int pass = 0; pass < 2; ++pass) {
-      __syncthreads();
-      clear();
-      visit(i0, i1, [&](uint32_t o, int id) {
-        if (o == lo && id < limit && id >= i0 && id < i1) atomicAdd(&sh.count[(id - i0) >> shift], 1u);
-      });
-      search<false, false>(n);
-      n -= sh.before;
-      i0 += sh.bin << shift;
-      i1 = min(a.V, i0 + (1 << shift));
       shift = 0;
+      while ((hi - lo) >> shift >= BINS) ++shift;
+      const uint32_t from = lo, to = hi;
+      hold(ties, 0, a.C, [&](uint32_t o, int id) { return o >= from && o <= to && kept(o, id); });
+      clear();
+      visit(0, a.V, [&](uint32_t o, int id) {
+        if (o >= from && o <= to && kept(o, id)) add<MASS>(o, from, shift);
+      });
+      fill<MASS>(from, shift);
     }
-    idlim = i0 + 1;
   }
 };
 
 template <typename ET, int NV>
-__global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
+__global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(3))) void sample_row_kernel(SampleArgs a) {
   constexpr int VEC = Tr<ET>::VEC, SUBS = NWAVE * NV;
   __shared__ RowLds sh;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int row = blockIdx.x, b = row / a.P;
-  const RowOf<ET> x(a.logits, b * a.row + (int64_t)(row % a.P) * a.pos, a.V);
+  const int row = blockIdx.x / a.share, part = blockIdx.x % a.share, b = row / a.P;
   const Rules r = rules_of(a, b);
+  if (part && (r.greedy || !r.cut())) return;
+  const RowOf<ET> x(a.logits, b * a.row + (int64_t)(row % a.P) * a.pos, a.V);
   const Chunk* chunks = a.chunks + (int64_t)row * a.C;
   int32_t* tokens = a.tokens ? a.tokens + (int64_t)row * a.n : nullptr;
   float* logprobs = a.logprobs ? a.logprobs + (int64_t)row * a.n : nullptr;
 
-  // The row's maximum, by the first wave.
-  if (wave == 0) {
-    float top = NEG_INF, low = NEG_INF;
-    for (int i = lane; i < a.C; i += 64) {
-      const Chunk o = chunks[i];
+  // The row's maximum, by every wave for itself.
+  float max = NEG_INF, low = NEG_INF;
+  int listed = 0;  // -1: more than the lists hold
+  for (int i0 = 0; i0 < a.C; i0 += 64) {
+    const int i = i0 + lane;
+    Chunk o = {0.0, NEG_INF, NEG_INF, INT_MAX, 0};
+    if (i < a.C) o = chunks[i];
+    if (i < a.C && wave == 0) {
       sh.top[i] = o.top;
       sh.listed[i] = o.listed;
       sh.upto[i] = o.sum;
-      top = fmaxf(top, o.top);
-      low = fmaxf(low, o.low);
     }
-    top = wave_max(top);
-    low = wave_max(low);
-    if (lane == 0) {
-      sh.max = top;
-      sh.low = low;
-      sh.n = 0;
-    }
+    max = fmaxf(max, o.top);
+    low = fmaxf(low, o.low);
+    const uint64_t over = __ballot(o.listed < 0);
+    int n = o.listed;
+#pragma unroll
+    for (int s = 32; s; s >>= 1) n += __shfl_xor(n, s, 64);
+    listed = over || listed < 0 ? -1 : listed + n;
   }
-  __syncthreads();
-  const float max = sh.max;
+  max = wave_max(max);
+  low = wave_max(low);
+  // Lists of up to MANY are gone through by one work-group, and those of them that the row's own bound leaves held in LDS.
+  const bool large = listed < 0 || listed > MANY;
+  if (part && !large) return;
   if (max == NEG_INF || r.greedy) {
+    if (part) return;
+    __syncthreads();
     if (t < a.n) {
       int id = -1;
       if (max > NEG_INF) {
@@ -524,22 +836,17 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
     return;
   }
   const double c = rate(r.T);
+  __syncthreads();
   // Sums of the chunks against the row's maximum, added up in order.
   if (r.whole()) {
-    for (int i = t; i < a.C; i += RW)
-      sh.upto[i] = sh.top[i] == NEG_INF ? 0.0 : sh.upto[i] * weight(sh.top[i], max, c);
-    __syncthreads();
     if (wave == 0) {
       double base = 0.0;
       for (int i0 = 0; i0 < a.C; i0 += 64) {
-        double z = i0 + lane < a.C ? sh.upto[i0 + lane] : 0.0;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const double u = __shfl_up(z, o, 64);
-          if (lane >= o) z += u;
-        }
-        z += base;
-        if (i0 + lane < a.C) sh.upto[i0 + lane] = z;
+        const int i = i0 + lane;
+        double z = 0.0;
+        if (i < a.C && sh.top[i] > NEG_INF) z = sh.upto[i] * weight(sh.top[i], max, c);
+        z = wave_upto(z) + base;
+        if (i < a.C) sh.upto[i] = z;
         base = __shfl(z, 63, 64);
       }
     }
@@ -549,35 +856,28 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
   if (!r.cut()) {
     if (a.bounds && t == 0) a.bounds[row] = make_uint2(0, INT_MAX);
     const double total = sh.upto[a.C - 1];
-    for (int d = wave; d < a.n; d += RW / 64) {
+    for (int d = wave; d < a.n; d += NWAVE) {
       const float u = a.uniforms[(int64_t)row * a.n + d];
       double left = (double)(u > 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f) * total;
       // The first chunk whose running sum passes it; the last with any weight if rounding leaves none.
-      int ch = 0, last = 0;
+      int ch = 0;
       for (int i0 = 0; i0 < a.C; i0 += 64) {
         const int i = i0 + lane;
-        const double z = i < a.C ? sh.upto[i] : total, y = i > 0 && i < a.C ? sh.upto[i - 1] : 0.0;
-        const uint64_t some = __ballot(i < a.C && z > (i ? y : 0.0));
-        if (some) last = i0 + 63 - __builtin_clzll(some);
-        const uint64_t past = __ballot(i < a.C && z > left);
+        const double z = i < a.C ? sh.upto[i] : 0.0, y = i > 0 && i < a.C ? sh.upto[i - 1] : 0.0;
+        const uint64_t some = __ballot(z > y);
+        if (some) ch = i0 + 63 - __builtin_clzll(some);
+        const uint64_t past = __ballot(z > left);
         if (past) {
           ch = i0 + __builtin_ctzll(past);
           break;
         }
-        ch = last;
       }
       const float top = sh.top[ch];
       left = (left - (ch ? sh.upto[ch - 1] : 0.0)) / weight(top, max, c);
-      const double* subs = a.subs + ((int64_t)row * a.C + ch) * SUBS;
-      const double own = lane < SUBS ? subs[lane] : 0.0;
-      double z = own;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(z, o, 64);
-        if (lane >= o) z += y;
-      }
+      const double own = lane < SUBS ? a.subs[((int64_t)row * a.C + ch) * SUBS + lane] : 0.0;
+      double z = wave_upto(own);
       uint64_t past = __ballot(own > 0.0 && z > left);
-      const uint64_t some = __ballot(own > 0.0);
+      const uint64_t some = __ballot(own > 0x1p-900);
       const int sub = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
       left -= __shfl(z - own, sub, 64);
       const int q = ch * WG * NV + sub / NWAVE * WG + sub % NWAVE * 64 + lane;
@@ -585,12 +885,7 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
       double e = 0.0;
 #pragma unroll
       for (int k = 0; k < VEC; ++k) e += weight(logit_at<ET>(v, k), top, c);
-      z = e;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(z, o, 64);
-        if (lane >= o) z += y;
-      }
+      z = wave_upto(e);
       past = __ballot(e > 0.0 && z > left);
       const uint64_t any = __ballot(e > 0.0);
       const int who = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
@@ -615,36 +910,34 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
     return;
   }
 
-  RowWork<ET, NV> work{a, sh, x, row, max, c, sh.low, false, 0, INT_MAX};
-  const double sum = r.by_p && !r.k ? sh.upto[a.C - 1] : 0.0;
-  if (r.by_p && !r.k) work.low = under(max, r.T, (1.0 - (double)r.p) * sum / a.V);
+  RowWork<ET, NV> work{a, sh, x, row, max, c, low, listed >= 0, false, false, 0, INT_MAX};
+  const bool mass_first = r.by_p && !r.k;
+  const double sum = mass_first ? sh.upto[a.C - 1] : 0.0;
+  if (mass_first) work.low = under(max, r.T, (1.0 - (double)r.p) * sum / a.V);
   if (r.m_first()) work.low = fmaxf(work.low, under(max, r.T, (double)r.m));
-  // Its candidates come to LDS, if they are few.
-  work.visit_chunks(0, a.C, [&](uint32_t o, int id) {
-    const int at = atomicAdd(&sh.n, 1);
-    if (at < HELD) sh.held[at] = (uint64_t)o << 32 | (uint32_t)id;
-  });
-  __syncthreads();
-  work.in_lds = sh.n <= HELD;
-
-  if (r.k) work.template cut<false>(r.k);
-  if (r.by_p) {
-    double mass = sum * ONE;
-    if (r.k) {
-      // The mass of the top k.
-      __syncthreads();
-      if (t == 0) sh.before = 0;
-      __syncthreads();
-      uint64_t own = 0;
-      work.visit(0, a.V, [&](uint32_t o, int id) {
-        if (work.kept(o, id)) own += whole_of(work.w(o));
-      });
-      uint64_t total;
-      scan64(own, sh.sums, total);
-      mass = (double)total;
+  if (part && !r.k && !r.by_p) return;
+  if (work.lists && (!large || a.share == 1)) work.hold(0, 0, a.C, [](uint32_t, int) { return true; });
+  if (r.k || r.by_p) {
+    work.shared = large && a.share > 1;
+    const int c0 = work.shared ? work.part_begin(part) : 0, c1 = work.shared ? work.part_begin(part + 1) : a.C;
+    if (mass_first) work.template count<true>(c0, c1);
+    else work.template count<false>(c0, c1);
+    if (work.shared && !(mass_first ? work.template share_counts<true>(part) : work.template share_counts<false>(part)))
+      return;
+    if (mass_first) {
+      const double need = ceil((double)r.p * (sum * ONE));
+      work.template cut<true>(need >= 1.0 ? (uint64_t)need : 1);
+    } else {
+      work.template cut<false>(r.k);
+      work.hold(r.k, 0, a.C, [&](uint32_t o, int id) { return work.kept(o, id); });
     }
-    const double need = ceil((double)r.p * mass);
-    work.template cut<true>(need >= 1.0 ? (uint64_t)need : 1);
+    work.shared = false;
+    if (r.by_p && r.k) {
+      work.template count<true>(0, a.C);
+      const uint64_t total = work.template search<true, true>(0);
+      const double need = ceil((double)r.p * (double)total);
+      work.template cut<true>(need >= 1.0 ? (uint64_t)need : 1);
+    }
   }
   if (r.by_m) {
     // The lowest logit whose weight is at least m, by 64 probes at a time.
@@ -667,12 +960,19 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
     if (t == 0) a.bounds[row] = make_uint2(work.kt, (uint32_t)work.idlim);
     return;
   }
+  if (logit_of<ET>(work.kt) > work.low) work.low = logit_of<ET>(work.kt);
+  if (a.fill) {
+    ET* const y = static_cast<ET*>(a.out) + b * a.out_row + (int64_t)(row % a.P) * a.out_pos;
+    work.visit(0, a.V, [&](uint32_t o, int id) {
+      if (work.kept(o, id)) y[id] = x.p[id];
+    });
+    return;
+  }
 
   // The kept tokens' masses by ids, then by the ids of a draw's bin.
   int shift = 0;
   while ((a.V - 1) >> shift >= BINS) ++shift;
   uint64_t* const fine = reinterpret_cast<uint64_t*>(sh.count);  // up to BINS / 2 ids of a bin
-  __syncthreads();
   work.clear();
   work.visit(0, a.V, [&](uint32_t o, int id) {
     if (work.kept(o, id)) atomicAdd((unsigned long long*)&sh.mass[id >> shift], (unsigned long long)whole_of(work.w(o)));
@@ -685,7 +985,7 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
     work.template search<false, true>(need);
     const int i0 = (int)sh.bin << shift, i1 = min(a.V, i0 + (1 << shift));
     const uint64_t left = need - sh.before;
-    for (int i = t; i < 1 << shift; i += RW) fine[i] = 0;
+    for (int i = t; i < 1 << shift; i += WG) fine[i] = 0;
     __syncthreads();
     work.visit(i0, i1, [&](uint32_t o, int id) {
       if (id >= i0 && id < i1 && work.kept(o, id)) fine[id - i0] = (uint64_t)o << 32 | 1u;
@@ -697,12 +997,7 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
       for (int i = 0; i < 1 << shift; i += 64) {
         const uint64_t e = i + lane < 1 << shift ? fine[i + lane] : 0;
         const uint64_t own = e ? whole_of(work.w((uint32_t)(e >> 32))) : 0;
-        uint64_t z = own;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-          const uint64_t y = __shfl_up((unsigned long long)z, o, 64);
-          if (lane >= o) z += y;
-        }
+        const uint64_t z = wave_upto((unsigned long long)own);
         const uint64_t past = __ballot(before + z >= left);
         if (past) {
           if (lane == __builtin_ctzll(past)) {
@@ -720,7 +1015,7 @@ __global__ __launch_bounds__(RW) void sample_row_kernel(SampleArgs a) {
 
 // ---- cut logits ---------------------------------------------------------------
 
-template <typename ET>
+template <typename ET, int NV>
 __global__ __launch_bounds__(WG) void truncate_kernel(SampleArgs a, int per, int inplace) {
   constexpr int VEC = Tr<ET>::VEC;
   const int row = blockIdx.x / per;
@@ -733,9 +1028,9 @@ __global__ __launch_bounds__(WG) void truncate_kernel(SampleArgs a, int per, int
   const uint32_t kt = bound.x;
   const int idlim = (int)bound.y;
   if (inplace && kt == 0) return;
-#pragma unroll 4
-  for (int j = 0; j < 8; ++j) {
-    const int q = (blockIdx.x % per * 8 + j) * WG + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int q = (blockIdx.x % per * NV + j) * WG + threadIdx.x;
     const int id = x.first(q);
     if (id >= a.V) return;
     u32x4 v = x.load(q);
@@ -747,7 +1042,7 @@ __global__ __launch_bounds__(WG) void truncate_kernel(SampleArgs a, int per, int
       const uint32_t o = order_of<ET>(l);
       if (o < kt || (o == kt && id + k >= idlim) || (kt && l != l)) gone |= 1u << k;
     }
-    const ET none = sizeof(ET) == 2 ? (ET)0xFF80u : (ET)NEG_INF;
+    const ET none = minus_inf<ET>();
     if (aligned && id >= 0 && id + VEC <= a.V) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k)
@@ -770,8 +1065,8 @@ __global__ __launch_bounds__(WG) void truncate_kernel(SampleArgs a, int per, int
 // ---- host ---------------------------------------------------------------------
 
 struct Plan {
-  int nv, C, cap;
-  size_t subs, lists, bounds, total;
+  int nv, C, cap, share;
+  size_t subs, lists, bounds, arrived, masses, counts, total;
 };
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -784,12 +1079,18 @@ int make_plan(int B, int P, int V, int dtype, bool cuts, bool truncate, Plan& pl
   pl.nv = rows * chunks(8) < 1024 && chunks(2) <= MAX_CHUNKS ? 2 : 8;
   pl.C = chunks(pl.nv);
   pl.cap = cuts ? (pl.nv == 8 ? 1024 : 512) : 0;
-  if (rows * pl.C > MAX_ITEMS / WG || rows > MAX_ITEMS / RW) return SV_ERR_UNSUPPORTED;
+  if (rows * pl.C > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
+  // Work-groups of a row for the case that it has many candidates: two to a CU.
+  pl.share = cuts ? (int)std::max<int64_t>(1, std::min<int64_t>(pl.C, 512 / rows)) : 1;
   const size_t n = (size_t)rows * pl.C;
   pl.subs = align256(n * sizeof(Chunk));
   pl.lists = align256(pl.subs + (truncate ? 0 : n * NWAVE * pl.nv * sizeof(double)));
   pl.bounds = align256(pl.lists + n * pl.cap * sizeof(uint64_t));
-  pl.total = align256(pl.bounds + (truncate ? (size_t)rows * sizeof(uint2) : 0));
+  pl.arrived = align256(pl.bounds + (truncate ? (size_t)rows * sizeof(uint2) : 0));
+  const size_t bins = pl.share > 1 ? (size_t)rows * BINS : 0;
+  pl.masses = align256(pl.arrived + (bins ? (size_t)rows * sizeof(unsigned) : 0));
+  pl.counts = pl.masses + bins * sizeof(uint64_t);
+  pl.total = pl.counts + bins * (1 + pl.share) * sizeof(uint32_t);
   return SV_OK;
 }
 
@@ -799,12 +1100,12 @@ int launch(const SampleArgs& a, bool inplace, hipStream_t st) {
   (void)hipGetLastError();
   hipLaunchKernelGGL((sample_stats_kernel<ET, NV>), dim3((uint32_t)rows * a.C), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
-  hipLaunchKernelGGL((sample_row_kernel<ET, NV>), dim3(rows), dim3(RW), 0, st, a);
+  hipLaunchKernelGGL((sample_row_kernel<ET, NV>), dim3((uint32_t)rows * a.share), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
-  if (a.out) {
-    constexpr int VEC = Tr<ET>::VEC;
-    const int per = (a.V + VEC - 1 + WG * 8 * VEC - 1) / (WG * 8 * VEC);
-    hipLaunchKernelGGL((truncate_kernel<ET>), dim3((uint32_t)rows * per), dim3(WG), 0, st, a, per, (int)inplace);
+  if (a.bounds) {
+    constexpr int VEC = Tr<ET>::VEC, N = NV == 2 ? 1 : 4;
+    const int per = (a.V + VEC - 1 + WG * N * VEC - 1) / (WG * N * VEC);
+    hipLaunchKernelGGL((truncate_kernel<ET, N>), dim3((uint32_t)rows * per), dim3(WG), 0, st, a, per, (int)inplace);
     if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   }
   return SV_OK;
@@ -851,6 +1152,12 @@ int prepare(const void* logits, int64_t row_stride, int64_t stride, const float*
   a.chunks = reinterpret_cast<Chunk*>(ws);
   a.subs = truncate ? nullptr : reinterpret_cast<double*>(ws + pl.subs);
   a.lists = reinterpret_cast<uint64_t*>(ws + pl.lists);
+  a.share = pl.share;
+  if (pl.share > 1) {
+    a.arrived = reinterpret_cast<unsigned*>(ws + pl.arrived);
+    a.masses = reinterpret_cast<uint64_t*>(ws + pl.masses);
+    a.counts = reinterpret_cast<uint32_t*>(ws + pl.counts);
+  }
   return SV_OK;
 }
 
@@ -907,6 +1214,12 @@ extern "C" int spec_verify_truncate(const void* logits, int64_t row_stride, int6
   a.out = out;
   a.out_row = out_row_stride;
   a.out_pos = out_stride;
-  a.bounds = reinterpret_cast<uint2*>(static_cast<char*>(workspace) + pl.bounds);
+  // Large batches get -inf written as they are read, and the kept logits after that, where vectors of both are alike
+  // (64 x 6 rows of 151,936: the third kernel alone takes 42 us).
+  const int64_t vec = 16 / es;
+  const int64_t apart = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(logits)) / (int64_t)es;
+  a.fill = pl.nv == 8 && !inplace && apart % vec == 0 && (out_row_stride - row_stride) % vec == 0 &&
+           (out_stride - stride) % vec == 0;
+  if (!a.fill) a.bounds = reinterpret_cast<uint2*>(static_cast<char*>(workspace) + pl.bounds);
   return dtype == SV_BF16 ? launch_nv<uint16_t>(a, pl, inplace, stream) : launch_nv<float>(a, pl, inplace, stream);
 }

@@ -53,7 +53,7 @@ def test_limits_and_workspace(kind):
     big = (1 << 20) + 1
     assert call(kind, V=big, row=3 * big, stride=big) == B.SV_ERR_UNSUPPORTED
     assert call(kind, B=1 << 16, P=1 << 16, row=1 << 30) == B.SV_ERR_UNSUPPORTED
-    assert call(kind, B=1 << 23, P=1) == B.SV_ERR_UNSUPPORTED
+    assert call(kind, B=1 << 24, P=1) == B.SV_ERR_UNSUPPORTED
     rc, n = call(kind, ws=None)
     assert rc == B.SV_OK and n > 0 and n % 256 == 0
     assert call(kind, ws_n=n - 1) == B.SV_ERR_WORKSPACE
