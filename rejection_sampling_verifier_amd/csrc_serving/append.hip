@@ -5,10 +5,14 @@
 // commit does (quantise.h).  Bytes bound it: two are read and one is written
 // for each element.  A work-group takes one block of a row with some of its
 // heads, a head at a time: its values wait in registers, rotated, for their
-// largest magnitude.  Cos and sin of up to 64 tokens lie in LDS for all heads
-// of the work-group.  The tokens after the last full block go to the tail by
-// the work-group of the row's first block, which is also the one that reads
-// the tail's old tokens, so that a ring of a single block will do.
+// largest magnitude, while the values of the head's other half are on their
+// way.  A thread has the same pairs of the same tokens in every head, so it
+// forms their cosines and sines once and keeps them (in LDS, 32 KB of it, they
+// leave room for three work-groups to a CU: 142 us for 16 prompts of up to 4096
+// tokens).  V's codes are turned in LDS in words of four tokens, which one lane
+// has read.  The tokens after the last full block go to the tail by the
+// work-group of the row's first block, which is also the one that reads the
+// tail's old tokens, so that a ring of a single block will do.
 
 #include <climits>
 
@@ -65,13 +69,13 @@ __device__ __forceinline__ Append row_append(const AppendArgs& a, int b, int* ba
 template <int KIND, int D, int PAGE>
 __global__ __launch_bounds__(WG) void cache_append_kernel(AppendArgs a) {
   constexpr int PER = D / 16;                                  // pairs of 16-byte pieces of a head's token
-  constexpr int NV = PAGE * PER < WG ? 1 : PAGE * PER / WG;    // those of a block, per thread
-  constexpr int CH = PAGE < 64 ? PAGE : 64;                    // tokens whose cos and sin are in LDS
-  constexpr int STEPS = CH * PER < WG ? 1 : CH * PER / WG;     // of a thread's pairs in as many tokens
+  constexpr int NV = PAGE * PER < WG ? 1 : PAGE * PER / WG;    // those of a block's keys, per thread
+  constexpr int QP = D / 8;                                    // pieces of a token
+  constexpr int NQ = PAGE / 4 * QP < WG ? 1 : PAGE / 4 * QP / WG;  // pieces of four tokens' values, per thread
+  constexpr int ROW = PAGE + 4;                                // bytes of a channel in LDS: rows in different banks
   __shared__ int bad;
-  __shared__ uint32_t tops[NWAVE];
-  __shared__ alignas(16) float2 cs[CH * (D / 2)];
-  __shared__ alignas(16) uint8_t codes[D * (PAGE + TPAD)];     // V: its channels' tokens side by side
+  __shared__ uint32_t tops[2][NWAVE];
+  __shared__ alignas(16) uint32_t codes[D * ROW / 4];          // V: its channels' tokens side by side
   const int t = threadIdx.x;
   const int b = blockIdx.x / (a.units * a.groups), unit = blockIdx.x / a.groups % a.units, group = blockIdx.x % a.groups;
   const Append r = row_append(a, b, &bad);
@@ -82,120 +86,174 @@ __global__ __launch_bounds__(WG) void cache_append_kernel(AppendArgs a) {
   if (r.n == 0 || unit >= max(r.filled, 1)) return;
   const int h0 = group * a.heads, h1 = min(h0 + a.heads, a.c.Hkv);
   const int64_t slot = (int64_t)a.c.Hkv * D;
-  const int pairs = a.rot.dims / 2;
   auto place = [&](int j) {  // ring slot of the row's j-th token since its last full block before the call
-    const int s = (r.start + j % a.c.tail);
+    const int s = r.start + j % a.c.tail;
     return s < a.c.tail ? s : s - a.c.tail;
   };
-  // The row's tokens j0 .. j0 + CH - 1: their cos and sin, as far as they are new.
-  auto turns = [&](int j0) {
-    if (!pairs) return;
-    __syncthreads();
-    for (int e = t; e < CH * pairs; e += WG) {
-      const int at = j0 + e / pairs - r.tail;  // its number among the new ones
-      if (at >= 0 && at < r.n) cs[e] = turn_of(a.rot, a.c.B, a.T, b, at, e % pairs, (int64_t)r.pos + at);
-    }
-    __syncthreads();
+  auto token = [&](bool val, int j) -> const uint16_t* {
+    return j < r.tail ? (val ? a.c.v_tail : a.c.k_tail) + ((int64_t)b * a.c.tail + place(j)) * slot
+                      : (val ? a.v : a.k) + b * a.kv_row + (j - r.tail) * a.kv_tok;
   };
-  // Piece pair c of head h of token j, which is jc-th of those in LDS: rotated and put out, if it is a new key.
-  auto take = [&](bool val, int h, int j, int jc, int c, u32x4& u, u32x4& w) {
-    const Pieces p = pieces_of(c, a.rot.dims, a.rot.interleaved);
-    const uint16_t* from = j < r.tail
-        ? (val ? a.c.v_tail : a.c.k_tail) + ((int64_t)b * a.c.tail + place(j)) * slot + h * D
-        : (val ? a.v : a.k) + b * a.kv_row + (j - r.tail) * a.kv_tok + h * D;
-    u = *reinterpret_cast<const u32x4*>(from + p.p0 * 8);
-    w = *reinterpret_cast<const u32x4*>(from + p.p1 * 8);
-    if (val || j < r.tail) return;
-    if (pairs) rotate_pieces(u, w, c, a.rot.dims, a.rot.interleaved, cs + jc * pairs);
+  // The thread's pairs of the window of PAGE tokens that begins with the row's
+  // j0-th: their cos and sin, as far as they are new.
+  float2 cs[NV][8];
+  auto turns = [&](int j0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int e = k * WG + t, at = j0 + e / PER - r.tail, c = e % PER;  // its number among the new ones
+      if (e < PAGE * PER && at >= 0 && at < r.n && c < a.rot.dims / 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[k][i] = turn_of(a.rot, a.c.B, a.T, b, at, c * 8 + i, (int64_t)r.pos + at);
+    }
+  };
+  // Keys rotated, and put out, where they are new.
+  auto turn = [&](int k, int h, int j, u32x4& u, u32x4& w) {
+    const int c = (k * WG + t) % PER;
+    if (c < a.rot.dims / 16) rotate_pieces(u, w, a.rot.interleaved, cs[k]);
     if (a.k_out) {
+      const Pieces p = pieces_of(c, a.rot.dims, a.rot.interleaved);
       uint16_t* to = a.k_out + b * a.ko_row + (j - r.tail) * a.ko_tok + h * D;
       *reinterpret_cast<u32x4*>(to + p.p0 * 8) = u;
       *reinterpret_cast<u32x4*>(to + p.p1 * 8) = w;
     }
   };
+  auto top_of = [&](const u32x4& v, uint32_t top) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+    return top;
+  };
+  auto all_tops = [&](uint32_t top, uint32_t* place) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    if ((t & 63) == 0) place[t >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NWAVE; ++k) top = max(top, place[k]);
+    return top;
+  };
 
   if (unit < r.filled) {
     const int j0 = unit * PAGE;
-    if (PAGE == CH) turns(j0);
     const int pid = a.c.block_table[(int64_t)b * a.c.max_blocks + r.blocks + unit];
-    for (int hv = h0 * 2; hv < h1 * 2; ++hv) {
-      const int h = hv >> 1;
-      const bool val = hv & 1;
+    u32x4 kv[NV][2], vv[NQ][4];
+    // Where the thread's pieces of head 0 are: what is divided and looked up is so once.
+    const uint16_t* kp[NV];
+    const uint16_t* vp[NQ][4];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) kp[k] = token(false, j0 + min((k * WG + t) / PER, PAGE - 1));
+#pragma unroll
+    for (int k = 0; k < NQ; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vp[k][i] = token(true, j0 + min((k * WG + t) / QP * 4, PAGE - 4) + i) + (k * WG + t) % QP * 8;
+    auto load_k = [&](int h) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        kv[k][0] = kv[k][1] = u32x4{0, 0, 0, 0};
+        if (k * WG + t >= PAGE * PER) continue;
+        const Pieces p = pieces_of((k * WG + t) % PER, a.rot.dims, a.rot.interleaved);
+        kv[k][0] = *reinterpret_cast<const u32x4*>(kp[k] + h * D + p.p0 * 8);
+        kv[k][1] = *reinterpret_cast<const u32x4*>(kp[k] + h * D + p.p1 * 8);
+      }
+    };
+    auto load_v = [&](int h) {
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          vv[k][i] = u32x4{0, 0, 0, 0};
+          if (k * WG + t < PAGE / 4 * QP) vv[k][i] = *reinterpret_cast<const u32x4*>(vp[k][i] + h * D);
+        }
+    };
+    load_k(h0);
+    turns(j0);
+    for (int h = h0; h < h1; ++h) {
       const int64_t at = (int64_t)pid * a.c.Hkv + h;
-      u32x4 v[NV][2];
+      load_v(h);
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (PAGE != CH && !val && k % STEPS == 0) turns(j0 + k / STEPS * CH);
-        const int e = k * WG + t, j = e / PER;
-        v[k][0] = v[k][1] = u32x4{0, 0, 0, 0};
-        if (e < PAGE * PER) take(val, h, j0 + j, j % CH, e % PER, v[k][0], v[k][1]);
+        const int e = k * WG + t, j = j0 + e / PER;
+        if (e < PAGE * PER && j >= r.tail) turn(k, h, j, kv[k][0], kv[k][1]);
+        top = top_of(kv[k][1], top_of(kv[k][0], top));
       }
+      top = all_tops(top, tops[0]);
+      {
+        const float scale = scale_of<KIND>(top);
+        const bool finite = top < 0x7F80u;
+        const float inv = KIND == SV_E4M3 && finite ? 1.f / scale : 0.f;  // a power of two: exact
+        if (t == 0) a.c.k_scale[at] = scale;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+          const int e = k * WG + t, j = e / PER;
+          if (e >= PAGE * PER) continue;
+          const Pieces p = pieces_of(e % PER, a.rot.dims, a.rot.interleaved);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w = v[k][i >> 2][i & 3];
-          top = max(top, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
-        }
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[2] = {0, 0};
+            if (finite) {
 #pragma unroll
-      for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-      __syncthreads();  // what the head before left in LDS has been read
-      if ((t & 63) == 0) tops[t >> 6] = top;
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < NWAVE; ++k) top = max(top, tops[k]);
-      const float scale = scale_of<KIND>(top);
-      const bool finite = top < 0x7F80u;
-      const float inv = KIND == SV_E4M3 && finite ? 1.f / scale : 0.f;  // a power of two: exact
-      if (t == 0) (val ? a.c.v_scale : a.c.k_scale)[at] = scale;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int e = k * WG + t, j = e / PER;
-        if (e >= PAGE * PER) continue;
-        const Pieces p = pieces_of(e % PER, a.rot.dims, a.rot.interleaved);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int d = (half ? p.p1 : p.p0) * 8;
-          uint32_t w[2] = {0, 0};
-          if (finite) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i >> 2] |= code8<KIND>(bf16_at(v[k][half], i), scale, inv) << (8 * (i & 3));
-          }
-          if (!val) {
-            *reinterpret_cast<uint2*>(a.c.k_pages + (at * PAGE + j) * D + d) = make_uint2(w[0], w[1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) codes[(d + i) * (PAGE + TPAD) + j] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+              for (int i = 0; i < 2; ++i)
+                w[i] = code32<KIND>(bf16_at(kv[k][half], 4 * i), bf16_at(kv[k][half], 4 * i + 1),
+                                    bf16_at(kv[k][half], 4 * i + 2), bf16_at(kv[k][half], 4 * i + 3), scale, inv);
+            }
+            *reinterpret_cast<uint2*>(a.c.k_pages + (at * PAGE + j) * D + (half ? p.p1 : p.p0) * 8) = make_uint2(w[0], w[1]);
           }
         }
       }
-      if (!val) continue;
+      if (h + 1 < h1) load_k(h + 1);
+      top = 0;
+#pragma unroll
+      for (int k = 0; k < NQ; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = top_of(vv[k][i], top);
+      top = all_tops(top, tops[1]);
+      {
+        const float scale = scale_of<KIND>(top);
+        const bool finite = top < 0x7F80u;
+        const float inv = KIND == SV_E4M3 && finite ? 1.f / scale : 0.f;
+        if (t == 0) a.c.v_scale[at] = scale;
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          const int f = k * WG + t;
+          if (f >= PAGE / 4 * QP) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            codes[((f % QP * 8 + i) * ROW) / 4 + f / QP] =
+                finite ? code32<KIND>(bf16_at(vv[k][0], i), bf16_at(vv[k][1], i), bf16_at(vv[k][2], i), bf16_at(vv[k][3], i), scale, inv)
+                       : 0;
+        }
+      }
       __syncthreads();
       for (int e = t; e < D * PAGE / 16; e += WG) {
         const int d = e / (PAGE / 16), j = e % (PAGE / 16) * 16;
-        *reinterpret_cast<u32x4*>(a.c.v_pages + (at * D + d) * PAGE + j) =
-            *reinterpret_cast<const u32x4*>(codes + d * (PAGE + TPAD) + j);
+        const uint32_t* from = codes + (d * ROW + j) / 4;
+        *reinterpret_cast<u32x4*>(a.c.v_pages + (at * D + d) * PAGE + j) = u32x4{from[0], from[1], from[2], from[3]};
       }
     }
   }
   if (unit) return;
   __syncthreads();  // the tail's old tokens have been read
-  const int all = r.tail + r.n;
-  for (int j0 = max(r.tail, r.filled * PAGE); j0 < all; j0 += CH) {
-    turns(j0);
-    const int n = min(CH, all - j0) * (h1 - h0) * 2 * PER;
-    for (int e = t; e < n; e += WG) {
-      const int c = e % PER, h = h0 + (e / PER >> 1) % (h1 - h0), jc = e / (PER * 2) / (h1 - h0);
-      const bool val = e / PER & 1;
-      u32x4 u, w;
-      take(val, h, j0 + jc, jc, c, u, w);
-      const Pieces p = pieces_of(c, a.rot.dims, a.rot.interleaved);
-      uint16_t* to = (val ? a.c.v_tail : a.c.k_tail) + ((int64_t)b * a.c.tail + place(j0 + jc)) * slot + h * D;
-      *reinterpret_cast<u32x4*>(to + p.p0 * 8) = u;
-      *reinterpret_cast<u32x4*>(to + p.p1 * 8) = w;
+  // The window of the tokens after the last full block.
+  const int j0 = r.filled * PAGE, all = r.tail + r.n;
+  turns(j0);
+  for (int h = h0; h < h1; ++h)
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int e = k * WG + t, j = j0 + e / PER;
+      if (e >= PAGE * PER || j < r.tail || j >= all) continue;
+      const Pieces p = pieces_of(e % PER, a.rot.dims, a.rot.interleaved);
+      const uint16_t* from = token(false, j) + h * D;
+      const uint16_t* fresh = token(true, j) + h * D;
+      u32x4 u = *reinterpret_cast<const u32x4*>(from + p.p0 * 8), w = *reinterpret_cast<const u32x4*>(from + p.p1 * 8);
+      const u32x4 x = *reinterpret_cast<const u32x4*>(fresh + p.p0 * 8), y = *reinterpret_cast<const u32x4*>(fresh + p.p1 * 8);
+      turn(k, h, j, u, w);
+      const int64_t to = ((int64_t)b * a.c.tail + place(j)) * slot + h * D;
+      *reinterpret_cast<u32x4*>(a.c.k_tail + to + p.p0 * 8) = u;
+      *reinterpret_cast<u32x4*>(a.c.k_tail + to + p.p1 * 8) = w;
+      *reinterpret_cast<u32x4*>(a.c.v_tail + to + p.p0 * 8) = x;
+      *reinterpret_cast<u32x4*>(a.c.v_tail + to + p.p1 * 8) = y;
     }
-  }
 }
 
 // Counters updated in place: after every work-group has read them.
@@ -292,8 +350,11 @@ extern "C" int spec_verify_append(const void* k, const void* v, int64_t kv_row, 
   a.T = T;
   a.units = (c.page - 1 + T) / c.page;  // blocks that T tokens complete at most
   const int64_t rows = (int64_t)c.B * a.units;
+  // Heads that share a work-group's cosines: as many as leave 4096 work-groups
+  // (16 prompts of up to 4096 tokens: 112 us with two of eight heads, 115 with
+  // four, 129 with all).
   a.heads = 1;
-  while (a.heads < c.Hkv && rows * ((c.Hkv + 2 * a.heads - 1) / (2 * a.heads)) >= 2048) a.heads *= 2;
+  while (a.heads < c.Hkv && rows * ((c.Hkv + 2 * a.heads - 1) / (2 * a.heads)) >= 4096) a.heads *= 2;
   a.groups = (c.Hkv + a.heads - 1) / a.heads;
   a.inplace = positions == positions_out;
   if (rows * a.groups > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;

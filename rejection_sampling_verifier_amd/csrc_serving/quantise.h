@@ -31,6 +31,17 @@ __device__ __forceinline__ uint32_t code8(float x, float scale, float inv) {
   return (uint32_t)(int)r & 0xFFu;
 }
 
+// Four codes in a word.
+template <int KIND>
+__device__ __forceinline__ uint32_t code32(float x0, float x1, float x2, float x3, float scale, float inv) {
+  if (KIND == SV_E4M3) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x0 * inv, x1 * inv, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x2 * inv, x3 * inv, lo, true);
+  }
+  return code8<KIND>(x0, scale, inv) | code8<KIND>(x1, scale, inv) << 8 | code8<KIND>(x2, scale, inv) << 16 |
+         code8<KIND>(x3, scale, inv) << 24;
+}
+
 constexpr int TPAD = 16;  // bytes between the channels of a buffer that transposes a block's codes
 
 }  // namespace svr

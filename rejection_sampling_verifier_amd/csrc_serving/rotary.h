@@ -83,27 +83,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
 
-// Rotates the two pieces; cs: the token's cos and sin by pair.  Products and
-// sums are rounded to float32 one by one, the results once to bf16.
-__device__ __forceinline__ void rotate_pieces(u32x4& u, u32x4& v, int c, int dims, int interleaved, const float2* cs) {
+// Rotates the two pieces of thread c; cs: cos and sin of the token's pairs 8 c
+// .. 8 c + 7.  Products and sums are rounded to float32 one by one, the results
+// once to bf16.
+__device__ __forceinline__ void rotate_pieces(u32x4& u, u32x4& v, int interleaved, const float2* cs) {
   if (!interleaved) {
-    if (c >= dims / 16) return;
-    const float4* f = reinterpret_cast<const float4*>(cs + c * 8);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 w = f[k];  // the pairs 2 k and 2 k + 1
+      const float2 w0 = cs[2 * k], w1 = cs[2 * k + 1];
       const float a0 = __uint_as_float(u[k] << 16), a1 = __uint_as_float(u[k] & 0xFFFF0000u);
       const float b0 = __uint_as_float(v[k] << 16), b1 = __uint_as_float(v[k] & 0xFFFF0000u);
-      u[k] = pack_bf16(a0 * w.x - b0 * w.y, a1 * w.z - b1 * w.w);
-      v[k] = pack_bf16(b0 * w.x + a0 * w.y, b1 * w.z + a1 * w.w);
+      u[k] = pack_bf16(a0 * w0.x - b0 * w0.y, a1 * w1.x - b1 * w1.y);
+      v[k] = pack_bf16(b0 * w0.x + a0 * w0.y, b1 * w1.x + a1 * w1.y);
     }
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = c * 8 + k;  // words of the two pieces are pairs
-    if (i >= dims / 2) return;
-    const float2 w = cs[i];
+  for (int k = 0; k < 8; ++k) {  // words of the two pieces are pairs
+    const float2 w = cs[k];
     const uint32_t x = k < 4 ? u[k & 3] : v[k & 3];
     const float a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xFFFF0000u);
     (k < 4 ? u : v)[k & 3] = pack_bf16(a * w.x - b * w.y, b * w.x + a * w.y);

@@ -93,7 +93,7 @@ __global__ __launch_bounds__(WG) void rotate_kernel(RotateArgs a, int groups) {
       const int e = e0 + k * WG, head = e / per % heads, c = e % per, j = e / per / heads;
       if (e >= all) break;
       const Pieces p = pieces_of(c, a.rot.dims, a.rot.interleaved);
-      rotate_pieces(u[k], v[k], c, a.rot.dims, a.rot.interleaved, cs + j * pairs);
+      if (c < a.rot.dims / 16) rotate_pieces(u[k], v[k], a.rot.interleaved, cs + j * pairs + c * 8);
       const int64_t tok = first + j;
       uint16_t* to = head < a.H ? a.qo + b * a.qo_row + tok * a.qo_tok + (int64_t)head * a.D
                                 : a.ko + b * a.ko_row + tok * a.ko_tok + (int64_t)(head - a.H) * a.D;
