@@ -81,7 +81,9 @@ struct Tile {
   __device__ __forceinline__ static int at_v(int d, int p) { return d * (KEYS / 8) + (p ^ (d & (KEYS / 8 - 1))); }
 };
 
-template <int KIND, int D>
+// SMALL: page < 64, so the keys of a tile may lie in different pages.  Otherwise
+// page, addresses and scales are the whole tile's.
+template <int KIND, int D, bool SMALL>
 __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RESIDENT))) void prefix_attention_kernel(PrefixArgs a) {
   constexpr int NP = KEYS * D / 16 / WG;  // 16-byte pieces of K's codes, and of V's, per thread
   __shared__ Tile<D> sh[2];
@@ -144,43 +146,71 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   const int keys = grp.blocks * a.c.page;  // at most 2^24
   auto page_at = [&](int key) { return key < keys ? table[key >> a.pshift] : -1; };
   auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.c.num_pages; };
-  // The tile on its way: codes, the value scales of the pieces, and of the lane's keys.
+  // The tile on its way: codes, the value scale of the thread's pieces, and what goes with the lane's keys.
+  constexpr int HALVES = SMALL ? 2 : 1;
   u32x4 kc[NP], vc[NP];
-  float vw;                  // the value scale of the thread's value pieces
-  float ks[2], vs[2];        // of the lane's keys in each half,
-  bool ok[2];                // where they exist
-  int pk[NP], pv, pl[2];     // pages of the tile after it
-  const int vp = t & 3;      // the keys of the thread's value pieces: 16 vp ..
+  float vw;                      // the value scale of the thread's value pieces
+  float ks[HALVES], vs[HALVES];  // of the lane's keys in each half,
+  bool ok[HALVES];               // where they exist
+  int pk[NP], pv, pl[HALVES];    // pages of the tile after it
+  const int vp = t & 3;          // the keys of the thread's value pieces: 16 vp ..
   auto find = [&](int tile) {
+    if constexpr (SMALL) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) pk[i] = page_at(tile * KEYS + (i * WG + t) / (D / 16));
-    pv = page_at(tile * KEYS + vp * 16);
+      for (int i = 0; i < NP; ++i) pk[i] = page_at(tile * KEYS + (i * WG + t) / (D / 16));
+      pv = page_at(tile * KEYS + vp * 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) pl[i] = page_at(tile * KEYS + i * 32 + g * 16);
+      for (int i = 0; i < 2; ++i) pl[i] = page_at(tile * KEYS + i * 32 + g * 16);
+    } else {
+      pv = page_at(tile * KEYS);
+    }
   };
   auto bring = [&](int tile) {
     const int mask = a.c.page - 1;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int s = i * WG + t, key = tile * KEYS + s / (D / 16), p = s % (D / 16);
-      kc[i] = u32x4{0, 0, 0, 0};
-      if (there(pk[i]))
-        kc[i] = *reinterpret_cast<const u32x4*>(a.c.k_pages + (((int64_t)pk[i] * a.c.Hkv + h) * a.c.page + (key & mask)) * D + p * 16);
-    }
     vw = 1.f;
+    if constexpr (SMALL) {
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int d = (i * WG + t) / 4;
-      vc[i] = u32x4{0, 0, 0, 0};
-      if (there(pv))
-        vc[i] = *reinterpret_cast<const u32x4*>(a.c.v_pages + (((int64_t)pv * a.c.Hkv + h) * D + d) * a.c.page + ((tile * KEYS + vp * 16) & mask));
-    }
-    if (there(pv)) vw = a.c.v_scale[(int64_t)pv * a.c.Hkv + h];
+      for (int i = 0; i < NP; ++i) {
+        const int s = i * WG + t, key = tile * KEYS + s / (D / 16), p = s % (D / 16);
+        kc[i] = u32x4{0, 0, 0, 0};
+        if (there(pk[i]))
+          kc[i] = *reinterpret_cast<const u32x4*>(a.c.k_pages + (((int64_t)pk[i] * a.c.Hkv + h) * a.c.page + (key & mask)) * D + p * 16);
+      }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ok[i] = there(pl[i]);
-      ks[i] = ok[i] ? a.c.k_scale[(int64_t)pl[i] * a.c.Hkv + h] : 0.f;
-      vs[i] = ok[i] ? a.c.v_scale[(int64_t)pl[i] * a.c.Hkv + h] : 1.f;
+      for (int i = 0; i < NP; ++i) {
+        const int d = (i * WG + t) / 4;
+        vc[i] = u32x4{0, 0, 0, 0};
+        if (there(pv))
+          vc[i] = *reinterpret_cast<const u32x4*>(a.c.v_pages + (((int64_t)pv * a.c.Hkv + h) * D + d) * a.c.page + ((tile * KEYS + vp * 16) & mask));
+      }
+      if (there(pv)) vw = a.c.v_scale[(int64_t)pv * a.c.Hkv + h];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ok[i] = there(pl[i]);
+        ks[i] = ok[i] ? a.c.k_scale[(int64_t)pl[i] * a.c.Hkv + h] : 0.f;
+        vs[i] = ok[i] ? a.c.v_scale[(int64_t)pl[i] * a.c.Hkv + h] : 1.f;
+      }
+    } else {
+      const int pg = __builtin_amdgcn_readfirstlane(pv);
+      ok[0] = there(pg);
+      if (ok[0]) {
+        const int64_t at = (int64_t)pg * a.c.Hkv + h;
+        const int in = (tile * KEYS) & mask;
+        const uint8_t* const k0 = a.c.k_pages + (at * a.c.page + in) * D;  // 64 keys side by side
+        const uint8_t* const v0 = a.c.v_pages + at * D * a.c.page + in;
+        const int row = (t >> 2) * a.c.page + vp * 16;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) kc[i] = *reinterpret_cast<const u32x4*>(k0 + (i * WG + t) * 16);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) vc[i] = *reinterpret_cast<const u32x4*>(v0 + row + i * (WG / 4) * a.c.page);
+        ks[0] = a.c.k_scale[at];
+        vw = vs[0] = a.c.v_scale[at];
+      } else {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) kc[i] = vc[i] = u32x4{0, 0, 0, 0};
+        ks[0] = 0.f;
+        vs[0] = 1.f;
+      }
     }
   };
   auto store = [&](Tile<D>& to) {
@@ -212,11 +242,11 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   for (int tile = tile0; tile < tile1; ++tile) {
     Tile<D>& now = sh[(tile - tile0) & 1];
     store(now);
-    float c[2];
-    ValueScale sc[2];
-    bool here[2];
+    float c[HALVES];
+    ValueScale sc[HALVES];
+    bool here[HALVES];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < HALVES; ++i) {
       here[i] = ok[i];
       c[i] = ok[i] ? ks[i] * a.scale2 : 0.f;
       sc[i] = value_scale(vs[i], ok[i]);
@@ -244,7 +274,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       float top = s[i][0];
 #pragma unroll
       for (int j = 1; j < 16; ++j) top = fmaxf(top, s[i][j]);
-      mx = fmaxf(mx, here[i] ? top * c[i] : NEG_INF);
+      mx = fmaxf(mx, here[i % HALVES] ? top * c[i % HALVES] : NEG_INF);
     }
     {
       float u, v;
@@ -261,14 +291,14 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
     bf16x8 p[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float off = sc[i].log - fmaxf(m, -FAR);  // -inf where there is no block
+      const float off = sc[i % HALVES].log - fmaxf(m, -FAR);  // -inf where there is no block
       float x[16], sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        x[j] = exp2_fast(fmaf(s[i][j], c[i], off));
+        x[j] = exp2_fast(fmaf(s[i][j], c[i % HALVES], off));
         sum += x[j];
       }
-      l = fmaf(sum, sc[i].inv, l);
+      l = fmaf(sum, sc[i % HALVES].inv, l);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         union { bf16x2 h[4]; bf16x8 v; } y;
@@ -395,6 +425,12 @@ int join(const PrefixArgs& a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
+template <int KIND>
+auto kernel_of(const sv_cache& c) -> void (*)(PrefixArgs) {
+  if (c.D == 64) return c.page < 64 ? prefix_attention_kernel<KIND, 64, true> : prefix_attention_kernel<KIND, 64, false>;
+  return c.page < 64 ? prefix_attention_kernel<KIND, 128, true> : prefix_attention_kernel<KIND, 128, false>;
+}
+
 }  // namespace
 
 namespace svr {
@@ -427,9 +463,7 @@ int prefix_plan(const sv_cache& c, const sv_prefix& p, int T, int H, PrefixPlan&
 }
 
 int prefix_launch(const PrefixArgs& a, hipStream_t st) {
-  void (*const k)(PrefixArgs) =
-      a.c.kind == SV_E4M3 ? (a.c.D == 64 ? prefix_attention_kernel<SV_E4M3, 64> : prefix_attention_kernel<SV_E4M3, 128>)
-                          : (a.c.D == 64 ? prefix_attention_kernel<SV_INT8, 64> : prefix_attention_kernel<SV_INT8, 128>);
+  void (*const k)(PrefixArgs) = a.c.kind == SV_E4M3 ? kernel_of<SV_E4M3>(a.c) : kernel_of<SV_INT8>(a.c);
   const int64_t grid = ((int64_t)a.qtiles * a.c.Hkv * a.splits + 7) / 8 * 8;
   hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(WG), 0, st, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
