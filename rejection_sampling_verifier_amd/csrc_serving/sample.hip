@@ -268,6 +268,21 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void sa
   u32x4 v[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) v[j] = x.load(q0 + j * WG);
+  const bool cut = !r.greedy && r.cut();
+  if (a.fill) {
+    // The output's vectors: what is kept of a row that rules cut comes later.
+    ET* const y = static_cast<ET*>(a.out) + b * a.out_row + (int64_t)(row % a.P) * a.out_pos;
+    const uint32_t none = Tr<ET>::NEG_INF_WORD;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int id = x.first(q0 + j * WG);
+      if (id >= 0 && id + VEC <= a.V) {
+        *reinterpret_cast<u32x4*>(y + id) = cut ? u32x4{none, none, none, none} : v[j];
+      } else {
+        for (int k = max(0, -id); k < VEC && id + k < a.V; ++k) y[id + k] = cut ? minus_inf<ET>() : x.p[id + k];
+      }
+    }
+  }
   if (a.arrived) {  // what the row's work-groups will add to
     for (int i = chunk * WG + t; i < BINS; i += a.C * WG) {
       a.masses[(int64_t)row * BINS + i] = 0;
@@ -308,21 +323,6 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(4))) void sa
   const float top = key < Bits<ET>::LEAST ? NEG_INF : Bits<ET>::logit(key);
   Chunk o = {0.0, top, NEG_INF, INT_MAX, 0};
   Chunk* const put = a.chunks + (int64_t)row * a.C + chunk;
-  const bool cut = !r.greedy && r.cut();
-  if (a.fill) {
-    // The output's vectors: what is kept of a row that rules cut comes later.
-    ET* const y = static_cast<ET*>(a.out) + b * a.out_row + (int64_t)(row % a.P) * a.out_pos;
-    const uint32_t none = Tr<ET>::NEG_INF_WORD;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int id = x.first(q0 + j * WG);
-      if (id >= 0 && id + VEC <= a.V) {
-        *reinterpret_cast<u32x4*>(y + id) = cut ? u32x4{none, none, none, none} : v[j];
-      } else {
-        for (int k = max(0, -id); k < VEC && id + k < a.V; ++k) y[id + k] = cut ? minus_inf<ET>() : x.p[id + k];
-      }
-    }
-  }
   if (r.greedy || top == NEG_INF) {
     if (top > NEG_INF) {
       int first = INT_MAX;

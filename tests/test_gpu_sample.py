@@ -294,3 +294,19 @@ def test_refusals_on_device_tensors():
         rsv.truncate_logits(x[:, :2], T, out=x[:, 1:])
     with pytest.raises(rsv.SpecVerifyError):
         rsv.truncate_logits(x, T, top_p=x.view(-1)[:2], out=x)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_that_nothing_cuts_keep_their_bits(dtype):
+    """NaN and zeros of both signs among them, in batches of every size, beside rows that are cut."""
+    for B, V in ((3, 3001), (600, 8200)):
+        x = logits_of(29, B, 2, V, dtype)
+        x[:, :, 5] = float("nan")
+        x[:, :, 6] = -float("nan")
+        x[:, :, 7:9] = torch.tensor([-0.0, 0.0]).to(x.dtype)
+        T = torch.tensor([0.0, 0.9, 0.9] * (B // 3))
+        k = torch.tensor([3, 0, 3] * (B // 3), dtype=torch.int32)
+        got = rsv.truncate_logits(x.cuda(), T.cuda(), top_k=k.cuda()).cpu()
+        bits = torch.int16 if dtype == "bf16" else torch.int32
+        assert torch.equal(got[0::3].view(bits), x[0::3].view(bits)) and torch.equal(got[1::3].view(bits), x[1::3].view(bits))
+        assert ((got[2::3] > -float("inf")).sum(2) == 3).all()
