@@ -106,8 +106,8 @@ __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int b) {
 // 2^52, which leaves its whole part in the sum's low bits.  fp64 additions and
 // multiply-adds run at the rate of fp32 ones here.  The factors are held in
 // scalar registers: as literals each would take two instructions to every
-// multiply-add (256 rows of 201,088 with the series of 2^r to the 10th power and
-// literals: 81 us).
+// multiply-add (256 rows of 201,088 54 us; with the series of 2^r to the 10th
+// power and literals 81).
 struct Series {
   double k[8];  // of r, r^2, ...; 1 of r^0
   __device__ __forceinline__ Series()
@@ -715,8 +715,8 @@ struct RowWork {
   }
 
   // The bound among the kept tokens of orders [from, to], WG of them at most: a
-  // thread adds up what comes before its own (15 us less on a row of float32
-  // logits than going on with bins).
+  // thread adds up what comes before its own (the row's kernel for 64 x 6 rows cut
+  // by top-k and top-p 29 -> 23 us, against bins down to equal logits and ids).
   template <bool MASS>
   __device__ __forceinline__ void rank(uint32_t from, uint32_t to, uint64_t need) {
     uint64_t* const key = sh.mass;  // order << 32 | ~id: larger ones come first
