@@ -332,8 +332,9 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 
 // out = the mean of what a row has of its own and of its prefix's parts, each
 // with its weight.  D / 4 threads take every PG-th part of a token's head, four
-// parts' loads at once, and the PG groups join in their order (8 rows of one
-// token, 64 parts: 51 us with one thread to a channel's parts).
+// parts' loads at once, and the PG groups join in their order.  PG = 8 beside
+// many parts (8 rows of one token, 64 parts: 5.7 us, 18 with PG = 1), 1 beside
+// up to 8 (64 x 6 tokens, 5 parts: 9.6 us, 25 with PG = 8).
 template <int D, int PG>
 __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
   constexpr int L = D / 4, ROWS = WG / (L * PG), AHEAD = 4;

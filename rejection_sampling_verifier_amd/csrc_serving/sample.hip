@@ -1110,17 +1110,21 @@ __global__ __launch_bounds__(WG) void truncate_kernel(SampleArgs a, int per, int
 
 struct Plan {
   int nv, C, cap, share;
+  bool fill;
   size_t subs, lists, bounds, arrived, masses, counts, total;
 };
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Chunks of 2 or 8 vectors per thread: small ones where the large ones are too
-// few to fill the chip.
+// Chunks of 8 vectors per thread, or of 2 for few rows, whose chunks would be
+// too few: six rows of 128,256 cut by top-p 33 us against 106, both kernels, as
+// four times as many work-groups count a row; but 16 rows of 151,936 with top-k
+// 44 against 23, as the k-th largest of a small chunk leaves more candidates.
 int make_plan(int B, int P, int V, int dtype, bool cuts, bool truncate, Plan& pl) {
   const int vec = dtype == SV_BF16 ? 8 : 4;
   const int64_t rows = (int64_t)B * P;
   auto chunks = [&](int nv) { return (V + vec - 1 + WG * nv * vec - 1) / (WG * nv * vec); };
-  pl.nv = rows * chunks(8) < 1024 && chunks(2) <= MAX_CHUNKS ? 2 : 8;
+  pl.nv = rows * chunks(8) < 64 && chunks(2) <= MAX_CHUNKS ? 2 : 8;
+  pl.fill = truncate && rows * chunks(8) >= 1024;
   pl.C = chunks(pl.nv);
   pl.cap = cuts ? (pl.nv == 8 ? 1024 : 512) : 0;
   if (rows * pl.C > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
@@ -1259,10 +1263,10 @@ extern "C" int spec_verify_truncate(const void* logits, int64_t row_stride, int6
   a.out_row = out_row_stride;
   a.out_pos = out_stride;
   // Large batches get -inf written as they are read, and the kept logits after that, where vectors of both are alike
-  // (64 x 6 rows of 151,936: the third kernel alone takes 42 us).
+  // (64 x 6 rows of 151,936: the third kernel alone takes 42 us).  In small ones that kernel takes 4, and a row with many tokens left would be gone through by one work-group.
   const int64_t vec = 16 / es;
   const int64_t apart = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(logits)) / (int64_t)es;
-  a.fill = pl.nv == 8 && !inplace && apart % vec == 0 && (out_row_stride - row_stride) % vec == 0 &&
+  a.fill = pl.fill && !inplace && apart % vec == 0 && (out_row_stride - row_stride) % vec == 0 &&
            (out_stride - stride) % vec == 0;
   if (!a.fill) a.bounds = reinterpret_cast<uint2*>(static_cast<char*>(workspace) + pl.bounds);
   return dtype == SV_BF16 ? launch_nv<uint16_t>(a, pl, inplace, stream) : launch_nv<float>(a, pl, inplace, stream);
