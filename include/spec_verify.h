@@ -33,7 +33,7 @@
  * only; outputs are fully overwritten.  The library allocates nothing, keeps
  * no mutable global state other than spec_verify_noalloc's static scratch,
  * and never synchronises: every call only enqueues
- * at most three kernels on `stream` (no memory set or copy), so a call can
+ * at most four kernels on `stream` (no memory set or copy), so a call can
  * be captured in a HIP graph and replayed; outputs are valid once the caller
  * has synchronised that stream.  Calls on different workspaces are
  * reentrant.
@@ -872,7 +872,7 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int64_t stride,
  * out          element (b, i, x) at b * out_row_stride + i * out_stride + x.  It
  *              may be the logits themselves with the same strides; otherwise it
  *              must not overlap them.
- * Other arguments as spec_verify_sample.  Three kernels.
+ * Other arguments as spec_verify_sample.  Two or three kernels.
  */
 int spec_verify_truncate(const void* logits, int64_t row_stride,
                          int64_t stride, const float* temperature,
