@@ -836,7 +836,7 @@ int spec_verify_append(const void* k, const void* v, int64_t kv_row,
  * Draw j is the smallest kept id x for which the mass of the kept ids up to x
  * exceeds uniforms[b][i][j] times the mass of all kept: spec_verify's draw,
  * and with top_k alone spec_verify's truncated draft.  Weights are formed in
- * float64; where rules cut a row masses are whole multiples of 2^-43, so a
+ * float64, and are 0 under 2^-1000, for which no draw is; where rules cut a row masses are whole multiples of 2^-43, so a
  * result does not depend on any order of summation.
  * Rows with T <= 0 (or NaN) take the largest logit's lowest id.  A NaN logit
  * counts as -inf and -inf is never drawn; where there is nothing else the

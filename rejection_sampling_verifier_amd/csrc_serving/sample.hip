@@ -126,10 +126,12 @@ struct Series {
   }
 };
 // The weight of a logit against a maximum, c = log2(e) / T.  1 at the maximum,
-// whatever it is, 0 for -inf.
+// whatever it is; 0 for -inf, for all else beside +inf, and under 2^-1000,
+// where float64's range ends.
 __device__ __forceinline__ double weight(float l, float top, double c) {
   if (l == top) return 1.0;
-  return l == NEG_INF ? 0.0 : Series().exp2(fmax(((double)l - (double)top) * c, -1000.0));
+  const double y = ((double)l - (double)top) * c;
+  return y >= -1000.0 ? Series().exp2(y) : 0.0;
 }
 // ln of a token's part of the sum `total` of the weights.
 __device__ __forceinline__ float log_part(float l, float top, float T, double total) {
@@ -917,22 +919,37 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(3))) void sa
         }
       }
       const float top = sh.top[ch];
-      left = (left - (ch ? sh.upto[ch - 1] : 0.0)) / weight(top, max, c);
+      const double of = weight(top, max, c), least = 0x1p-1000 / of;  // what weighs less against the chunk's maximum weighs nothing
+      left = (left - (ch ? sh.upto[ch - 1] : 0.0)) / of;
       const double own = lane < SUBS ? a.subs[((int64_t)row * a.C + ch) * SUBS + lane] : 0.0;
-      double z = wave_upto(own);
-      uint64_t past = __ballot(own > 0.0 && z > left);
-      const uint64_t some = __ballot(own > 0x1p-900);
-      const int sub = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
-      left -= __shfl(z - own, sub, 64);
-      const int q = ch * WG * NV + sub / NWAVE * WG + sub % NWAVE * 64 + lane;
-      const u32x4 v = x.load(q);
-      double e = 0.0;
+      const double upto = wave_upto(own);
+      // Of the wave's vectors whose running sum passes what is left, the first that hold a token with a weight; if
+      // there are none, the last that do.  A sum alone does not tell: 2^-1000 is in it for each -inf.  The chunk's
+      // maximum is in one of them.
+      const uint64_t may = __ballot(own >= least);
+      uint64_t up = __ballot(upto > left) & may, down = may & ~up, any = 0;
+      u32x4 v;
+      int q = 0;
+      double e = 0.0, before = 0.0;
+      while (!any && (up | down)) {
+        const int sub = up ? __builtin_ctzll(up) : 63 - __builtin_clzll(down);
+        up &= ~(1ull << sub);
+        down &= ~(1ull << sub);
+        q = ch * WG * NV + sub / NWAVE * WG + sub % NWAVE * 64 + lane;
+        v = x.load(q);
+        e = 0.0;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) e += weight(logit_at<ET>(v, k), top, c);
-      z = wave_upto(e);
-      past = __ballot(e > 0.0 && z > left);
-      const uint64_t any = __ballot(e > 0.0);
-      const int who = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(any);
+        for (int k = 0; k < VEC; ++k) {
+          const double g = weight(logit_at<ET>(v, k), top, c);
+          e += g >= least ? g : 0.0;
+        }
+        any = __ballot(e > 0.0);
+        before = __shfl(upto - own, sub, 64);
+      }
+      left -= before;
+      const double z = wave_upto(e);
+      const uint64_t past = __ballot(e > 0.0 && z > left);
+      const int who = past ? __builtin_ctzll(past) : any ? 63 - __builtin_clzll(any) : 0;
       if (lane == who) {
         double sum = z - e;
         int id = -1;
@@ -940,7 +957,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(3))) void sa
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           const float y = logit_at<ET>(v, k);
-          const double g = weight(y, top, c);
+          const double w = weight(y, top, c), g = w >= least ? w : 0.0;
           if (g > 0.0 && (id < 0 || !(sum > left))) {
             id = x.first(q) + k;
             l = y;
