@@ -629,8 +629,9 @@ typedef struct {
 /*
  * spec_verify_attention_prefix - spec_verify_attention of rows that share
  * prefixes: each query sees its row's prefix too, and softmax and weights are
- * over both.  A prefix's keys are read once for all its rows.  A probability
- * beside a prefix's value is rounded to 8 bits.
+ * over both.  A prefix's keys are read once for all its rows.  Beside its
+ * codes a probability is rounded to 11 bits, to at least 8 where it is less
+ * than 2^-16 of the largest (each times its value scale) of 64 keys.
  *
  * weights[b][t][j] are those of the row's own blocks.
  * prefix       NULL: spec_verify_attention.

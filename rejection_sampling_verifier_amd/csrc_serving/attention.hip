@@ -49,7 +49,6 @@ constexpr int CMIN = 4;        // tiles of a run at least: one per wave
 // Two, each with a whole tile on its way, beat three of half the registers
 // (16 rows of up to 16k tokens, one query each, D = 128: 76 against 83 us).
 constexpr int RESIDENT = 2;
-constexpr float GROW = 4.f;    // a maximum may lag this much (a factor of 16) before the sums are rescaled
 // Where f16 takes probabilities times value scales: a tile's largest of both
 // makes 2^(MID - HALF) to 2^(MID + HALF + 1), at most 2^15 and, as f16's
 // smallest step is 2^-24, a probability is off by at most 2^-21 of the
@@ -58,11 +57,6 @@ constexpr float MID = 5.f, HALF = 9.f, STEP = 3.f;
 // Tail and new tokens: 2^x that the sums take, so that 2^GROW times 320 of
 // them times the largest bf16 stay below 2^127.
 constexpr int NEAR_X = -18;
-constexpr float ALIKE = 4.f;   // value scales of one tile that differ by 2^5 and more need more range than f16 has
-constexpr float LOW = -110.f;  // scores further below the maximum count as this far, so that 2^x stays in float32's range
-constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
-constexpr int TOP = 100;       // sums are not raised above 2^TOP
-constexpr int LOST = -40;
 
 struct AttnArgs {
   const uint16_t* q;

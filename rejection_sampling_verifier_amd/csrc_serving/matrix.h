@@ -9,6 +9,12 @@ namespace svr {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float VMIN = 0x1p-126f;  // smallest value scale told apart (see spec_verify.h)
+constexpr float GROW = 4.f;    // a maximum may lag this much (a factor of 16) before the sums are rescaled
+constexpr float ALIKE = 4.f;   // value scales of one tile that differ by 2^5 and more need more range than f16 has
+constexpr float LOW = -110.f;  // scores further below the maximum count as this far, so that 2^x stays in float32's range
+constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
+constexpr int TOP = 100;       // sums are not raised above 2^TOP
+constexpr int LOST = -40;
 
 // ---- lanes 16 and 32 apart --------------------------------------------------
 __device__ __forceinline__ void swap16(float x, float& u, float& v) {

@@ -11,13 +11,15 @@
 //
 // A work-group takes MT = 128 queries, 32 to a wave, and one of S parts of the
 // prefix's keys, in tiles of 64.  The tile's codes come to registers while the
-// tile before is worked on, are widened to bf16 once for the work-group and
-// kept in LDS twice, so that one barrier a tile will do.  The products are
-// transposed, S^T = K Q^T and O^T = V^T P^T, with the keys dealt so that lane
-// group g = lane / 32 of a product has the scores of keys 16 g .. 16 g + 15 of
-// 32, which is the operand that O^T needs: probabilities stay in their lanes.
-// A block's value scale 2^e f goes into the values (2^e, exactly) and into the
-// probabilities (f, below 2), which are rounded to bf16.
+// tile before is worked on, are widened once for the work-group, K's to bf16
+// and V's to f16 (both exact), and kept in LDS twice, so that one barrier a
+// tile will do.  The products are transposed, S^T = K Q^T and O^T = V^T P^T,
+// with the keys dealt so that lane group g = lane / 32 of a product has the
+// scores of keys 16 g .. 16 g + 15 of 32, which is the operand that O^T needs:
+// probabilities stay in their lanes.  They take their block's value scale and
+// a power of two that follows the tile's largest of both, as in attention.hip,
+// so that f16 holds 11 bits of them whatever the scales are.  Where some lie too
+// far below the largest for f16, what it loses goes into a product of its own.
 
 #include <algorithm>
 #include <climits>
@@ -30,11 +32,14 @@ using namespace svr;
 
 namespace {
 
-constexpr float FAR = 0x1p127f;  // in place of an infinite -m, where every score is -inf
-constexpr float GROW = 4.f;      // a maximum may lag this much (a factor of 16) before the sums are rescaled
 constexpr int KEYS = 64;         // of a tile
 constexpr int MT = 32 * NWAVE;   // queries of one
 constexpr int RESIDENT = 2;      // work-groups of a CU, by registers and LDS
+// A tile's largest probability times value scale makes 2^(MID - HALF) to 2^(MID
+// + HALF + 1) in f16, which holds at least 8 bits of what is 2^LEAST and more.
+constexpr float MID = 8.f, HALF = 6.f, STEP = 3.f;
+constexpr int LEAST = -17;
+constexpr int FRESH = -200;      // a power of two that no tile has: of sums that hold nothing yet
 
 // A group's prefix and its rows, brought into range.
 struct Group {
@@ -51,24 +56,19 @@ __device__ __forceinline__ Group group_of(const PrefixArgs& a, int g) {
   return r;
 }
 
-template <int KIND>
-__device__ __forceinline__ u32x4 widen_by(uint32_t w0, uint32_t w1, float scale) {
-  union { bf16x2 p[4]; u32x4 v; } r;
-  if (KIND == SV_E4M3) {
-    r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
-    r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
-    r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
-    r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
-  } else {
+typedef short i16x2 __attribute__((ext_vector_type(2)));
+
+// Codes in f16 as bf16, which holds them exactly too, times 2^-112: the exponent of f16 in the place of bf16's, two
+// instructions to two codes (none has more than 8 bits or is below 2^-9, so what the shift drops is zero).
+constexpr float CODE = 0x1p112f;
+__device__ __forceinline__ bf16x8 f16_as_bf16(f16x8 v) {
+  u32x4 r = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t w = k < 2 ? w0 : w1;
-      const int s = (k & 1) * 16;
-      const float x = (float)(int8_t)(w >> s) * scale, y = (float)(int8_t)(w >> (s + 8)) * scale;
-      r.v[k] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-    }
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t two = r[k];  // of r[k] itself __builtin_bit_cast takes r's first word (clang of ROCm 7.2.0)
+    r[k] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(i16x2, two) >> 3) & 0x8FFF8FFFu;
   }
-  return r.v;
+  return as_bf16(r);
 }
 
 // A tile's place in LDS: pieces of 8 values (16 bytes), piece p of a row at p ^
@@ -115,21 +115,27 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       const int at = __builtin_ctzll(past);
       qt -= __builtin_amdgcn_readlane(inc - n, at);
       which += at;
-#pragma unroll
-      for (int k = 0; k < (int)(sizeof(Group) / 4); ++k)
-        reinterpret_cast<int*>(&grp)[k] = __builtin_amdgcn_readlane(reinterpret_cast<int*>(&grp)[k], at);
       break;
     }
     qt -= __builtin_amdgcn_readlane(inc, 63);
   }
+#pragma unroll
+  for (int k = 0; k < (int)(sizeof(Group) / 4); ++k)  // past the loop, so that they are scalars
+    reinterpret_cast<int*>(&grp)[k] = __builtin_amdgcn_readlane(reinterpret_cast<int*>(&grp)[k], which & 63);
   const int tile0 = part * grp.per, tile1 = min(tile0 + grp.per, grp.tiles);
   if (tile0 >= tile1) return;
 
   // The lane's query.
-  const int r = qt * MT + w * 32 + col, in = r / each_row, rest = r % each_row, tok = rest / a.G;
-  const int b = grp.first + min(in, grp.rows - 1);
-  const bool live = in < grp.rows && tok < (a.qlens ? min(max(a.qlens[b], 0), a.T) : a.T);
-  const int head = h * a.G + rest % a.G;
+  struct Query {
+    int b, tok, head;
+    bool live;
+  };
+  auto query_of = [&](int t, int G) {
+    const int r = qt * MT + (t >> 6) * 32 + (t & 31), in = r / (a.T * G), rest = r % (a.T * G), tok = rest / G;
+    const int b = grp.first + min(in, grp.rows - 1);
+    return Query{b, tok, h * G + rest % G, in < grp.rows && tok < (a.qlens ? min(max(a.qlens[b], 0), a.T) : a.T)};
+  };
+  const auto [b, tok, head, live] = query_of(t, a.G);
   const bool queries = __any(live);  // a wave without only brings keys
   bf16x8 q[D / 16];
   {
@@ -146,35 +152,26 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   const int keys = grp.blocks * a.c.page;  // at most 2^24
   auto page_at = [&](int key) { return key < keys ? table[key >> a.pshift] : -1; };
   auto there = [&](int pg) { return (uint32_t)pg < (uint32_t)a.c.num_pages; };
-  // The tile on its way: codes, the value scale of the thread's pieces, and what goes with the lane's keys.
+  // The tile on its way: codes, and what goes with the lane's keys.
   constexpr int HALVES = SMALL ? 2 : 1;
   u32x4 kc[NP], vc[NP];
-  float vw;                      // the value scale of the thread's value pieces
   float ks[HALVES], vs[HALVES];  // of the lane's keys in each half,
   bool ok[HALVES];               // where they exist
-  int pk[NP], pv, pl[HALVES];    // pages of the tile after it
+  int pv;                        // the page of the tile after it, or of its 16 keys from 16 vp on
   const int vp = t & 3;          // the keys of the thread's value pieces: 16 vp ..
   auto find = [&](int tile) {
-    if constexpr (SMALL) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) pk[i] = page_at(tile * KEYS + (i * WG + t) / (D / 16));
-      pv = page_at(tile * KEYS + vp * 16);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) pl[i] = page_at(tile * KEYS + i * 32 + g * 16);
-    } else {
-      pv = page_at(tile * KEYS);
-    }
+    pv = page_at(tile * KEYS + (SMALL ? vp * 16 : 0));
   };
   auto bring = [&](int tile) {
     const int mask = a.c.page - 1;
-    vw = 1.f;
     if constexpr (SMALL) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const int s = i * WG + t, key = tile * KEYS + s / (D / 16), p = s % (D / 16);
+        const int pk = __builtin_amdgcn_readlane(pv, (i * WG + __builtin_amdgcn_readfirstlane(w) * 64) / D);  // a wave's keys are of one
         kc[i] = u32x4{0, 0, 0, 0};
-        if (there(pk[i]))
-          kc[i] = *reinterpret_cast<const u32x4*>(a.c.k_pages + (((int64_t)pk[i] * a.c.Hkv + h) * a.c.page + (key & mask)) * D + p * 16);
+        if (there(pk))
+          kc[i] = *reinterpret_cast<const u32x4*>(a.c.k_pages + (((int64_t)pk * a.c.Hkv + h) * a.c.page + (key & mask)) * D + p * 16);
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -183,12 +180,12 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
         if (there(pv))
           vc[i] = *reinterpret_cast<const u32x4*>(a.c.v_pages + (((int64_t)pv * a.c.Hkv + h) * D + d) * a.c.page + ((tile * KEYS + vp * 16) & mask));
       }
-      if (there(pv)) vw = a.c.v_scale[(int64_t)pv * a.c.Hkv + h];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        ok[i] = there(pl[i]);
-        ks[i] = ok[i] ? a.c.k_scale[(int64_t)pl[i] * a.c.Hkv + h] : 0.f;
-        vs[i] = ok[i] ? a.c.v_scale[(int64_t)pl[i] * a.c.Hkv + h] : 1.f;
+        const int p0 = __builtin_amdgcn_readlane(pv, 2 * i), p1 = __builtin_amdgcn_readlane(pv, 2 * i + 1), pl = g ? p1 : p0;
+        ok[i] = there(pl);
+        ks[i] = ok[i] ? a.c.k_scale[(int64_t)pl * a.c.Hkv + h] : 0.f;
+        vs[i] = ok[i] ? a.c.v_scale[(int64_t)pl * a.c.Hkv + h] : 1.f;
       }
     } else {
       const int pg = __builtin_amdgcn_readfirstlane(pv);
@@ -204,7 +201,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
         for (int i = 0; i < NP; ++i) vc[i] = *reinterpret_cast<const u32x4*>(v0 + row + i * (WG / 4) * a.c.page);
         ks[0] = a.c.k_scale[at];
-        vw = vs[0] = a.c.v_scale[at];
+        vs[0] = a.c.v_scale[at];
       } else {
 #pragma unroll
         for (int i = 0; i < NP; ++i) kc[i] = vc[i] = u32x4{0, 0, 0, 0};
@@ -217,15 +214,14 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int s = i * WG + t, key = s / (D / 16), p = s % (D / 16) * 2;
-      to.k[Tile<D>::at_k(key, p)] = widen_by<KIND>(kc[i][0], kc[i][1], 1.f);
-      to.k[Tile<D>::at_k(key, p + 1)] = widen_by<KIND>(kc[i][2], kc[i][3], 1.f);
+      to.k[Tile<D>::at_k(key, p)] = __builtin_bit_cast(u32x4, widen<KIND>(kc[i][0], kc[i][1]));
+      to.k[Tile<D>::at_k(key, p + 1)] = __builtin_bit_cast(u32x4, widen<KIND>(kc[i][2], kc[i][3]));
     }
-    const float by = ldexpf(1.f, value_scale(vw, true).e);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int d = (i * WG + t) / 4;
-      to.v[Tile<D>::at_v(d, vp * 2)] = widen_by<KIND>(vc[i][0], vc[i][1], by);
-      to.v[Tile<D>::at_v(d, vp * 2 + 1)] = widen_by<KIND>(vc[i][2], vc[i][3], by);
+      to.v[Tile<D>::at_v(d, vp * 2)] = __builtin_bit_cast(u32x4, widen_f16<KIND>(vc[i][0], vc[i][1]));
+      to.v[Tile<D>::at_v(d, vp * 2 + 1)] = __builtin_bit_cast(u32x4, widen_f16<KIND>(vc[i][2], vc[i][3]));
     }
   };
 
@@ -235,6 +231,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
   float m = NEG_INF, l = 0.f;  // l: of the lane's own keys
+  int x = FRESH;               // the sums o are times 2^x
 
   find(tile0);
   bring(tile0);
@@ -242,14 +239,13 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
   for (int tile = tile0; tile < tile1; ++tile) {
     Tile<D>& now = sh[(tile - tile0) & 1];
     store(now);
-    float c[HALVES];
-    ValueScale sc[HALVES];
+    float c[HALVES], v[HALVES];
     bool here[HALVES];
 #pragma unroll
     for (int i = 0; i < HALVES; ++i) {
       here[i] = ok[i];
       c[i] = ok[i] ? ks[i] * a.scale2 : 0.f;
-      sc[i] = value_scale(vs[i], ok[i]);
+      v[i] = vs[i];
     }
     __syncthreads();
     if (tile + 1 < tile1) {
@@ -257,69 +253,151 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
       find(min(tile + 2, tile1 - 1));
     }
     if (!queries) continue;
-    f32x16 s[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[i][j] = 0.f;
-      const int key = i * 32 + 16 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, now.k[Tile<D>::at_k(key, ks * 2 + g)]), q[ks],
-                                                       s[i], 0, 0, 0);
+    // Pages whose value scales are too unlike for f16 are worked on one after the other, as parts of 16 keys: those of
+    // one half and lane group each.
+    int passes = 1;
+    if constexpr (SMALL) {
+      const float e0 = value_scale(v[0], here[0]).e, e1 = value_scale(v[1], here[1]).e;
+      float x0, x1;
+      swap32(fmaxf(here[0] ? e0 : -150.f, here[1] ? e1 : -150.f), x0, x1);
+      const float least = fmaxf(x0, x1) - ALIKE;
+      if (__any((here[0] & (e0 < least)) | (here[1] & (e1 < least)))) passes = 4;
     }
-    float mx = NEG_INF;
+    for (int pass = 0; pass < passes; ++pass) {
+      bool on[HALVES];
+      ValueScale sc[HALVES];
+      if constexpr (SMALL) asm volatile("" : "+v"(v[0]), "+v"(v[1]) :: "memory");  // nothing is kept in registers from pass to pass
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float top = s[i][0];
-#pragma unroll
-      for (int j = 1; j < 16; ++j) top = fmaxf(top, s[i][j]);
-      mx = fmaxf(mx, here[i % HALVES] ? top * c[i % HALVES] : NEG_INF);
-    }
-    {
-      float u, v;
-      swap32(mx, u, v);
-      mx = fmaxf(u, v);
-    }
-    if (__any(mx > m + GROW)) {
-      const float to = fmaxf(m, mx), f = to == NEG_INF ? 1.f : exp2_fast(m - to);
-      m = to;
-      l *= f;
-#pragma unroll
-      for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
-    }
-    bf16x8 p[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float off = sc[i % HALVES].log - fmaxf(m, -FAR);  // -inf where there is no block
-      float x[16], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        x[j] = exp2_fast(fmaf(s[i][j], c[i % HALVES], off));
-        sum += x[j];
+      for (int i = 0; i < HALVES; ++i) {
+        on[i] = here[i] & (passes == 1 || pass == 2 * i + g);
+        sc[i] = value_scale(v[i], on[i]);
       }
-      l = fmaf(sum, sc[i % HALVES].inv, l);
+      f32x16 s[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        union { bf16x2 h[4]; bf16x8 v; } y;
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y.h[j] = __builtin_convertvector(f32x2{x[8 * u + 2 * j], x[8 * u + 2 * j + 1]}, bf16x2);
-        p[i][u] = y.v;
+        for (int j = 0; j < 16; ++j) s[i][j] = 0.f;
+        const int key = i * 32 + 16 * (col >> 2 & 1) + 4 * (col >> 3) + (col & 3);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          s[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, now.k[Tile<D>::at_k(key, ks * 2 + g)]), q[ks],
+                                                         s[i], 0, 0, 0);
       }
-    }
+      float mx = NEG_INF, top = HALVES == 1 ? (float)sc[0].e : -150.f;  // the tile's largest score and value scale
 #pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt)
+      for (int i = 0; i < 2; ++i) {
+        float most = s[i][0];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int j = 1; j < 16; ++j) most = fmaxf(most, s[i][j]);
+        mx = fmaxf(mx, on[i % HALVES] ? most * c[i % HALVES] : NEG_INF);
+        if (HALVES > 1) top = fmaxf(top, on[i % HALVES] ? (float)sc[i % HALVES].e : -150.f);
+      }
+      {
+        float u, v;
+        swap32(mx, u, v);
+        mx = fmaxf(u, v);
+        if (HALVES > 1) {
+          swap32(top, u, v);
+          top = fmaxf(u, v);
+        }
+      }
+      // Maximum and power of two follow the tile (see softmax_cached in attention.hip).
+      auto off_range = [&]() { return fabsf(fmaxf(mx - m, LOW) + (top - MID + (float)x)) > HALF; };
+      if (__any((mx > m + GROW) | off_range())) {
+        const float to = fmaxf(m, mx), f = to == NEG_INF ? 1.f : exp2_fast(m - to);
+        const bool fresh = __all(m == NEG_INF);  // the sums are zero
+        m = to;
+        l *= f;
+        const float e = fmaxf(mx - m, LOW) + top;
+        const float goal = x == FRESH ? MID + HALF - GROW : e + (float)x > MID ? MID + HALF - STEP : MID - HALF + STEP;
+        int dx = mx > NEG_INF && off_range() ? (int)rintf(goal - e) - x : 0;
+        if (!fresh) {
+#pragma unroll
+          for (int dt = 0; dt < D / 32; ++dt) o[dt] *= f;
+          if (__any(dx != 0)) {
+            float big = 0.f;
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) big = fmaxf(big, fabsf(o[dt][j]));
+            float u, v;
+            swap32(big, u, v);
+            big = fmaxf(u, v);
+            if (big > 0.f) dx = min(dx, TOP - __builtin_amdgcn_frexp_expf(big));
+            int left = dx;
+            do {  // once, but between the ends of float32's range
+              const int step = min(max(left, -120), 120);
+              left -= step;
+              const float k = ldexpf(1.f, step);
+#pragma unroll
+              for (int dt = 0; dt < D / 32; ++dt) o[dt] *= k;
+            } while (__any(left != 0));
+          }
+        }
+        x += dx;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // Beside sums that may not be raised further: what is added for 2^LOST is 2^-130 of the largest of them.
+        const int up = max(sc[i % HALVES].e + x, LOST);
+        const float off = (float)up + sc[i % HALVES].log - fmaxf(m, -FAR);  // -inf where there is no block
+        float y[16], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          y[j] = exp2_fast(fmaf(s[i][j], c[i % HALVES], off));
+          sum += y[j];
+        }
+        l += ldexpf(sum * sc[i % HALVES].inv, -up);
+        float low = y[0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) low = fminf(low, y[j]);
+        f16x8 p[2];
+        const bool lost = __any(on[i % HALVES] & (low < ldexpf(1.f, LEAST)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          union { f16x2 h[4]; f16x8 v; } z;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z.h[j] = __builtin_convertvector(f32x2{y[8 * u + 2 * j], y[8 * u + 2 * j + 1]}, f16x2);
+          p[u] = z.v;
+          // What f16 lost, in bf16, which has float32's range.  Scores whose 64 keys span e^19 and more come here: 64 x 6
+          // tokens over 8192 keys take 130 us a call with scores of a standard deviation of 1, 165 with 4.
+          if (lost) {
+            union { bf16x2 h[4]; bf16x8 v; } r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              r.h[j] = __builtin_convertvector(f32x2{fmaf((float)z.v[2 * j], -CODE, y[8 * u + 2 * j] * CODE),
+                                                     fmaf((float)z.v[2 * j + 1], -CODE, y[8 * u + 2 * j + 1] * CODE)}, bf16x2);
+            asm volatile("" ::: "memory");  // the values are read where they are used: there are no registers for more
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+              o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  f16_as_bf16(__builtin_bit_cast(f16x8, now.v[Tile<D>::at_v(dt * 32 + col, i * 4 + g * 2 + u)])), r.v, o[dt], 0, 0, 0);
+            asm volatile("" ::: "memory");
+          }
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, now.v[Tile<D>::at_v(dt * 32 + col, i * 4 + g * 2 + u)]), p[i][u], o[dt], 0, 0, 0);
+#pragma unroll
+          for (int dt = 0; dt < D / 32; ++dt)
+            o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(f16x8, now.v[Tile<D>::at_v(dt * 32 + col, i * 4 + g * 2 + u)]), p[u], o[dt], 0, 0, 0);
+      }
+    }
   }
   l = sum32(l);
-  if (!live) return;
-  const float whole = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = (((int64_t)part * a.c.B + b) * a.T + tok) * a.H + head;
+  int again = t, group = a.G;
+  asm volatile("" : "+v"(again), "+s"(group));
+  const Query of = query_of(again, group);  // anew: there are no registers to keep it in
+  if (!of.live) return;
+  float whole = l == 0.f ? 0.f : 1.f / l;
+  if (__any((x < -80) | (x > 80))) {  // by two factors, each in float32's range
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) o[dt] *= ldexpf(1.f, -x / 2);
+    whole = ldexpf(whole, -x - -x / 2);
+  } else {
+    whole = ldexpf(whole, -x);
+  }
+  const int64_t at = (((int64_t)part * a.c.B + of.b) * a.T + of.tok) * a.H + of.head;
   if (g == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt)
@@ -331,7 +409,8 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 }
 
 // out = the mean of what a row has of its own and of its prefix's parts, each
-// with its weight.  D / 4 threads take every PG-th part of a token's head, four
+// with its weight; on the way too x is a mean, so that no sum of it passes
+// float32's range.  D / 4 threads take every PG-th part of a token's head, four
 // parts' loads at once, and the PG groups join in their order.  PG = 8 beside
 // many parts (8 rows of one token, 64 parts: 5.7 us, 18 with PG = 1), 1 beside
 // up to 8 (64 x 6 tokens, 5 parts: 9.6 us, 25 with PG = 8).
@@ -377,16 +456,20 @@ __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
     float to = top;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) to = fmaxf(to, ml[k].x);  // a part read twice is no other maximum
-    const float f = top == NEG_INF ? 0.f : exp2_fast(top - to);
-    sum *= f;
-    x *= f;
+    const float f = top == NEG_INF ? 0.f : sum * exp2_fast(top - to);
+    float w[AHEAD];
+    sum = f;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) {
-      if (s0 + k * PG >= parts || (ml[k].x == NEG_INF && ml[k].y == ml[k].y)) continue;
-      const float w = ml[k].y * exp2_fast(ml[k].x - to);
-      sum += w;
-      x += y[k] * w;
+      const bool nothing = s0 + k * PG >= parts || (ml[k].x == NEG_INF && ml[k].y == ml[k].y);
+      w[k] = nothing ? 0.f : ml[k].y * exp2_fast(ml[k].x - to);
+      sum += w[k];
     }
+    const float whole = sum == 0.f ? 0.f : 1.f / sum;
+    x *= f * whole;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (w[k] != 0.f) x += y[k] * (w[k] * whole);
     top = to;
   }
   if constexpr (PG > 1) {
@@ -397,19 +480,21 @@ __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
     const int first = threadIdx.x / L;
 #pragma unroll
     for (int k = 1; k < PG; ++k) top = fmaxf(top, sml[first + k].x);
+    float w[PG];
     sum = 0.f;
-    x = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < PG; ++k) {
       const float2 ml = sml[first + k];
-      if (ml.x == NEG_INF && ml.y == 0.f) continue;
-      const float f = exp2_fast(ml.x - top);
-      sum = fmaf(ml.y, f, sum);
-      x += sx[threadIdx.x + k * L] * f;
+      w[k] = ml.x == NEG_INF && ml.y == 0.f ? 0.f : ml.y * exp2_fast(ml.x - top);
+      sum += w[k];
     }
+    const float whole = sum == 0.f ? 0.f : 1.f / sum;
+    x = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < PG; ++k)
+      if (w[k] != 0.f) x += sx[threadIdx.x + k * L] * (w[k] * whole);
   }
   if (!live) return;
-  if (parts) x *= 1.f / sum;
   if (none && !(sum > 0.f)) x = kept;
   union { bf16x2 p[2]; uint2 u; } y;
   y.p[0] = __builtin_convertvector(f32x2{x[0], x[1]}, bf16x2);
