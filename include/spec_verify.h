@@ -867,7 +867,9 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int64_t stride,
  * spec_verify_truncate - the logits of tokens that spec_verify_sample's rules
  * leave out become -inf, the others keep their bits: spec_verify on target (or
  * draft) logits cut so verifies against the distribution that
- * spec_verify_sample draws from.  Greedy rows, and rows that no rule cuts, are
+ * spec_verify_sample draws from.  NaN counts as -inf, and becomes it, in every
+ * row that a rule applies to.  Greedy rows, and rows whose rules are all off
+ * (top_k 0 or less or V or more, top_p 1 or more, min_p 0 or less, or NaN), are
  * not changed.
  *
  * out          element (b, i, x) at b * out_row_stride + i * out_stride + x.  It

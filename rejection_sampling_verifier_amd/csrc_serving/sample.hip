@@ -65,7 +65,7 @@ struct SampleArgs {
   Chunk* chunks;      // [rows][C]
   double* subs;       // [rows][C][4 NV] sums of a wave's vectors, rows without a cut; of spec_verify_sample
   uint64_t* lists;    // [rows][C][cap] order << 32 | id
-  uint2* bounds;      // [rows] of spec_verify_truncate
+  uint2* bounds;      // [rows] of spec_verify_truncate; 0 for a row without a rule
   unsigned* arrived;  // [rows] work-groups that have put out their counts
   uint64_t* masses;   // [rows][BINS] of all of them
   uint32_t* counts;   // [rows][1 + share][BINS] of all of them, and of each
@@ -878,7 +878,7 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(3))) void sa
       tokens[t] = id;
       if (logprobs) logprobs[t] = id < 0 ? NEG_INF : 0.f;
     }
-    if (a.bounds && t == 0) a.bounds[row] = make_uint2(0, INT_MAX);
+    if (a.bounds && t == 0) a.bounds[row] = make_uint2(r.greedy || !r.cut() ? 0 : Bits<ET>::LEAST, INT_MAX);
     return;
   }
   const double c = rate(r.T);
@@ -1018,7 +1018,9 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(3))) void sa
     }
   }
   if (a.bounds) {
-    if (t == 0) a.bounds[row] = make_uint2(work.kt, (uint32_t)work.idlim);
+    // -inf, and NaN as it, is left out by any rule, also by one that leaves all else.
+    const bool all = work.kt < Bits<ET>::LEAST;
+    if (t == 0) a.bounds[row] = all ? make_uint2(Bits<ET>::LEAST, INT_MAX) : make_uint2(work.kt, (uint32_t)work.idlim);
     return;
   }
   if (logit_of<ET>(work.kt) > work.low) work.low = logit_of<ET>(work.kt);
