@@ -853,7 +853,8 @@ int spec_verify_append(const void* k, const void* v, int64_t kv_row,
  * logprobs     [B, P, n] float32 or NULL: ln of each token's part of the kept
  *              mass, 0 for greedy rows.
  * workspace, workspace_bytes  as spec_verify, but it need not be zero-filled.
- * B, P >= 1; V in [1, 2^20]; n in [1, SV_MAX_NODES].  Two kernels.
+ * B, P >= 1; V in [1, 2^20]; n in [1, SV_MAX_NODES]; fewer than 2^24 parts of
+ * 16,384 logits (8192 of float32) in all rows.  Two kernels.
  */
 int spec_verify_sample(const void* logits, int64_t row_stride, int64_t stride,
                        const float* uniforms, const float* temperature,
@@ -875,7 +876,8 @@ int spec_verify_sample(const void* logits, int64_t row_stride, int64_t stride,
  * out          element (b, i, x) at b * out_row_stride + i * out_stride + x.  It
  *              may be the logits themselves with the same strides; otherwise it
  *              must not overlap them.
- * Other arguments as spec_verify_sample.  Two or three kernels.
+ * Other arguments as spec_verify_sample; fewer than 2^24 parts of 8192 logits
+ * (4096 of float32) in all rows.  Two or three kernels.
  */
 int spec_verify_truncate(const void* logits, int64_t row_stride,
                          int64_t stride, const float* temperature,

@@ -1134,6 +1134,9 @@ struct Plan {
 };
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Work-groups of a row in truncate_kernel, which takes half a chunk.
+int cut_groups(int nv, int V, int vec) { return (V + vec - 1 + WG * (nv / 2) * vec - 1) / (WG * (nv / 2) * vec); }
+
 // Chunks of 8 vectors per thread, or of 2 for few rows, whose chunks would be
 // too few: six rows of 128,256 cut by top-p 33 us against 106, both kernels, as
 // four times as many work-groups count a row; but 16 rows of 151,936 with top-k
@@ -1146,7 +1149,7 @@ int make_plan(int B, int P, int V, int dtype, bool cuts, bool truncate, Plan& pl
   pl.fill = truncate && rows * chunks(8) >= 1024;
   pl.C = chunks(pl.nv);
   pl.cap = cuts ? (pl.nv == 8 ? 1024 : 512) : 0;
-  if (rows * pl.C > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
+  if (rows * (truncate ? cut_groups(pl.nv, V, vec) : pl.C) > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
   // Work-groups of a row for the case that it has many candidates: two to a CU.
   pl.share = cuts ? (int)std::max<int64_t>(1, std::min<int64_t>(pl.C, 512 / rows)) : 1;
   const size_t n = (size_t)rows * pl.C;
@@ -1170,9 +1173,8 @@ int launch(const SampleArgs& a, bool inplace, hipStream_t st) {
   hipLaunchKernelGGL((sample_row_kernel<ET, NV>), dim3((uint32_t)rows * a.share), dim3(WG), 0, st, a);
   if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   if (a.bounds) {
-    constexpr int VEC = Tr<ET>::VEC, N = NV == 2 ? 1 : 4;
-    const int per = (a.V + VEC - 1 + WG * N * VEC - 1) / (WG * N * VEC);
-    hipLaunchKernelGGL((truncate_kernel<ET, N>), dim3((uint32_t)rows * per), dim3(WG), 0, st, a, per, (int)inplace);
+    const int per = cut_groups(NV, a.V, Tr<ET>::VEC);
+    hipLaunchKernelGGL((truncate_kernel<ET, NV / 2>), dim3((uint32_t)rows * per), dim3(WG), 0, st, a, per, (int)inplace);
     if (hipGetLastError() != hipSuccess) return SV_ERR_HIP;
   }
   return SV_OK;
