@@ -637,7 +637,7 @@ typedef struct {
  * prefix       NULL: spec_verify_attention.
  * Other arguments as spec_verify_attention, but the workspace's size also
  * depends on prefix->count and max_blocks, and a workspace is of one shape of
- * these too.  (B T H / Hkv / 128 + count) Hkv < 2^23.
+ * these too.  (B T H / Hkv / 128 + count) Hkv < 2^23, B T H D < 2^34.
  * Three kernels, four with weights.
  */
 int spec_verify_attention_prefix(

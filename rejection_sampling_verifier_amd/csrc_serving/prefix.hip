@@ -503,11 +503,15 @@ __global__ __launch_bounds__(WG) void prefix_join_kernel(PrefixArgs a) {
   if (d == 0 && parts) a.lse[at] = top + __builtin_amdgcn_logf(sum);
 }
 
+constexpr int join_threads(int splits) { return splits <= 8 ? 1 : 8; }  // PG
+int64_t join_groups(const sv_cache& c, int T, int H, int splits) {
+  const int rows = WG / (c.D / 4 * join_threads(splits));
+  return ((int64_t)c.B * T * H + rows - 1) / rows;
+}
 template <int D, int PG>
 int join(const PrefixArgs& a, hipStream_t st) {
-  constexpr int ROWS = WG / (D / 4 * PG);
-  const int64_t rows = (int64_t)a.c.B * a.T * a.H;
-  hipLaunchKernelGGL((prefix_join_kernel<D, PG>), dim3((uint32_t)((rows + ROWS - 1) / ROWS)), dim3(WG), 0, st, a);
+  const int64_t groups = join_groups(a.c, a.T, a.H, a.splits);
+  hipLaunchKernelGGL((prefix_join_kernel<D, PG>), dim3((uint32_t)groups), dim3(WG), 0, st, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 
@@ -538,7 +542,7 @@ int prefix_plan(const sv_cache& c, const sv_prefix& p, int T, int H, PrefixPlan&
   const int64_t tiles = ((int64_t)p.max_blocks * c.page + KEYS - 1) / KEYS;
   pl.splits = (int)std::max<int64_t>(1, std::min(256 * RESIDENT / (full * c.Hkv), (tiles + 1) / 2));
   const int64_t grid = qtiles * c.Hkv * pl.splits;
-  if (grid > (1 << 23)) return SV_ERR_UNSUPPORTED;
+  if (grid > (1 << 23) || join_groups(c, T, H, pl.splits) > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
   pl.qtiles = (int)qtiles;
   const size_t rows = (size_t)c.B * T * H, al = 255;
   pl.o = 0;
@@ -556,7 +560,7 @@ int prefix_launch(const PrefixArgs& a, hipStream_t st) {
 }
 
 int prefix_join(const PrefixArgs& a, hipStream_t st) {
-  const bool few = a.splits <= 8;
+  const bool few = join_threads(a.splits) == 1;
   return a.c.D == 64 ? (few ? join<64, 1>(a, st) : join<64, 8>(a, st)) : (few ? join<128, 1>(a, st) : join<128, 8>(a, st));
 }
 

@@ -7,8 +7,9 @@ from __future__ import annotations
 import pytest
 
 from rejection_sampling_verifier_amd import binding as B
+from tests.test_prefix_abi import attention, prefix
 from tests.test_sample_abi import call
-from tests.test_serving_abi import P
+from tests.test_serving_abi import P, cache
 
 
 @pytest.mark.parametrize("dtype, part", [(B.SV_BF16, 8192), (B.SV_F32, 4096)])
@@ -23,3 +24,14 @@ def test_truncate_counts_the_work_groups_of_its_last_kernel(dtype, part):
     assert call("truncate", B=rows, **dict(one, out=P[0])) == B.SV_ERR_UNSUPPORTED   # in place
     rc, n = call("sample", ws=None, B=rows, **{k: one[k] for k in ("P", "V", "row", "stride", "dtype")})
     assert rc == B.SV_OK and n > 0
+
+
+@pytest.mark.parametrize("D, H", [(64, 64), (128, 32)])
+def test_prefix_counts_the_work_groups_of_its_join(D, H):
+    """D / 4 work-items to a token's head: B T H D below 2^34."""
+    def rc(B_, H_):
+        heads = dict(T=64, H=H_, q_row=64 * H_ * D, q_tok=H_ * D, kv_row=64 * H_ * D, kv_tok=H_ * D)
+        return attention(ws=None, c=cache(B=B_, Hkv=H_, D=D, max_blocks=1), prefix=prefix(count=1, max_blocks=1), **heads)
+    assert rc(65536, H)[0] == B.SV_ERR_UNSUPPORTED
+    code, n = rc(65535, H)
+    assert code == B.SV_OK and n > 0
