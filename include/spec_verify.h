@@ -774,8 +774,9 @@ typedef struct {
  * parents      [B, T] int32 or NULL, as in spec_verify_attention.
  * query_lens   [B] int32 or NULL: row b has only that many (0 .. T) tokens;
  *              what lies behind them is not read and not written.
- * B, T, H, Hkv >= 1, T at most SV_MAX_NODES with parents; D a multiple of 16,
- * at most 512.  One kernel, no workspace.
+ * B, T, H, Hkv >= 1, H and Hkv at most 65536, T at most SV_MAX_NODES with
+ * parents, fewer than 2^24 fours of tokens in all rows; D a multiple of 16, at
+ * most 512.  One kernel, no workspace.
  */
 int spec_verify_rotate(const void* q, int64_t q_row, int64_t q_tok,
                        const void* k, int64_t k_row, int64_t k_tok,

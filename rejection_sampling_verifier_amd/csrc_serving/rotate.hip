@@ -105,10 +105,10 @@ __global__ __launch_bounds__(WG) void rotate_kernel(RotateArgs a, int groups) {
 
 template <int TT>
 int launch(const RotateArgs& a, hipStream_t st) {
-  const int groups = (a.T + TT - 1) / TT;
-  if ((int64_t)a.B * groups > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
+  const int64_t groups = ((int64_t)a.T + TT - 1) / TT;
+  if (a.B * groups > MAX_ITEMS / WG) return SV_ERR_UNSUPPORTED;
   (void)hipGetLastError();
-  hipLaunchKernelGGL(rotate_kernel<TT>, dim3((uint32_t)((int64_t)a.B * groups)), dim3(WG), 0, st, a, groups);
+  hipLaunchKernelGGL(rotate_kernel<TT>, dim3((uint32_t)(a.B * groups)), dim3(WG), 0, st, a, (int)groups);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_HIP;
 }
 

@@ -4,6 +4,8 @@ tokens take.  Every call here is a size query or is refused."""
 
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 
 from rejection_sampling_verifier_amd import binding as B
@@ -35,3 +37,12 @@ def test_prefix_counts_the_work_groups_of_its_join(D, H):
     assert rc(65536, H)[0] == B.SV_ERR_UNSUPPORTED
     code, n = rc(65535, H)
     assert code == B.SV_OK and n > 0
+
+
+@pytest.mark.parametrize("T", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 26])
+def test_rotate_counts_tokens_past_32_bits(T):
+    rot = B.SvRotary(P[9], None, None, 0, 16, 0)
+    n = 1 << 10
+    rc = B.load_library().spec_verify_rotate(P[0] << 16, 0, n, P[1] << 16, 0, n, ctypes.byref(rot), P[5], None, None, 1, T, 1, 1,
+                                             16, P[2] << 16, 0, n, P[3] << 16, 0, n, None)
+    assert rc == B.SV_ERR_UNSUPPORTED
