@@ -636,8 +636,9 @@ typedef struct {
  * weights[b][t][j] are those of the row's own blocks.
  * prefix       NULL: spec_verify_attention.
  * Other arguments as spec_verify_attention, but the workspace's size also
- * depends on prefix->count and max_blocks, and a workspace is of one shape of
- * these too.  (B T H / Hkv / 128 + count) Hkv < 2^23, B T H D < 2^34.
+ * depends on prefix->max_blocks (for SV_MAX_BLOCKS it is the largest): one that
+ * is large enough serves every prefix of a shape, and calls without one.
+ * (B T H / Hkv / 128 + count) Hkv < 2^23, B T H D < 2^34.
  * Three kernels, four with weights.
  */
 int spec_verify_attention_prefix(

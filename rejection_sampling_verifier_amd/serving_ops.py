@@ -13,8 +13,8 @@ import operator
 
 import torch
 
-from .binding import (SV_BF16, SV_E4M3, SV_INT8, SV_MAX_K, SvCache, SvControls, SvPrefix, SvRotary, _cached_workspace,
-                      _check, _dtype_code, _OnStream, _stream_handle, load_library)
+from .binding import (SV_BF16, SV_E4M3, SV_INT8, SV_MAX_BLOCKS, SV_MAX_K, SvCache, SvControls, SvPrefix, SvRotary,
+                      _cached_workspace, _check, _dtype_code, _OnStream, _stream_handle, load_library)
 
 _KINDS = {"e4m3": SV_E4M3, "int8": SV_INT8}
 
@@ -284,7 +284,8 @@ def _attention_bytes(cache, T, H, tree, weights, prefix=None):
 
 def attention_workspace_bytes(cache, T, H, *, tree=False, weights=False, prefix=None):
     """Bytes of workspace that cache_attention needs for T new tokens and H
-    heads; prefix: the shape of prefix_table, if any."""
+    heads; prefix: the shape of prefix_table, if any (that of (1, 65536)
+    serves every table)."""
     return _attention_bytes(cache, T, H, tree, weights, None if prefix is None else tuple(prefix))
 
 
@@ -345,7 +346,8 @@ def cache_attention(q, k_new, v_new, cache, positions, blocks, *, parents=None, 
     _maybe("parents", parents, (B, T), torch.int32, dev)
     _maybe("query_lens", query_lens, (B,), torch.int32, dev)
     prefix = _prefix(prefix_table, prefix_blocks, prefix_starts, dev)
-    shared = None if prefix is None else (prefix.count, prefix.max_blocks)
+    # the size that serves every prefix: a table that grows must not mean another workspace
+    shared = None if prefix is None else (1, SV_MAX_BLOCKS)
     handle, scope = _scope(dev, stream)
     need = _attention_bytes(cache, T, H, parents is not None, weights is not None and weights is not False, shared)
     with scope:
