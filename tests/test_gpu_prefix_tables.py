@@ -10,7 +10,7 @@ import rejection_sampling_verifier_amd as rsv
 from rejection_sampling_verifier_amd import binding
 from tests import cache_ref as R
 from tests.test_gpu_attention import make_qkv, views
-from tests.test_gpu_prefix import shared_state
+from tests.test_gpu_prefix import check, shared_state
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,39 @@ def test_tables_of_any_width_share_a_workspace():
         assert torch.equal(out, fresh[s][0]) and torch.equal(w, fresh[s][1]), s
         out, w = rsv.cache_attention(*views(qkv, 8, 2), cache, positions, blocks, weights=True, workspace=ws)
         assert torch.equal(out, plain[0]) and torch.equal(w, plain[1])
+
+
+RANGES = {  # starts -> the prefix of each of five rows, -1: none
+    (0, 2, 5): [0, 0, 1, 1, 1], (5, -3, 9): [1] * 5, (3, 1, 2): [-1, 1, -1, -1, -1], (-2 ** 31, 2 ** 31 - 1, 0): [0] * 5,
+    (2, 2, 4): [-1, -1, 1, 1, -1], (9, 9, 9): [-1] * 5, (3, 4, 1): [-1, -1, -1, 0, -1], (-7, -7, 2): [1, 1, -1, -1, -1]}
+
+
+@pytest.mark.parametrize("lengths", [(9, 5), (-1, 10 ** 9), (-2 ** 31, 2 ** 31 - 1), (0, 3)])
+@pytest.mark.parametrize("starts", RANGES, ids=str)
+def test_ranges_and_lengths_of_any_kind(starts, lengths):
+    """What lies in no range goes without a prefix, lengths count as what the table holds, and nothing is written
+    beside the outputs and the workspace."""
+    rows, prefix, _, _ = shared_state(33, [20, 300, 0, 45, 7], [9, 5], [0, 2, 5], Hkv=2, D=64, page=16, kind="e4m3")
+    cache, positions, blocks = R.to_gpu(rows)
+    qkv = make_qkv(34, 5, 3, 8, 2, 64)
+    table, width = prefix["prefix_table"], prefix["prefix_table"].shape[1]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    n = rsv.attention_workspace_bytes(cache, 3, 8, weights=True, prefix=(2, width))
+    around = torch.full((n + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    around[256:256 + n] = 0
+    outs = torch.full((7, 3, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    masses = torch.full((7, 3, cache.max_blocks), 7.0, device="cuda")
+    rsv.cache_attention(*views(qkv.cuda(), 8, 2), cache, positions, blocks, prefix_table=table.cuda(),
+                        prefix_blocks=i32(lengths), prefix_starts=i32(starts), out=outs[1:6], weights=masses[1:6],
+                        workspace=around[256:256 + n])
+    assert (around[:256] == 0xA5).all() and (around[256 + n:] == 0xA5).all()
+    for t in (outs, masses):
+        assert (t[0] == 7).all() and (t[6] == 7).all()
+    # the rows as if their prefixes' pages stood in their own tables
+    before = [0 if i < 0 else min(max(lengths[i], 0), width) for i in RANGES[starts]]
+    own = rows["table"].shape[1]
+    whole = dict(rows, table=torch.full((5, width + own), -1, dtype=torch.int32), blocks=rows["blocks"] + torch.tensor(before))
+    for b, i in enumerate(RANGES[starts]):
+        whole["table"][b, :before[b]] = table[i, :before[b]]
+        whole["table"][b, before[b]:before[b] + own] = rows["table"][b]
+    check(whole, before, own, *views(qkv, 8, 2), outs[1:6], masses[1:6])
