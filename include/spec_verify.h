@@ -736,8 +736,8 @@ int spec_verify_evict(const float* totals, const int32_t* block_table,
  * / 2, or 2 i and 2 i + 1 where interleaved is 1.  Pair i (a, b) of a token at
  * position p becomes
  *   (a cos x - b sin x, b cos x + a sin x),  x = p freqs[i]
- * with x, its cosine and its sine in 64 bits, the last two rounded to float32,
- * the products and sums in float32 and the result rounded to bf16.  The other
+ * with x (up to 2^52 in magnitude), its cosine and its sine in 64 bits, the
+ * last two rounded to float32, the products and sums in float32 and the result rounded to bf16.  The other
  * channels stay as they are.
  *
  * freqs        [dims / 2] float32 device.  dims a multiple of 16, at most D.
@@ -838,9 +838,16 @@ int spec_verify_append(const void* k, const void* v, int64_t kv_row,
  *           NaN: all)
  * Draw j is the smallest kept id x for which the mass of the kept ids up to x
  * exceeds uniforms[b][i][j] times the mass of all kept: spec_verify's draw,
- * and with top_k alone spec_verify's truncated draft.  Weights are formed in
- * float64, and are 0 under 2^-1000, for which no draw is; where rules cut a row masses are whole multiples of 2^-43, so a
- * result does not depend on any order of summation.
+ * and with top_k alone spec_verify's truncated draft.
+ * Weights are formed in float64, to 2^-39 of each, and are 0 under 2^-1000, so
+ * that such a token is not drawn.  Where rules cut a row the weights added up
+ * are whole multiples of 2^-43.  A cut by mass or a draw is that of exact
+ * weights unless a border lies within 2^-37 of the row's mass or, where rules
+ * cut the row, 2^-43 times the number of tokens added up.  Sums of whole
+ * multiples do not depend on their order.  A sum over a whole row, by which
+ * rows without rules are drawn from and top_p goes without a top_k, is float64's
+ * over parts of the row, which depend on B P and the row's alignment: so near a
+ * border its result may change with the batch.
  * Rows with T <= 0 (or NaN) take the largest logit's lowest id.  A NaN logit
  * counts as -inf and -inf is never drawn; where there is nothing else the
  * token is -1 and its logprob -inf.

@@ -8,8 +8,13 @@
 // that logit, an id.  The bound is found by counting (top-k) or adding up
 // (top-p) over bins of the logits' order, not by sorting.  Weights are formed
 // in float64 and added as whole numbers of 2^-43: such sums do not depend on
-// their order, so atomics may form them, and a token is the one that 64 bits
-// give unless a border lies within about 2^-36 of the draw.
+// their order, so atomics may form them.  A cut or a draw is the one of exact
+// weights unless a border lies nearer than what their errors add up to: 2^-39
+// of each weight from the series (twice where a chunk's sum is brought to the
+// row's maximum), 2^-44 of the largest for each token added up, and that in the
+// part of the mass and in the whole.  The sum of a whole row, which draws
+// without a cut and top-p without top-k go by, is float64's by chunks: so near
+// a border a result may depend on how many chunks there are.
 //
 // HBM reads bound it.  sample_stats_kernel reads each logit once: per chunk of
 // a row the maximum and, where a rule or a draw needs it, the sum.  Where
