@@ -7,9 +7,10 @@
 // heads, a head at a time: its values wait in registers, rotated, for their
 // largest magnitude, while the values of the head's other half are on their
 // way.  A thread has the same pairs of the same tokens in every head, so it
-// forms their cosines and sines once and keeps them (in LDS, 32 KB of it, they
-// leave room for three work-groups to a CU: 142 us for 16 prompts of up to 4096
-// tokens).  V's codes are turned in LDS in words of four tokens, which one lane
+// forms their cosines and sines once and keeps them: 124 registers, four
+// work-groups to a CU, at pages of 64 tokens and D = 128 (16 prompts of up to
+// 4096 tokens 109 us; in LDS, 32 KB of it, they leave room for three: 142), 210
+// and two at pages of 128 (175 us), 427 and one at 256 (248 us).  V's codes are turned in LDS in words of four tokens, which one lane
 // has read.  The tokens after the last full block go to the tail by the
 // work-group of the row's first block, which is also the one that reads the
 // tail's old tokens, so that a ring of a single block will do.

@@ -359,8 +359,9 @@ __global__ __launch_bounds__(WG) __attribute__((amdgpu_waves_per_eu(RESIDENT, RE
 #pragma unroll
           for (int j = 0; j < 4; ++j) z.h[j] = __builtin_convertvector(f32x2{y[8 * u + 2 * j], y[8 * u + 2 * j + 1]}, f16x2);
           p[u] = z.v;
-          // What f16 lost, in bf16, which has float32's range.  Scores whose 64 keys span e^19 and more come here: 64 x 6
-          // tokens over 8192 keys take 130 us a call with scores of a standard deviation of 1, 165 with 4.
+          // What f16 lost, in bf16, which has float32's range.  Tiles whose scores span e^13 to e^21 and more come here,
+          // by where they lie in f16's: 64 x 6 tokens over 8192 keys take 79 us with scores of a standard deviation of
+          // 1, 35 more with 4.
           if (lost) {
             union { bf16x2 h[4]; bf16x8 v; } r;
 #pragma unroll

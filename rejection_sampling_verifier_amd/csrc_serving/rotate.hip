@@ -154,7 +154,8 @@ extern "C" int spec_verify_rotate(const void* q, int64_t q_row, int64_t q_tok, c
   RotateArgs a = {static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<uint16_t*>(q_out),
                   static_cast<uint16_t*>(k_out), q_row, q_tok, k_row, k_tok, qo_row, qo_tok, ko_row, ko_tok, *rotary,
                   positions, parents, query_lens, B, T, H, Hkv, D};
-  // 384 tokens of 40 heads: 5.8 us one to a work-group, 7.4 four; 4096: 19.1 and 16.0.
+  // 384 tokens of 40 heads: 5.6 us one to a work-group, 7.4 four; 2048: 12.5 and 10.6; 4096: 19.6 and 15.6.  Of 16
+  // heads 4.8 and 4.9, 9.2 and 7.0, 13.8 and 9.9; of 136 9.2 and 15.7, 23.7 and 26.2, 44.6 and 46.2.
   const int64_t tokens = (int64_t)B * T;
   return tokens <= 2048 ? launch<1>(a, stream) : launch<4>(a, stream);
 }
