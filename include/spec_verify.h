@@ -518,7 +518,8 @@ typedef enum { SV_E4M3 = 0, SV_INT8 = 1 } sv_kind;
  * with a scale for each block and kv head; the tokens after the last full
  * block (the tail) are held in bf16, so nothing is ever quantised twice and a
  * rejected draft leaves no trace.  All pointers are device pointers; the
- * pages, tails and scales are written by spec_verify_commit only.
+ * pages, tails and scales are written by spec_verify_commit and
+ * spec_verify_append only.
  *
  * k_pages      [num_pages, Hkv, page, D] codes
  * v_pages      [num_pages, Hkv, D, page] codes: a channel's tokens side by
