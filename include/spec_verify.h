@@ -812,8 +812,9 @@ int spec_verify_rotate(const void* q, int64_t q_row, int64_t q_tok,
  *              Rows that are left as they were, and what lies behind lens[b],
  *              are not written.
  * positions_out, blocks_out [B] int32; both may be the inputs themselves (then
- *              a second kernel updates them).  Beyond that no output may
- *              overlap an input or another output.
+ *              a second kernel updates them).  Beyond that no output, the cache's
+ *              pages, scales and tails among them, may overlap an input or
+ *              another output.
  * T in [1, 2^24]; B (page - 1 + T) / page Hkv < 2^24.
  */
 int spec_verify_append(const void* k, const void* v, int64_t kv_row,

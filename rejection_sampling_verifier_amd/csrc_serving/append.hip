@@ -315,13 +315,19 @@ extern "C" int spec_verify_append(const void* k, const void* v, int64_t kv_row, 
     if (s < 0 || s > FAR || s % 8) return SV_ERR_ARG;
   const int64_t width = (int64_t)c.Hkv * c.D * 2;
   const View in[] = {{k, kv_row * 2, kv_tok * 2, width}, {v, kv_row * 2, kv_tok * 2, width}};
-  // Work-groups write the cache and the counters while others still read the prompt.
-  const Array written[] = {{c.k_pages, pages * c.page * c.D}, {c.v_pages, pages * c.page * c.D}, {c.k_scale, pages * 4},
-                           {c.v_scale, pages * 4}, {c.k_tail, tail}, {c.v_tail, tail}, {positions_out, nb},
-                           {blocks_out, nb}};
-  for (const View& i : in)
-    for (const Array& o : written)
+  // Work-groups write the cache and the counters while others still read the prompt and the lists.
+  const Array written[] = {{positions_out, nb}, {blocks_out, nb}, {c.k_pages, pages * c.page * c.D},
+                           {c.v_pages, pages * c.page * c.D}, {c.k_scale, pages * 4}, {c.v_scale, pages * 4},
+                           {c.k_tail, tail}, {c.v_tail, tail}};
+  for (const Array& o : written) {
+    for (const View& i : in)
       if (overlap({i.p, (size_t)((c.B - 1) * i.row + (T - 1) * i.tok + i.width)}, o)) return SV_ERR_ARG;
+    if (&o < written + 2) continue;  // the counters: above
+    for (const Array& i : lists)
+      if (overlap(i, o)) return SV_ERR_ARG;
+    for (const Output& i : counters)
+      if (overlap(i.a, o)) return SV_ERR_ARG;
+  }
   if (k_out) {
     const View out = {k_out, ko_row * 2, ko_tok * 2, width};
     const Array whole = {k_out, (size_t)((c.B - 1) * out.row + (T - 1) * out.tok + out.width)};
